@@ -30,3 +30,11 @@ from ._binding import (  # noqa: F401
     fp8_status_string,
     lib,
 )
+from ._attention import (  # noqa: F401,E402
+    fp8_attention_decode,
+    fp8_attention_decode_workspace_size,
+    fp8_attention_prompt,
+    fp8_kv_slots,
+    fp8_qk_norm_rope,
+    fp8_rope_turns,
+)

@@ -105,6 +105,24 @@ def lib() -> ctypes.CDLL:
         L.fp8_status_string.argtypes = [_st]
         L.fp8_device_status.restype = _st
         L.fp8_device_status.argtypes = [ctypes.c_int]
+        _sz = ctypes.c_size_t
+        L.fp8_kv_slots.restype = _st
+        L.fp8_kv_slots.argtypes = [_vp, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp,
+                                   _vp, _vp, _vp, _vp, _vp]
+        L.fp8_qk_norm_rope.restype = _st
+        L.fp8_qk_norm_rope.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64,
+                                       _vp, _vp, ctypes.c_float, _vp, _vp, _i64, ctypes.c_int,
+                                       _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64,
+                                       _vp]
+        L.fp8_attention_prompt.restype = _st
+        L.fp8_attention_prompt.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64,
+                                           _i64, _vp, _i64, ctypes.c_float, _vp, _i64, _vp]
+        L.fp8_attention_decode.restype = _st
+        L.fp8_attention_decode.argtypes = [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64,
+                                           _vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64,
+                                           ctypes.c_float, _vp, _i64, _vp, _sz, _vp]
+        L.fp8_attention_decode_workspace_size.restype = _sz
+        L.fp8_attention_decode_workspace_size.argtypes = [_i64] * 7
         L.fp8_selftest_wait_timeout.restype = _st
         L.fp8_selftest_wait_timeout.argtypes = [_i64, _vp, _vp]
         _lib = L

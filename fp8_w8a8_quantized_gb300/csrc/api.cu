@@ -181,6 +181,16 @@ fp8_status_t linear_checks(const void* x, const uint8_t* wq, const float* s_w, c
     return current_device(&d);
 }
 
+fp8_status_t device_info(int* num_sms, unsigned** status) {
+    DeviceState* d = nullptr;
+    const fp8_status_t st = current_device(&d);
+    if (st == FP8_OK) {
+        *num_sms = d->num_sms;
+        *status = d->status;
+    }
+    return st;
+}
+
 bool encode_tmap_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                     uint64_t ld_bytes, uint32_t box_cols, uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();

@@ -1,0 +1,196 @@
+// Block tables, slot maps and positions of a serving step, built on the GPU
+// from the requests' lengths.  With page size p, request b holds c_b cached
+// tokens and brings n_b new ones:
+//
+//   have_b  = ceil(c_b / p),  need_b = ceil((c_b + n_b) / p)
+//   first_b = sum_{a < b} (need_a - have_a),  cu_b = sum_{a < b} n_a
+//   table[b, have_b + i] = free[first_b + i]              (i < need_b - have_b)
+//   pos[cu_b + i] = c_b + i,  slot[cu_b + i] = table[b, pos / p] p + pos mod p
+//
+// There is next to nothing to compute: the call is bound by its launch and by
+// two dependent global reads (the lengths, then the page of a token).  So it
+// is ONE launch without a pass between the sums and their use: every CTA scans
+// all the lengths itself (kChunk at a time, 8 bytes a request out of L2) and
+// then writes its own range of tokens and its share of the table rows.  A
+// token on a page that this very call takes looks the page up in `free`, not
+// in the table, so no CTA reads what another one writes.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace fp8k {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 8;                   // requests per thread and chunk
+constexpr int kChunk = kThreads * kPer;   // requests scanned at a time
+
+struct Sums {
+    int64_t tokens, pages;
+};
+
+// Inclusive block scan of one Sums per thread; `total` gets the block's sum.
+__device__ __forceinline__ Sums scan_block(Sums v, Sums* warp_sums, Sums& total) {
+    const int lane = lane_id(), warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xFFFFFFFFu, v.tokens, o);
+        const int64_t p = __shfl_up_sync(0xFFFFFFFFu, v.pages, o);
+        if (lane >= o) {
+            v.tokens += t;
+            v.pages += p;
+        }
+    }
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    total = Sums{0, 0};
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) {
+            v.tokens += total.tokens;
+            v.pages += total.pages;
+        }
+        total.tokens += warp_sums[w].tokens;
+        total.pages += warp_sums[w].pages;
+    }
+    return v;
+}
+
+__device__ __forceinline__ int64_t pages_of(int64_t tokens, int64_t page, int64_t width) {
+    const int64_t n = (tokens + page - 1) / page;
+    return n < width ? n : width;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    kv_slots(const int32_t* __restrict__ ctx, const int32_t* __restrict__ fresh, int64_t B,
+             const int32_t* __restrict__ free_pages, int64_t n_free, int64_t page,
+             int32_t* __restrict__ table, int64_t width, int64_t ld_table, int64_t T,
+             int64_t per_cta, int64_t* __restrict__ slot, int32_t* __restrict__ pos,
+             int32_t* __restrict__ cu, int32_t* __restrict__ lens, int32_t* __restrict__ used) {
+    __shared__ int64_t s_cu[kChunk + 1];     // first token of each request of the chunk
+    __shared__ int64_t s_first[kChunk + 1];  // first page taken from `free`
+    __shared__ int32_t s_ctx[kChunk];
+    __shared__ Sums warp_sums[kThreads / 32];
+    pdl_launch_dependents();
+    pdl_wait_primary();
+
+    const int64_t t_lo = blockIdx.x * per_cta;
+    const int64_t t_hi = t_lo + per_cta < T ? t_lo + per_cta : T;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    const int64_t my_warp = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    Sums carry{0, 0};
+    for (int64_t b0 = 0; b0 < B; b0 += kChunk) {
+        const int n = static_cast<int>(B - b0 < kChunk ? B - b0 : kChunk);
+        int32_t c[kPer], f[kPer];
+        Sums mine{0, 0};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int r = threadIdx.x * kPer + i;
+            c[i] = r < n ? max(ctx[b0 + r], 0) : 0;
+            f[i] = r < n ? max(fresh[b0 + r], 0) : 0;
+            mine.tokens += f[i];
+            mine.pages += pages_of(static_cast<int64_t>(c[i]) + f[i], page, width) -
+                          pages_of(c[i], page, width);
+        }
+        Sums total;
+        const Sums upto = scan_block(mine, warp_sums, total);
+        int64_t t = carry.tokens + upto.tokens - mine.tokens;
+        int64_t p = carry.pages + upto.pages - mine.pages;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int r = threadIdx.x * kPer + i;
+            if (r < n) {
+                s_cu[r] = t;
+                s_first[r] = p;
+                s_ctx[r] = c[i];
+                if (blockIdx.x == 0) {
+                    cu[b0 + r] = static_cast<int32_t>(t < T ? t : T);
+                    const int64_t len = static_cast<int64_t>(c[i]) + f[i];
+                    lens[b0 + r] = static_cast<int32_t>(len < INT32_MAX ? len : INT32_MAX);
+                }
+            }
+            t += f[i];
+            p += pages_of(static_cast<int64_t>(c[i]) + f[i], page, width) -
+                 pages_of(c[i], page, width);
+        }
+        carry.tokens += total.tokens;
+        carry.pages += total.pages;
+        if (threadIdx.x == 0) {
+            s_cu[n] = carry.tokens;
+            s_first[n] = carry.pages;
+        }
+        __syncthreads();
+
+        // the pages that the requests take: one warp per table row
+        const int64_t skip = (my_warp - b0 % warps + warps) % warps;
+        for (int64_t r = skip; r < n; r += warps) {
+            const int64_t first = s_first[r], take = s_first[r + 1] - first;
+            const int64_t have = pages_of(s_ctx[r], page, width);
+            for (int64_t i = lane_id(); i < take; i += 32)
+                table[(b0 + r) * ld_table + have + i] =
+                    first + i < n_free ? free_pages[first + i] : -1;
+        }
+        // this CTA's tokens that belong to the chunk's requests
+        const int64_t lo = t_lo > s_cu[0] ? t_lo : s_cu[0];
+        const int64_t hi = t_hi < s_cu[n] ? t_hi : s_cu[n];
+        for (int64_t k = lo + threadIdx.x; k < hi; k += kThreads) {
+            int a = 0, e = n;  // the last request that starts at or before token k
+            while (e - a > 1) {
+                const int mid = (a + e) >> 1;
+                if (s_cu[mid] <= k) a = mid; else e = mid;
+            }
+            const int64_t at = s_ctx[a] + (k - s_cu[a]);
+            const int64_t pg = at / page;
+            const int64_t have = pages_of(s_ctx[a], page, width);
+            int64_t id = -1;
+            if (pg < have) {
+                id = table[(b0 + a) * ld_table + pg];
+            } else if (pg < width) {
+                const int64_t i = s_first[a] + pg - have;
+                if (i < n_free) id = free_pages[i];
+            }
+            slot[k] = id < 0 ? -1 : id * page + (at - pg * page);
+            pos[k] = static_cast<int32_t>(at < INT32_MAX ? at : INT32_MAX);
+        }
+        __syncthreads();
+    }
+    // room that no token needs
+    for (int64_t k = (t_lo > carry.tokens ? t_lo : carry.tokens) + threadIdx.x; k < t_hi;
+         k += kThreads) {
+        slot[k] = -1;
+        pos[k] = 0;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        cu[B] = static_cast<int32_t>(carry.tokens < T ? carry.tokens : T);
+        *used = static_cast<int32_t>(carry.pages < INT32_MAX ? carry.pages : INT32_MAX);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_slots(const int32_t* ctx, const int32_t* fresh, int64_t B,
+                            const int32_t* free_pages, int64_t n_free, int64_t page,
+                            int32_t* table, int64_t width, int64_t ld_table, int64_t T,
+                            int64_t* slot, int32_t* pos, int32_t* cu, int32_t* lens,
+                            int32_t* used, int num_sms, cudaStream_t st) {
+    // a token per thread and a table row per warp, as far as the SMs go
+    int64_t want = (T + kThreads - 1) / kThreads;
+    const int64_t rows = (B + kThreads / 32 - 1) / (kThreads / 32);
+    if (T > B && rows > want) want = rows;  // (one token each: at most one page each)
+    const int64_t grid = want < 1 ? 1 : want < num_sms ? want : num_sms;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_slots, ctx, fresh, B, free_pages, n_free, page, table, width,
+                              ld_table, T, (T + grid - 1) / grid, slot, pos, cu, lens, used);
+}
+
+}  // namespace fp8k

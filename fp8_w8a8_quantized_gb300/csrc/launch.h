@@ -99,6 +99,79 @@ cudaError_t launch_quant_weight_blocks(const void* w, int64_t N, int64_t K, int6
 // [M, ceil(K/128)] and s_w [ceil(N/128), ceil(K/128)].
 cudaError_t launch_gemm_blockwise(const GemmArgs& a);
 
+// Slot maps, positions and block-table entries of a step (kv_slots.cu).
+cudaError_t launch_kv_slots(const int32_t* ctx, const int32_t* fresh, int64_t B,
+                            const int32_t* free_pages, int64_t n_free, int64_t page,
+                            int32_t* table, int64_t width, int64_t ld_table, int64_t T,
+                            int64_t* slot, int32_t* pos, int32_t* cu, int32_t* lens,
+                            int32_t* used, int num_sms, cudaStream_t st);
+
+// Norms and rotation of queries and keys, FP8 cache write (norm_rope.cu).
+// Token strides ld* in elements; gamma_*, k_out, slot and the caches may be null.
+struct QkNormRopeArgs {
+    const uint16_t *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    int64_t T;
+    int Hq, Hkv, D, rot;
+    bool pairs;  // pairs (2 i, 2 i + 1) instead of (i, i + rot / 2)
+    const uint16_t *gamma_q, *gamma_k;
+    float eps;
+    const int32_t* positions;
+    const uint64_t* turns;
+    uint16_t *q_out, *k_out;
+    int64_t ldqo, ldko;
+    const float *k_scale, *v_scale;
+    int64_t scale_stride;
+    const int64_t* slot;
+    uint8_t *k_cache, *v_cache;
+    int64_t n_slots;
+};
+cudaError_t launch_qk_norm_rope(const QkNormRopeArgs& a, int num_sms, cudaStream_t st);
+
+// Causal attention over packed prompts (attention.cu).
+struct PromptArgs {
+    const uint16_t *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    int64_t T, B;
+    const int32_t* cu;
+    int Hq, Hkv, D;
+    float scale;
+    uint16_t* out;
+    int64_t ldo;
+    unsigned* status;
+    int num_sms;
+};
+cudaError_t launch_attention_prompt(const PromptArgs& a, cudaStream_t st);
+
+// Attention of one query per request over the paged FP8 cache (attention.cu).
+struct DecodeArgs {
+    const uint16_t* q;
+    int64_t ldq;
+    int64_t B;
+    int Hq, Hkv, D;
+    const uint8_t *k_cache, *v_cache;
+    int64_t n_pages;
+    const float *k_scale, *v_scale;
+    int64_t scale_stride;
+    const int32_t* table;
+    int64_t width, ld_table, page;
+    const int32_t* lens;
+    int64_t prefix;
+    float scale;
+    uint16_t* out;
+    int64_t ldo;
+    void* workspace;
+    unsigned* status;
+    int num_sms;
+};
+cudaError_t launch_attention_decode(const DecodeArgs& a, cudaStream_t st);
+size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t room,
+                                  int64_t prefix);
+
+// The current device's SM count and status word, after the same checks as
+// every other entry point (api.cu).
+fp8_status_t device_info(int* num_sms, unsigned** status);
+
 // Self-test of the bounded waits (selftest.cu): one CTA whose waits run out
 // after limit_ns; report[0..3] as fp8_selftest_wait_timeout documents.
 cudaError_t launch_wait_timeout_selftest(uint64_t limit_ns, unsigned* status,

@@ -353,6 +353,166 @@ FP8_API fp8_status_t fp8_linear_rmsnorm(const void* x_bf16, const void* gamma_bf
                                         int64_t M, int64_t N, int64_t K, void* workspace,
                                         size_t ws_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The attention block: what a serving step runs between the QKV layer and the
+ * O layer.  Queries, keys and values are bf16 [T, heads, D] tensors of packed
+ * tokens; a leading dimension ld* is the distance of two tokens in elements
+ * (so q, k and v may be views into one fused projection), and the heads of a
+ * token are contiguous.  The cache is the one that fp8_kv_cache_quant_kv
+ * writes, E4M3 [n_slots, Hkv, D] each for keys and values, cut into pages of
+ * page_size consecutive slots; row b of a block table names the pages of
+ * request b in order.  The pages have no counterpart for these operators.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Block tables, slot maps and positions of a step, from the requests' lengths.
+ * Request b has ctx_lens[b] tokens in the cache and new_lens[b] new ones
+ * (negative counts as 0).  With p = page_size, W = table_width:
+ *   have_b = min(W, ceil(ctx / p)),  need_b = min(W, ceil((ctx + new) / p)),
+ *   first_b = sum_{a<b} (need_a - have_a),  cu_b = sum_{a<b} new_a,
+ *   block_table[b, have_b + i] = free_pages[first_b + i], 0 <= i < need_b - have_b,
+ *   and for the i-th new token of request b, at index t = cu_b + i:
+ *   positions[t] = ctx_b + i,
+ *   slot_mapping[t] = block_table[b, positions[t] / p] * p + positions[t] % p.
+ * A token without a page has slot -1, which the cache writes skip: its table
+ * entry is negative, the table row is full, or free_pages ran out (then the
+ * table entry becomes -1 too).
+ *
+ *   ctx_lens, new_lens [device, in]  int32 [B]
+ *   free_pages   [device, in]      int32 [n_free], taken from the front
+ *   block_table  [device, in/out]  int32 [B, table_width], leading dimension
+ *                                  ld_table; entries below have_b are read,
+ *                                  have_b .. need_b - 1 written, others kept
+ *   max_tokens                     room in slot_mapping and positions; tokens
+ *                                  beyond it are dropped, entries beyond the
+ *                                  tokens get slot -1 and position 0
+ *   slot_mapping [device, out]     int64 [max_tokens]
+ *   positions    [device, out]     int32 [max_tokens]
+ *   cu_seqlens   [device, out]     int32 [B + 1], cu_b limited to max_tokens
+ *   seq_lens     [device, out]     int32 [B], ctx + new
+ *   pages_used   [device, out]     int32 [1], sum of need - have: more than
+ *                                  n_free says that free_pages ran out
+ * Requirements: page_size >= 1; B, n_free, max_tokens, page_size, table_width
+ * < 2^31; outputs must not overlap the inputs or one another.
+ */
+FP8_API fp8_status_t fp8_kv_slots(const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,
+                                  const int32_t* free_pages, int64_t n_free, int64_t page_size,
+                                  int32_t* block_table, int64_t table_width, int64_t ld_table,
+                                  int64_t max_tokens, int64_t* slot_mapping, int32_t* positions,
+                                  int32_t* cu_seqlens, int32_t* seq_lens, int32_t* pages_used,
+                                  void* stream);
+
+/*
+ * Norms of queries and keys for each head, the rotation of their positions,
+ * and the FP8 cache write, in one pass.  For each token t and head h, in fp32:
+ *   y_d = x_d / sqrt(mean_d x_d^2 + eps) * gamma_d   (y = x without a gamma)
+ *   (y_a, y_b) -> (y_a cos w - y_b sin w, y_b cos w + y_a sin w)
+ *   for the rot_dim / 2 pairs i: (a, b) = (i, i + rot_dim / 2), or
+ *   (2 i, 2 i + 1) with interleaved != 0, and w = 2 pi frac(position *
+ *   turns[i] / 2^64); elements rot_dim .. D - 1 stay; then one rounding to
+ *   bf16.  Frequencies are given as 64-bit fractions of a turn so that the
+ *   angle of a far position is exact: turns[i] = round(2^64 f_i / (2 pi)) for
+ *   a frequency of f_i radians per position.
+ *   With a cache, keys and values are then quantized exactly as
+ *   fp8_kv_cache_quant_kv(k_out, v, ...) would.
+ *
+ *   q, k   [device, in]   bf16 [T, Hq, D] and [T, Hkv, D], token strides ldq, ldk
+ *   v      [device, in]   bf16 [T, Hkv, D], ldv: for the cache; else NULL
+ *   gamma_q, gamma_k [device, in]  bf16 [D] each, or NULL: no norm
+ *   positions [device, in] int32 [T];  turns [device, in] uint64 [rot_dim / 2]
+ *   q_out  [device, out]  bf16 [T, Hq, D], ldqo; may be q itself (ldqo = ldq)
+ *   k_out  [device, out]  bf16 [T, Hkv, D], ldko; may be k itself; NULL with
+ *                         a cache: the rotated keys go to the cache alone
+ *   k_scale, v_scale, scale_stride, slot_mapping, n_slots
+ *                         as for fp8_kv_cache_quant_kv
+ *   k_cache, v_cache [device, out]  E4M3 [n_slots, Hkv, D], or both NULL: no
+ *                         cache write (v, scales and slots are then unused)
+ * Requirements: D % 16 == 0, D <= 256; 0 <= rot_dim <= D, rot_dim % 16 == 0;
+ * leading dimensions >= heads * D and % 8 == 0; bf16 tensors and gammas
+ * 16-byte aligned, caches 8, positions and scales 4, turns and slots 8;
+ * eps >= 0 finite; Hq + 2 Hkv <= 65536.
+ */
+FP8_API fp8_status_t fp8_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                      const void* v, int64_t ldv, int64_t T, int64_t Hq,
+                                      int64_t Hkv, int64_t D, const void* gamma_q,
+                                      const void* gamma_k, float eps, const int32_t* positions,
+                                      const uint64_t* turns, int64_t rot_dim, int interleaved,
+                                      void* q_out, int64_t ldqo, void* k_out, int64_t ldko,
+                                      const float* k_scale, const float* v_scale,
+                                      int64_t scale_stride, const int64_t* slot_mapping,
+                                      uint8_t* k_cache, uint8_t* v_cache, int64_t n_slots,
+                                      void* stream);
+
+/*
+ * Causal attention over whole prompts, packed one after the other.  Sequence
+ * s holds tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1; query head h reads
+ * key and value head h / (Hq / Hkv):
+ *   out[i, h] = bf16_rn( sum_{j <= i, same sequence} w_ij v_j / sum w_ij ),
+ *   w_ij = exp(scale q_i . k_j - max_j), products accumulated in fp32, the
+ *   maximum and sums in fp32, w rounded to bf16 for its product with v.
+ * Keys and values that a query does not see have no influence on it, whatever
+ * they hold (infinities and NaN among it).  Tokens outside every sequence get
+ * no output.
+ *
+ *   q, k, v [device, in]  bf16 [T, Hq, D], [T, Hkv, D], [T, Hkv, D]
+ *   cu_seqlens [device, in]  int32 [S + 1], non-decreasing, 0 .. T
+ *   out    [device, out]  bf16 [T, Hq, D], ldo; overlaps no input
+ * Requirements: Hq % Hkv == 0, Hq / Hkv <= 64; D % 16 == 0, 16 <= D <= 128;
+ * leading dimensions >= heads * D and % 8 == 0; 16-byte aligned tensors;
+ * scale > 0 finite; Hkv <= 65535.
+ */
+FP8_API fp8_status_t fp8_attention_prompt(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                          const void* v, int64_t ldv, int64_t T, int64_t Hq,
+                                          int64_t Hkv, int64_t D, const int32_t* cu_seqlens,
+                                          int64_t S, float scale, void* out, int64_t ldo,
+                                          void* stream);
+
+/*
+ * Attention of one new token per request over the paged FP8 cache:
+ *   out[b, h] = bf16_rn( v_scale[hk] sum_{j < len_b} w_j v_j / sum w_j ),
+ *   w_j = exp(scale k_scale[hk] q . k_j - max_j),  hk = h / (Hq / Hkv),
+ * where token j of request b lies in slot block_table[b, j / p] * p + j % p.
+ * len_b is seq_lens[b], at least 0 and at most table_width * page_size; a
+ * request without tokens gets zeros.  A table entry outside 0 ..
+ * n_slots / page_size - 1 hides its page's tokens.
+ * The first prefix_len tokens are read once for all requests, from the pages
+ * of table row 0: the caller says by prefix_len > 0 that every request's
+ * first prefix_len tokens are the same ones (a shared system prompt, in pages
+ * that all rows name).  A request with fewer tokens sees its len_b of them.
+ *
+ *   q      [device, in]   bf16 [B, Hq, D], ldq
+ *   k_cache, v_cache [device, in]  E4M3 [n_slots, Hkv, D], contiguous
+ *   k_scale, v_scale [device, in]  fp32 [Hkv] with scale_stride 1, or [1]
+ *                         with scale_stride 0; k_scale > 0
+ *   block_table [device, in]  int32 [B, table_width], leading dim ld_table
+ *   seq_lens [device, in]  int32 [B]
+ *   prefix_len            0 .. table_width * page_size
+ *   out    [device, out]  bf16 [B, Hq, D], ldo; overlaps no input
+ *   workspace [device]    fp8_attention_decode_workspace_size() bytes,
+ *                         256-byte aligned; need not start at zero; not in
+ *                         use by another call in flight.  NULL if that is 0.
+ * Requirements: Hq % Hkv == 0, Hq / Hkv <= 64; D % 16 == 0, 16 <= D <= 128;
+ * leading dimensions >= heads * D and % 8 == 0; 16-byte aligned tensors;
+ * scale > 0 finite; page_size >= 1; table_width * page_size < 2^31;
+ * B * Hkv < 2^24.
+ */
+FP8_API fp8_status_t fp8_attention_decode(const void* q, int64_t ldq, int64_t B, int64_t Hq,
+                                          int64_t Hkv, int64_t D, const uint8_t* k_cache,
+                                          const uint8_t* v_cache, int64_t n_slots,
+                                          const float* k_scale, const float* v_scale,
+                                          int64_t scale_stride, const int32_t* block_table,
+                                          int64_t table_width, int64_t ld_table,
+                                          int64_t page_size, const int32_t* seq_lens,
+                                          int64_t prefix_len, float scale, void* out, int64_t ldo,
+                                          void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes fp8_attention_decode needs; 0 for invalid sizes. */
+FP8_API size_t fp8_attention_decode_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                                   int64_t table_width, int64_t page_size,
+                                                   int64_t prefix_len);
+
 /* Workspace bytes fp8_linear needs for an [M, K] x [N, K]^T layer:
  * round_up(M*K, 256) + round_up(4*M, 256).  0 for invalid sizes. */
 FP8_API size_t fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K);
