@@ -24,7 +24,7 @@ LIB_NAME = "libfp8w8a8.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "quant.cu", "quant_variants.cu", "norm_quant.cu", "gemm_pair.cu", "gemm_decode.cu", "gemm_blockwise.cu", "noalloc.cu",
-           "selftest.cu", "attention_api.cu", "kv_slots.cu", "norm_rope.cu", "attention.cu"]
+           "selftest.cu", "attention_api.cu", "kv_slots.cu", "norm_rope.cu", "attention_prompt.cu", "attention_decode.cu"]
 HEADERS = ["ptx.cuh", "launch.h", "quant_math.cuh", "decode_common.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

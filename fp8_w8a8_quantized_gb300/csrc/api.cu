@@ -57,7 +57,8 @@ fp8_status_t current_device(DeviceState** out) {
                        cudaSuccess ||
                    fp8k::prepare_gemm_decode() != cudaSuccess ||
                    fp8k::prepare_gemm_blockwise() != cudaSuccess ||
-                   fp8k::prepare_gemm_pair() != cudaSuccess) {
+                   fp8k::prepare_gemm_pair() != cudaSuccess ||
+                   fp8k::prepare_attention() != cudaSuccess) {
             d.verdict = FP8_ERR_CUDA;
         } else {
             d.pair_clusters = fp8k::gemm_pair_resident_clusters(d.num_sms);
@@ -201,6 +202,21 @@ bool encode_tmap_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
     const cuuint32_t estr[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+bool encode_tmap_heads(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads,
+                       uint64_t dim, uint64_t token_bytes, uint32_t box_dim, uint32_t box_heads,
+                       uint32_t box_tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {dim, heads, tokens};
+    const cuuint64_t strides[2] = {2 * dim, token_bytes};
+    const cuuint32_t box[3] = {box_dim, box_heads, box_tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }

@@ -1,5 +1,6 @@
 // C-ABI entry points of the attention block (fp8w8a8.h): host-side argument
-// checks and the launches of kv_slots.cu, norm_rope.cu and attention.cu.
+// checks and the launches of kv_slots.cu, norm_rope.cu, attention_prompt.cu and
+// attention_decode.cu.
 #include <cuda_runtime.h>
 
 #include <cmath>

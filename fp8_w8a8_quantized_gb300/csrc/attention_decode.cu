@@ -56,38 +56,6 @@ struct Row {
     }
 };
 
-__global__ void __launch_bounds__(kThreads) attention_prompt(const PromptArgs a) {
-    pdl_launch_dependents();
-    pdl_wait_primary();
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = w / a.Hq;
-    const int h = static_cast<int>(w - t * a.Hq), hk = h / (a.Hq / a.Hkv);
-    if (t >= a.T) return;
-    const int lane = lane_id();
-    const bool on = lane * 4 < a.D;
-    // the sequence that holds token t
-    int64_t lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.cu[mid] <= t) lo = mid; else hi = mid;
-    }
-    const int64_t first = a.cu[lo] < 0 ? 0 : a.cu[lo];
-    if (t < first || t >= a.cu[lo + 1]) return;
-    const float c = a.scale * kLog2e;
-    float q[4] = {};
-    if (on) widen4(*reinterpret_cast<const uint2*>(a.q + t * a.ldq + h * a.D + lane * 4), q);
-    Row r;
-    for (int64_t j = first; j <= t; ++j) {
-        float k[4] = {}, v[4] = {};
-        if (on) {
-            widen4(*reinterpret_cast<const uint2*>(a.k + j * a.ldk + hk * a.D + lane * 4), k);
-            widen4(*reinterpret_cast<const uint2*>(a.v + j * a.ldv + hk * a.D + lane * 4), v);
-        }
-        r.add(q, k, v, c);
-    }
-    if (on) r.write(a.out + t * a.ldo + h * a.D + lane * 4, 1.0f);
-}
-
 __global__ void __launch_bounds__(kThreads) attention_decode(const DecodeArgs a) {
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -132,10 +100,6 @@ cudaError_t launch(void (*kernel)(Args), int64_t warps, cudaStream_t st, const A
 }
 
 }  // namespace
-
-cudaError_t launch_attention_prompt(const PromptArgs& a, cudaStream_t st) {
-    return launch(attention_prompt, a.T * a.Hq, st, a);
-}
 
 size_t attention_decode_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) {
     return 0;

@@ -47,6 +47,12 @@ struct GemmArgs {
 bool encode_tmap_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                     uint64_t ld_bytes, uint32_t box_cols, uint32_t box_rows);
 
+// bf16 [tokens, heads, dim] (token stride token_bytes) as a 3-D tensor map with
+// 128-byte swizzle and zeros beyond the edges; box_dim <= 64.  (api.cu)
+bool encode_tmap_heads(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads,
+                       uint64_t dim, uint64_t token_bytes, uint32_t box_dim, uint32_t box_heads,
+                       uint32_t box_tokens);
+
 // Weight-streaming split-K tcgen05 GEMM for M <= kDecodeMaxM (gemm_decode.cu);
 // the block-scaled variant (gemm_blockwise.cu) up to kBlockwiseDecodeMaxM.
 constexpr int kDecodeMaxM = 256;
@@ -128,7 +134,7 @@ struct QkNormRopeArgs {
 };
 cudaError_t launch_qk_norm_rope(const QkNormRopeArgs& a, int num_sms, cudaStream_t st);
 
-// Causal attention over packed prompts (attention.cu).
+// Causal attention over packed prompts (attention_prompt.cu).
 struct PromptArgs {
     const uint16_t *q, *k, *v;
     int64_t ldq, ldk, ldv;
@@ -143,7 +149,7 @@ struct PromptArgs {
 };
 cudaError_t launch_attention_prompt(const PromptArgs& a, cudaStream_t st);
 
-// Attention of one query per request over the paged FP8 cache (attention.cu).
+// Attention of one query per request over the paged FP8 cache (attention_decode.cu).
 struct DecodeArgs {
     const uint16_t* q;
     int64_t ldq;
@@ -187,5 +193,6 @@ fp8_status_t linear_checks(const void* x, const uint8_t* wq, const float* s_w, c
 cudaError_t prepare_gemm_decode();
 cudaError_t prepare_gemm_blockwise();
 cudaError_t prepare_gemm_pair();
+cudaError_t prepare_attention();
 
 }  // namespace fp8k

@@ -189,7 +189,8 @@ def prompt_tol(want, size):
 PROMPTS = [([1], 1, 1, 16), ([2, 0, 1, 3], 2, 1, 32), ([129], 4, 1, 128), ([128, 127, 1, 255], 8, 2, 64),
            ([300, 5, 0, 0, 77], 6, 2, 80), ([64, 65, 63], 7, 1, 96), ([513], 3, 3, 112),
            ([1] * 70, 8, 8, 128), ([200, 40], 64, 1, 128), ([257, 256, 31], 12, 4, 48),
-           ([1000, 1025], 4, 2, 128), ([33] * 40, 5, 5, 64)]
+           ([1000, 1025], 4, 2, 128), ([33] * 40, 5, 5, 64),
+           ([1500, 2, 1999], 16, 16, 128), ([3001], 32, 4, 64)]
 
 
 @pytest.mark.parametrize("lens,Hq,Hkv,D", PROMPTS)
