@@ -522,7 +522,7 @@ cudaError_t launch_attention_prompt(const PromptArgs& a, cudaStream_t st) {
     return a.D <= 64 ? launch_dim<64>(a, st) : launch_dim<128>(a, st);
 }
 
-cudaError_t prepare_attention() {
+cudaError_t prepare_attention_prompt() {
     const cudaError_t e = cudaFuncSetAttribute(attention_prompt<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem_bytes<64>()));
     return e != cudaSuccess ? e

@@ -193,6 +193,7 @@ fp8_status_t linear_checks(const void* x, const uint8_t* wq, const float* s_w, c
 cudaError_t prepare_gemm_decode();
 cudaError_t prepare_gemm_blockwise();
 cudaError_t prepare_gemm_pair();
-cudaError_t prepare_attention();
+cudaError_t prepare_attention_prompt();
+cudaError_t prepare_attention_decode();
 
 }  // namespace fp8k
