@@ -6,9 +6,10 @@
 // follows the maximum in steps of at least 2^8).
 //
 // Bound by reading the cache: 2 D bytes a token and key head, each used for
-// the G = Hq / Hkv queries of the group, so nothing of it goes through shared
-// memory or is read twice.  A warp takes 16 tokens of one key head at a time,
-// straight from global memory into registers, the next 16 while it computes:
+// the G = Hq / Hkv queries of the group.  A warp takes 32 tokens of one key
+// head at a time.  Asynchronous copies bring them into a ring of its own in
+// shared memory (no barrier but the warp's own), kStages steps deep: up to 192
+// KB of loads in flight an SM.
 //
 //   S^T [16 tokens x 8 queries] = K [16 x D] Q^T     m16n8k16, f16, fp32 sums
 //   O^T [D x 8 queries]        += V^T [D x 16] P^T
@@ -43,17 +44,17 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;       // log2 of how far p may exceed 1 before m moves
-constexpr int kTile = 16;            // tokens of a warp's step
+constexpr int kTile = 32;            // tokens of a warp's step
+constexpr int kWarps = 8;            // warps of a CTA
 constexpr int kCtas = 152;           // CTAs at most (one per SM)
 constexpr int64_t kMaxPlan = 4096;   // requests up to which the work is cut by tokens
-constexpr int kMinUnits = 4;         // steps that are worth a CTA
+constexpr int kMinTokens = 64;       // tokens of a request that are worth a CTA
 
-// Where the work of CTA `c` begins inside a request: that request's steps.
+// A request whose steps several CTAs share, for the kernel that joins them.
 struct Cut {
     int64_t first, end;  // its steps, counted over all requests
-    int64_t total;       // steps of all requests (a header's total of 0: no cut here)
+    int64_t per;         // steps of a CTA (0: the request is not cut)
     int32_t request, group;
-    int32_t ctas, pad;
 };
 
 struct Shape {
@@ -75,8 +76,7 @@ __host__ __device__ inline Shape shape_of(int Hq, int Hkv) {
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -116,26 +116,42 @@ __device__ __forceinline__ float scaled(float x, int n) {
            __uint_as_float(static_cast<uint32_t>(127 + n - h) << 23);
 }
 
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+// 16 bytes into shared memory: an asynchronous copy, or zeros at once where
+// there is nothing to copy (`src` is not touched then).
+__device__ __forceinline__ void copy_async16(uint32_t dst, const uint8_t* src, bool there) {
+    if (there)
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the last N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
-__device__ __forceinline__ uint2 ld_stream8(const uint8_t* p) {
+__device__ __forceinline__ uint2 ld_shared8(uint32_t addr) {
     uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                 : "=r"(v.x), "=r"(v.y)
-                 : "l"(p));
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
 
-__device__ __forceinline__ int64_t cut_at(int64_t total, int c, int ctas) {
-    return total / ctas * c + total % ctas * c / ctas;
+// Steps of a CTA: an even share, and no fewer than are worth a CTA.  (32-bit
+// division where the numbers allow: the 64-bit one takes a microsecond here.)
+__device__ __forceinline__ int64_t divide_up(int64_t n, int64_t d) {
+    n += d - 1;
+    return (n | d) >> 32 ? n / d : static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
 }
 
-// The partial results in the workspace: after kCtas cuts, (m, l) and then o of
+// The partial results in the workspace: after the cuts, (m, l) and then o of
 // [cta][0: the request that the CTA begins in, 1: the one it ends in][head][row].
 struct Parts {
     Cut* cuts;
@@ -155,24 +171,34 @@ __device__ __forceinline__ Parts parts_of(void* ws, int heads) {
     return p;
 }
 
-// One request's tokens, as far as a warp is concerned.
+// A warp's ring: kStages steps of kTile tokens' keys, then values, in rows of DP
+// bytes.  16-byte chunk c of row r lies at c ^ key_swizzle(r) (values:
+// value_swizzle(r)), so that the fragments' 16-byte reads meet no bank twice.
 template <int DP>
-struct Tokens {
-    static constexpr int KW = DP / 64;   // 16-byte loads of a token's keys
-    static constexpr int VW = DP / 32;   // words of a lane's share of a token's values
-    uint4 k[2][KW];
-    uint32_t v[4][VW];
+struct Ring {
+    static constexpr int kStages = DP == 128 ? 3 : 6;
+    static constexpr uint32_t kHalf = kTile * DP;       // bytes of the keys of a step
+    static constexpr uint32_t kBytes = 2 * kHalf * kStages;
+    static constexpr int kChunks = DP / 16;
+    __device__ static uint32_t key(int r, int c) {
+        return static_cast<uint32_t>(r * DP + 16 * (DP == 128 ? c ^ ((r & 1) << 2) : c));
+    }
+    __device__ static uint32_t value(int r, int c) {
+        return static_cast<uint32_t>(r * DP + 16 * (c ^ (DP == 128 ? (r >> 1 & 3) << 1 : r >> 1 & 3)));
+    }
 };
 
 // NT: tiles of 8 queries.  DP: 64 or 128, at least D.  W: warps of a CTA.
 template <int NT, int DP, int W>
 __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a, const bool planned) {
-    using Tok = Tokens<DP>;
+    using R16 = Ring<DP>;
     constexpr int R = 8 * NT;
     constexpr int MT = DP / 16;  // tiles of 16 output elements
-    extern __shared__ __align__(16) uint8_t smem[];
-    int64_t* upto = reinterpret_cast<int64_t*>(smem);      // [B + 1] steps before request b
+    constexpr int ST = R16::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    int64_t* upto = reinterpret_cast<int64_t*>(smem + W * R16::kBytes);  // [B + 1] steps before request b
     __shared__ int64_t warp_sums[W];
+    __shared__ uint32_t there_of[W][ST];  // which tokens of a step exist
     const int warp = threadIdx.x >> 5, lane = lane_id();
     const int g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
@@ -188,14 +214,13 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
     };
 
     // the line of work
-    int64_t total = 0, lo, hi;
-    int ctas = gridDim.x;
+    int64_t per = 0, lo, hi;
     if (planned) {
         int64_t carry = 0;
         for (int64_t b0 = 0; b0 < a.B; b0 += W * 32) {
             const int64_t b = b0 + threadIdx.x;
             // (a request without tokens has one step: someone has to write its zeros)
-            const int64_t n = b < a.B ? max((length(b) + step - 1) / step, int64_t(1)) : 0;
+            const int64_t n = b < a.B ? max(divide_up(length(b), step), int64_t(1)) : 0;
             int64_t x = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -215,58 +240,53 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
         }
         if (threadIdx.x == 0) upto[0] = 0;
         __syncthreads();
-        total = upto[a.B] * sh.groups;
-        const int64_t worth = (total + kMinUnits - 1) / kMinUnits;
-        ctas = worth < ctas ? static_cast<int>(worth) : ctas;
-        lo = hi = 0;
-        if (static_cast<int>(blockIdx.x) < ctas) {
-            lo = cut_at(total, blockIdx.x, ctas);
-            hi = cut_at(total, blockIdx.x + 1, ctas);
-        }
+        const int64_t total = upto[a.B] * sh.groups;
+        per = max(divide_up(total, gridDim.x), int64_t(max(kMinTokens / step, 1)));
+        lo = min(per * blockIdx.x, total);
+        hi = min(lo + per, total);
     } else {  // so many requests that each goes to one CTA as a whole
         lo = blockIdx.x;
         hi = a.B * sh.groups;
     }
     const Parts parts = parts_of<NT, DP, W>(a.workspace, sh.heads);
-    if (planned && threadIdx.x == 0 && static_cast<int>(blockIdx.x) >= ctas)
-        parts.cuts[blockIdx.x].total = 0;
+    const bool by_request = a.B * sh.groups <= kCtas;  // the cuts' order: requests, or CTAs that begin in one
+    if (planned && threadIdx.x == 0 && !by_request) parts.cuts[blockIdx.x].per = 0;
 
     const int way = warp / sh.heads, my_head = warp - way * sh.heads;
     const bool works = way < sh.ways;
+    const uint32_t ring = smem_u32(smem) + warp * R16::kBytes;
     const int64_t begin = lo;
     while (lo < hi) {
         // the request that step `lo` lies in, and how far this CTA goes in it
         int64_t b, first, end, u0, u1;  // its steps; this CTA's, counted from its first
-        int group;
+        int group = 0;
         if (planned) {
-            group = static_cast<int>(lo / upto[a.B]);
-            const int64_t at = lo - group * upto[a.B];
-            int64_t x = 0, y = a.B;
+            int64_t at = lo;
+            while (at >= upto[a.B]) {
+                at -= upto[a.B];
+                ++group;
+            }
+            int x = 0, y = static_cast<int>(a.B);
             while (y - x > 1) {
-                const int64_t mid = (x + y) >> 1;
+                const int mid = (x + y) >> 1;
                 if (upto[mid] <= at) x = mid; else y = mid;
             }
             b = x;
-            first = group * upto[a.B] + upto[b];
-            end = group * upto[a.B] + upto[b + 1];
+            first = lo - at + upto[b];
+            end = lo - at + upto[b + 1];
             u0 = lo - first;
             u1 = min(end, hi) - first;
-            if (lo == begin && threadIdx.x == 0) {
-                Cut cut;
-                cut.first = first;
-                cut.end = end;
-                cut.total = u0 > 0 ? total : 0;
-                cut.request = static_cast<int32_t>(b);
-                cut.group = group;
-                cut.ctas = ctas;
-                cut.pad = 0;
-                parts.cuts[blockIdx.x] = cut;
+            // the CTA that begins a request, or that begins inside one, tells of the cut
+            if (threadIdx.x == 0 && (by_request ? u0 == 0 : u0 > 0 && u0 <= per)) {
+                const bool cut = by_request ? hi < end : true;
+                parts.cuts[by_request ? group * a.B + b : blockIdx.x] =
+                    Cut{first, end, cut ? per : 0, static_cast<int32_t>(b), group};
             }
         } else {
             group = static_cast<int>(lo / a.B);
             b = lo - group * a.B;
             first = end = u0 = 0;
-            u1 = (length(b) + step - 1) / step;
+            u1 = divide_up(length(b), step);
         }
         const bool whole = !planned || (lo == first && hi >= end);
         const int slot = lo == begin ? 0 : 1;  // (only a CTA's first and last request can be cut)
@@ -290,6 +310,44 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
             l[x][0] = l[x][1] = 0.0f;
         }
         if (on) {
+            const int64_t row_bytes = static_cast<int64_t>(a.Hkv) * a.D;
+            const uint8_t* kc = a.k_cache + static_cast<int64_t>(hk) * a.D;
+            const uint8_t* vc = a.v_cache + static_cast<int64_t>(hk) * a.D;
+            const int32_t* own_row = a.table + b * a.ld_table;
+            const unsigned page = static_cast<unsigned>(a.page);
+            // the slot of a lane's token of a step; -1 where there is none
+            auto slot_of = [&](int64_t u) {
+                const int64_t tok = (u * sh.ways + way) * kTile + lane;
+                if (u >= u1 || tok >= len) return -1;
+                const unsigned pg = static_cast<unsigned>(tok) / page;
+                const int id = __ldg((tok < a.prefix ? a.table : own_row) + pg);
+                if (id < 0 || id >= a.n_pages) return -1;
+                return static_cast<int>(id * page + (static_cast<unsigned>(tok) - pg * page));
+            };
+            auto issue = [&](int stage, int slots) {
+                const unsigned votes = __ballot_sync(0xFFFFFFFFu, slots >= 0);
+                if (lane == 0) there_of[warp][stage] = votes;
+                const uint32_t dst = ring + stage * 2 * R16::kHalf;
+#pragma unroll
+                for (int i = 0; i < kTile * R16::kChunks / 32; ++i) {
+                    const int r = (32 * i + lane) / R16::kChunks, ch = lane % R16::kChunks;
+                    const int s = __shfl_sync(0xFFFFFFFFu, slots, r);
+                    const bool there = s >= 0 && 16 * ch < a.D;
+                    const int64_t off = s * row_bytes + 16 * ch;
+                    copy_async16(dst + R16::key(r, ch), kc + off, there);
+                    copy_async16(dst + R16::kHalf + R16::value(r, ch), vc + off, there);
+                }
+            };
+            int ahead[ST];  // the slots of the next steps to be issued
+#pragma unroll
+            for (int i = 0; i < ST; ++i) ahead[i] = slot_of(u0 + i);
+#pragma unroll
+            for (int i = 0; i < ST - 1; ++i) {
+                if (u0 + i < u1) issue(i, ahead[i]);
+                copy_commit();
+            }
+            int next = ahead[ST - 1];
+
             // queries: row g of each tile, the elements that this lane's keys meet
             const float unit = a.scale * kLog2e * a.k_scale[hk * a.scale_stride];
 #pragma unroll
@@ -337,96 +395,60 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
                 c[x][1] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t + 4);
             }
 
-            const int64_t row_bytes = static_cast<int64_t>(a.Hkv) * a.D;
-            const uint8_t* kc = a.k_cache + static_cast<int64_t>(hk) * a.D;
-            const uint8_t* vc = a.v_cache + static_cast<int64_t>(hk) * a.D;
-            const int32_t* own_row = a.table + b * a.ld_table;
-            const int page = static_cast<int>(a.page);
-            // the slot of token (lane mod 16) of a step, -1 where there is none
-            auto slot_of = [&](int64_t u) {
-                const int64_t tok = (u * sh.ways + way) * kTile + (lane & 15);
-                if (u >= u1 || tok >= len) return -1;
-                const int pg = static_cast<int>(tok) / page;
-                const int id = __ldg((tok < a.prefix ? a.table : own_row) + pg);
-                if (id < 0 || id >= a.n_pages) return -1;
-                return id * page + (static_cast<int>(tok) - pg * page);
-            };
-            auto load_k = [&](Tok& x, int slots) {
+            int stage = 0;
+            for (int64_t u = u0; u < u1; ++u) {
+                copy_wait<ST - 2>();
+                __syncwarp();  // step u has landed for all lanes, and all are done with step u - 1
+                const unsigned there = there_of[warp][stage];
+                const uint32_t src = ring + stage * 2 * R16::kHalf;
+                if (u + ST - 1 < u1) issue(stage == 0 ? ST - 1 : stage - 1, next);
+                copy_commit();
+                next = slot_of(u + ST);
+                stage = stage + 1 == ST ? 0 : stage + 1;
+
+                float s[2][NT][4];  // of 16 tokens each
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int s = __shfl_sync(0xFFFFFFFFu, slots, g + 8 * r);
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int j = 0; j < Tok::KW; ++j) {
-                        x.k[r][j] = make_uint4(0, 0, 0, 0);
-                        const int d = 64 * j + 16 * t;
-                        if (s >= 0 && d < a.D) x.k[r][j] = ld_stream(kc + s * row_bytes + d);
-                    }
-                }
-            };
-            auto load_v = [&](Tok& x, int slots) {
+                    for (int y = 0; y < NT; ++y)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int s = __shfl_sync(0xFFFFFFFFu, slots, 2 * t + (r & 1) + 8 * (r >> 1));
+                        for (int e = 0; e < 4; ++e) s[h][y][e] = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < Tok::VW; ++i) x.v[r][i] = 0;
-                    const int d = DP / 8 * g;
-                    if (s >= 0 && d < a.D) {
-                        const uint8_t* p = vc + s * row_bytes + d;
-                        if constexpr (DP == 128) {
-                            const uint4 w = ld_stream(p);
-                            x.v[r][0] = w.x, x.v[r][1] = w.y, x.v[r][2] = w.z, x.v[r][3] = w.w;
-                        } else {
-                            const uint2 w = ld_stream8(p);
-                            x.v[r][0] = w.x, x.v[r][1] = w.y;
+                for (int j = 0; j < DP / 64; ++j) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 k0 = ld_shared16(src + R16::key(16 * h + g, 4 * j + t));
+                        const uint4 k1 = ld_shared16(src + R16::key(16 * h + g + 8, 4 * j + t));
+                        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w};
+                        const uint32_t w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a0 = f16_lo(w0[i]), a1 = f16_lo(w1[i]);
+                            const uint32_t a2 = f16_hi(w0[i]), a3 = f16_hi(w1[i]);
+#pragma unroll
+                            for (int y = 0; y < NT; ++y)
+                                mma_16816(s[h][y], a0, a1, a2, a3, q[y][4 * j + i][0], q[y][4 * j + i][1]);
                         }
                     }
                 }
-            };
-
-            Tok x;
-            int now = slot_of(u0);
-            load_k(x, now);
-            load_v(x, now);
-            int next = slot_of(u0 + 1);
-            for (int64_t u = u0; u < u1; ++u) {
-                const unsigned there = __ballot_sync(0xFFFFFFFFu, now >= 0);
-                const bool on0 = (there >> g) & 1u, on1 = (there >> (g + 8)) & 1u;
-                float s[NT][4];
-#pragma unroll
-                for (int y = 0; y < NT; ++y)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[y][e] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < Tok::KW; ++j) {
-                    const uint32_t w0[4] = {x.k[0][j].x, x.k[0][j].y, x.k[0][j].z, x.k[0][j].w};
-                    const uint32_t w1[4] = {x.k[1][j].x, x.k[1][j].y, x.k[1][j].z, x.k[1][j].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = f16_lo(w0[i]), a1 = f16_lo(w1[i]);
-                        const uint32_t a2 = f16_hi(w0[i]), a3 = f16_hi(w1[i]);
-#pragma unroll
-                        for (int y = 0; y < NT; ++y)
-                            mma_16816(s[y], a0, a1, a2, a3, q[y][4 * j + i][0], q[y][4 * j + i][1]);
-                    }
-                }
-                load_k(x, next);
-                // softmax: columns 2 t, 2 t + 1 of tokens g and g + 8
+                // softmax: columns 2 t, 2 t + 1 of tokens 16 h + g and 16 h + g + 8
                 bool raise = false;
 #pragma unroll
-                for (int y = 0; y < NT; ++y) {
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[y][e] *= c[y][e & 1];
-                        if (!(e < 2 ? on0 : on1)) s[y][e] = -INFINITY;
-                        raise |= s[y][e] - m[y][e & 1] > kSlack;
-                    }
-                }
+                    for (int y = 0; y < NT; ++y)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s[h][y][e] *= c[y][e & 1];
+                            if (!((there >> (16 * h + 8 * (e >> 1) + g)) & 1u)) s[h][y][e] = -INFINITY;
+                            raise |= s[h][y][e] - m[y][e & 1] > kSlack;
+                        }
                 if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
                     for (int y = 0; y < NT; ++y)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float top = fmaxf(s[y][e], s[y][e + 2]);
+                            float top = fmaxf(fmaxf(s[0][y][e], s[0][y][e + 2]), fmaxf(s[1][y][e], s[1][y][e + 2]));
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1)
                                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
@@ -442,37 +464,55 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
                             }
                         }
                 }
-                uint32_t p[NT][2];
+                uint32_t p[2][NT][2];
 #pragma unroll
                 for (int y = 0; y < NT; ++y) {
                     const float b0 = m[y][0] == -INFINITY ? 0.0f : m[y][0];
                     const float b1 = m[y][1] == -INFINITY ? 0.0f : m[y][1];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[y][e] = ex2(s[y][e] - (e & 1 ? b1 : b0));
-                        l[y][e & 1] += s[y][e];
-                    }
-                    p[y][0] = transpose_8x8(pack_f16(s[y][0], s[y][1]));
-                    p[y][1] = transpose_8x8(pack_f16(s[y][2], s[y][3]));
-                }
+                    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int i = 0; i < Tok::VW; ++i) {
-                    const uint32_t p0 = __byte_perm(x.v[0][i], x.v[1][i], 0x5140);
-                    const uint32_t p1 = __byte_perm(x.v[0][i], x.v[1][i], 0x7362);
-                    const uint32_t p2 = __byte_perm(x.v[2][i], x.v[3][i], 0x5140);
-                    const uint32_t p3 = __byte_perm(x.v[2][i], x.v[3][i], 0x7362);
-                    const uint32_t a0 = f16_lo(p0), a1 = f16_hi(p0), a2 = f16_lo(p2), a3 = f16_hi(p2);
-                    const uint32_t c0 = f16_lo(p1), c1 = f16_hi(p1), c2 = f16_lo(p3), c3 = f16_hi(p3);
-#pragma unroll
-                    for (int y = 0; y < NT; ++y) {
-                        mma_16816(o[2 * i][y], a0, a1, a2, a3, p[y][0], p[y][1]);
-                        mma_16816(o[2 * i + 1][y], c0, c1, c2, c3, p[y][0], p[y][1]);
+                        for (int e = 0; e < 4; ++e) {
+                            s[h][y][e] = ex2(s[h][y][e] - (e & 1 ? b1 : b0));
+                            l[y][e & 1] += s[h][y][e];
+                        }
+                        p[h][y][0] = transpose_8x8(pack_f16(s[h][y][0], s[h][y][1]));
+                        p[h][y][1] = transpose_8x8(pack_f16(s[h][y][2], s[h][y][3]));
                     }
                 }
-                load_v(x, next);
-                now = next;
-                next = slot_of(u + 2);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[4][DP / 32];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 16 * h + 2 * t + (r & 1) + 8 * (r >> 1);
+                        const uint32_t half = src + R16::kHalf;
+                        if constexpr (DP == 128) {
+                            const uint4 w = ld_shared16(half + R16::value(row, g));
+                            v[r][0] = w.x, v[r][1] = w.y, v[r][2] = w.z, v[r][3] = w.w;
+                        } else {
+                            const uint2 w = ld_shared8(half + R16::value(row, g >> 1) + 8 * (g & 1));
+                            v[r][0] = w.x, v[r][1] = w.y;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < DP / 32; ++i) {
+                        const uint32_t p0 = __byte_perm(v[0][i], v[1][i], 0x5140);
+                        const uint32_t p1 = __byte_perm(v[0][i], v[1][i], 0x7362);
+                        const uint32_t p2 = __byte_perm(v[2][i], v[3][i], 0x5140);
+                        const uint32_t p3 = __byte_perm(v[2][i], v[3][i], 0x7362);
+                        const uint32_t a0 = f16_lo(p0), a1 = f16_hi(p0), a2 = f16_lo(p2), a3 = f16_hi(p2);
+                        const uint32_t c0 = f16_lo(p1), c1 = f16_hi(p1), c2 = f16_lo(p3), c3 = f16_hi(p3);
+#pragma unroll
+                        for (int y = 0; y < NT; ++y) {
+                            mma_16816(o[2 * i][y], a0, a1, a2, a3, p[h][y][0], p[h][y][1]);
+                            mma_16816(o[2 * i + 1][y], c0, c1, c2, c3, p[h][y][0], p[h][y][1]);
+                        }
+                    }
+                }
             }
+            copy_wait<0>();
+            __syncwarp();
 #pragma unroll
             for (int y = 0; y < NT; ++y)
 #pragma unroll
@@ -485,8 +525,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
         // Several warps with one head: added up in shared memory, each row by
         // the warps of its head in turn.
         if (sh.ways > 1) {
-            float* so = reinterpret_cast<float*>(smem + (planned ? (a.B + 1) * 8 + 8 : 0));
-            so = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(so) + 15) & ~uintptr_t(15));
+            float* so = reinterpret_cast<float*>(smem);  // (where the rings were)
             float2* sml = reinterpret_cast<float2*>(so + W * R * DP);
             __syncthreads();
             if (on && way > 0) {
@@ -529,6 +568,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
                 }
             }
         }
+        if (sh.ways > 1 && lo < hi) __syncthreads();  // before the rings fill again
         if (!on || way > 0) continue;
         if (whole) {
             const float vs = a.v_scale[hk * a.scale_stride];
@@ -572,11 +612,12 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
     }
 }
 
-// Adds up the parts of a request that several CTAs hold.  CTA (c, y): the
-// request in which CTA c begins, if c is the first one to begin inside it;
-// rows y, y + gridDim.y, ... of its heads.  Each of the warps sums every
-// kWarps-th part, then they are summed in their order.
-constexpr int kJoinWarps = 8;
+// Adds up the parts of the requests that several CTAs hold: the CTAs (x, ...)
+// do the request of cut x.  A row of few parts is a warp's; the parts of a
+// row that has many are dealt to the CTA's warps, whose sums are then added in
+// the warps' order.
+constexpr int kJoinWarps = 16;
+constexpr int kBatch = 4;  // parts in flight a warp
 template <int NT, int DP, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const DecodeArgs a) {
     constexpr int R = 8 * NT;
@@ -587,40 +628,67 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const D
     pdl_wait_primary();
     const Shape sh = shape_of<NT, W>(a.Hq, a.Hkv);
     const Parts parts = parts_of<NT, DP, W>(a.workspace, sh.heads);
-    const int c1 = blockIdx.x + 1;
-    const Cut cut = parts.cuts[c1];
-    if (cut.total == 0) return;              // CTA c1 begins with a request's first token
-    const int c0 = c1 - 1;
-    const int64_t c0_from = cut_at(cut.total, c0, cut.ctas);
-    if (c0_from > cut.first) return;         // an earlier CTA begins inside it too
-    const bool begins = c0_from == cut.first;  // else c0 has its part in slot 1
+    const Cut cut = parts.cuts[blockIdx.x];
+    if (cut.per == 0) return;
+    const int c0 = static_cast<int>(divide_up(cut.first + 1, cut.per) - 1);
+    const bool begins = cut.per * c0 == cut.first;  // else c0 has its part in slot 1
+    const int last = static_cast<int>(divide_up(cut.end, cut.per) - 1);
     const int G = a.Hq / a.Hkv, lane = lane_id(), warp = threadIdx.x >> 5;
-    int last = c1;
-    while (last + 1 < cut.ctas && cut_at(cut.total, last + 1, cut.ctas) < cut.end) ++last;
-    for (int y = blockIdx.y; y < sh.heads * R; y += gridDim.y) {
-        const int head = y / R, row = y - head * R;
-        const int hk = cut.group / sh.blocks * sh.heads + head;
-        const int r = cut.group % sh.blocks * R + row;
-        if (hk >= a.Hkv || r >= G) continue;
-        auto at = [&](int cta) {
-            const int slot = cta == c0 && !begins ? 1 : 0;
-            return ((static_cast<size_t>(cta) * 2 + slot) * sh.heads + head) * R + row;
-        };
+    const int r0 = cut.group % sh.blocks * R, h0 = cut.group / sh.blocks * sh.heads;
+    const int rows = min(R, G - r0), items = rows * min(sh.heads, a.Hkv - h0);
+    const bool few = last - c0 < 4 * kBatch;
+    const int step = few ? 1 : kJoinWarps, offset = few ? 0 : warp;
+    for (int y = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y; y < items;
+         y += few ? gridDim.y * kJoinWarps : gridDim.y) {
+        const int head = y / rows, row = y - head * rows;
         float m = -INFINITY, l = 0.0f, o[V] = {};
-        for (int cta = c0 + warp; cta <= last; cta += kJoinWarps) {
-            const size_t i = at(cta);
-            const float2 ml = parts.ml[i];
-            const float top = fmaxf(m, ml.x);
-            const float keep = m == -INFINITY ? 0.0f : ex2(m - top);
-            const float take = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
+        for (int cta = c0 + offset; cta <= last; cta += kBatch * step) {
+            float2 ml[kBatch];
+            float part[kBatch][V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = o[e] * keep + parts.o[i * DP + V * lane + e] * take;
-            l = l * keep + ml.y * take;
+            for (int i = 0; i < kBatch; ++i) {
+                const int from = cta + i * step;
+                ml[i] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) part[i][e] = 0.0f;
+                if (from <= last) {
+                    const int slot = from == c0 && !begins ? 1 : 0;
+                    const size_t at = ((static_cast<size_t>(from) * 2 + slot) * sh.heads + head) * R + row;
+                    ml[i] = parts.ml[at];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) part[i][e] = parts.o[at * DP + 32 * e + lane];
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+            const float keep = m == -INFINITY ? 0.0f : ex2(m - top);
             m = top;
+            l *= keep;
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] *= keep;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float take = ml[i].x == -INFINITY ? 0.0f : ex2(ml[i].x - top);
+                l += ml[i].y * take;
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] += part[i][e] * take;
+            }
+        }
+        const int hk = h0 + head;
+        const float vs = a.v_scale[hk * a.scale_stride];
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + cut.request * a.ldo +
+                             static_cast<int64_t>(hk * G + r0 + row) * a.D;
+        if (few) {
+            const float inv = l == 0.0f ? 0.0f : vs / l;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (32 * e + lane < a.D) dst[32 * e + lane] = __float2bfloat16_rn(o[e] * inv);
+            continue;
         }
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < V; ++e) s_o[warp][V * lane + e] = o[e];
+        for (int e = 0; e < V; ++e) s_o[warp][32 * e + lane] = o[e];
         if (lane == 0) s_ml[warp] = make_float2(m, l);
         __syncthreads();
         if (threadIdx.x < DP) {
@@ -632,20 +700,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const D
                 sum += s_o[w][threadIdx.x] * take;
                 all += s_ml[w].y * take;
             }
-            const float inv = all == 0.0f ? 0.0f : a.v_scale[hk * a.scale_stride] / all;
-            if (static_cast<int>(threadIdx.x) < a.D)
-                reinterpret_cast<__nv_bfloat16*>(a.out)[cut.request * a.ldo +
-                                                        static_cast<int64_t>(hk * G + r) * a.D + threadIdx.x] =
-                    __float2bfloat16_rn(sum * inv);
+            const float inv = all == 0.0f ? 0.0f : vs / all;
+            if (static_cast<int>(threadIdx.x) < a.D) dst[threadIdx.x] = __float2bfloat16_rn(sum * inv);
         }
     }
 }
 
-template <int NT, int DP, int W>
+template <int NT, int DP>
 struct Launch {
-    static size_t smem(int64_t B, int ways) {
-        const size_t plan = B <= kMaxPlan ? (B + 1) * 8 + 24 : 16;
-        return plan + (ways > 1 ? W * 8 * NT * (DP * 4 + 8) : 0);
+    static constexpr int W = kWarps;
+    static size_t smem(int64_t B) {
+        return W * Ring<DP>::kBytes + (B <= kMaxPlan ? (B + 1) * 8 : 0);
     }
     static size_t workspace(int64_t B, int Hq, int Hkv) {
         if (B > kMaxPlan) return 0;
@@ -654,7 +719,7 @@ struct Launch {
     }
     static cudaError_t prepare() {
         return cudaFuncSetAttribute(attention_decode<NT, DP, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(smem(kMaxPlan, 2)));
+                                    static_cast<int>(smem(kMaxPlan)));
     }
     static cudaError_t run(const DecodeArgs& a, cudaStream_t st) {
         const Shape s = shape_of<NT, W>(a.Hq, a.Hkv);
@@ -664,7 +729,7 @@ struct Launch {
         const int ctas = a.num_sms < kCtas ? a.num_sms : kCtas;
         cfg.gridDim = dim3(static_cast<unsigned>(ctas));
         cfg.blockDim = dim3(W * 32);
-        cfg.dynamicSmemBytes = smem(a.B, s.ways);
+        cfg.dynamicSmemBytes = smem(a.B);
         cfg.stream = st;
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -672,17 +737,22 @@ struct Launch {
         cfg.numAttrs = 1;
         cudaError_t e = cudaLaunchKernelEx(&cfg, attention_decode<NT, DP, W>, a, planned);
         if (e != cudaSuccess || !planned || ctas < 2) return e;
-        cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), a.B <= 8 ? s.heads * 8 * NT : s.heads);
+        // Few requests have many parts each: a CTA for every row.  Many have a
+        // few each, most of them, but one may still have almost all.
+        const int64_t cuts = a.B * s.groups <= kCtas ? a.B * s.groups : ctas;
+        const int64_t rows = s.heads * (a.Hq / a.Hkv < 8 * NT ? a.Hq / a.Hkv : 8 * NT);
+        const int64_t wide = cuts <= 16 ? rows : s.heads;
+        cfg.gridDim = dim3(static_cast<unsigned>(cuts), static_cast<unsigned>(wide));
         cfg.blockDim = dim3(kJoinWarps * 32);
         cfg.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&cfg, attention_decode_join<NT, DP, W>, a);
     }
 };
 
-using Narrow64 = Launch<1, 64, 16>;
-using Narrow128 = Launch<1, 128, 16>;
-using Wide64 = Launch<2, 64, 8>;
-using Wide128 = Launch<2, 128, 8>;
+using Narrow64 = Launch<1, 64>;
+using Narrow128 = Launch<1, 128>;
+using Wide64 = Launch<2, 64>;
+using Wide128 = Launch<2, 128>;
 
 }  // namespace
 
