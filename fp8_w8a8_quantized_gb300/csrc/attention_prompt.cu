@@ -14,19 +14,26 @@
 // 128 / G tokens with all their heads, keys and values are read once for the
 // group, and short prompts fill the tile.  A CTA works on two such tiles (A
 // and B) and walks over the keys in tiles of 128:
-//   warps 0-3, 4-7  softmax of tile A and B: a thread holds a row of S (128
-//                   fp32), writes P as bf16 over it, rescales O where needed
-//                   and finally writes the row's output;
-//   warp 8          TMA loads: Q once per item, K and V through a ring;
-//   warp 9          issues the MMAs: S = Q K^T (both from shared memory) and
-//                   O += P V (P from tensor memory);
-//   warp 10         looks for infinities and NaN in values that some row of
+//   warps 0-7, 8-15 softmax of tile A and B: a warp holds 16 rows of S, four
+//                   lanes a row, writes P as bf16 over S, rescales O where
+//                   needed and finally writes the rows' output.  (Four warps a
+//                   tile, a lane a row, took 1450 clocks a tile, mostly
+//                   latency; the tensor core waits for S -> P of one tile
+//                   once it is done with the other one's MMAs, 1024 clocks);
+//   warp 16         TMA loads: Q once per item, K and V through a ring;
+//   warp 17         issues the MMAs: S = Q K^T (both from shared memory) and
+//                   O += P V (P from tensor memory), tile A's and tile B's in
+//                   turn, so that one tile is in its softmax while the tensor
+//                   core has the other one (with an issuer for each tile they
+//                   fell into step and both waited).  P comes in two halves,
+//                   the MMAs of the first 64 keys start with the first;
+//   warp 18         looks for infinities and NaN in values that some row of
 //                   the item must not see (below).
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each: all 512.  While one tile is in
 // its softmax the tensor core works on the other one.
 //
 // A masked weight is 0, but 0 * inf is NaN: in tiles where some row masks some
-// key, warp 10 sets non-finite values to 0 in shared memory before the MMA
+// key, warp 18 sets non-finite values to 0 in shared memory before the MMA
 // reads them and remembers that it did; the rows that do see such a value get
 // it back, from global memory, when they write their output.
 #include <cuda.h>
@@ -46,17 +53,18 @@ constexpr float kSlack = 8.0f;  // log2 of how far p may exceed 1 before m moves
 constexpr int kRows = 128;      // rows of a query tile
 constexpr int kKeys = 128;      // keys of a tile
 constexpr int kStages = 5;
-constexpr int kThreads = 32 * 12;  // (warp 11 only fills up its warpgroup)
-constexpr int kMainRegs = 208, kSideRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168, the launch's
+constexpr int kMainWarps = 16;
+constexpr int kThreads = 32 * (kMainWarps + 4);
+constexpr int kMainRegs = 104, kSideRegs = 64;  // 512 x 104 + 128 x 64 = 640 x 96, the launch's
 constexpr int kClean = 4;       // (the ring holds two tiles of values at most)
 constexpr int kFlags = 4;       // items whose "values were set to 0" flag is kept
 
 struct Bars {
     uint64_t full[kStages], empty[kStages];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2];
     uint64_t v_issued[kClean];  // such a tile of values is on its way (its stage's phase is current)
-    uint64_t v_clean[kClean];   // warp 10 is done with it
+    uint64_t v_clean[kClean];   // warp 18 is done with it
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -82,6 +90,13 @@ struct Item {
 // numbered so that sequence b's begin at cu[b] / per + b (there is room for
 // all of them, with some numbers unused), the last block first, since it has
 // the most keys.
+//
+// CTAs take items in turn, every other round from the other end, so that
+// none gets the longer one each time.
+__device__ __forceinline__ int64_t turn_of(int64_t round) {
+    return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 __device__ __forceinline__ Item find_item(int64_t n, int64_t blocks, const PromptArgs& a, int tpt) {
     Item it;
     const int64_t i = blocks - 1 - n / a.Hkv;
@@ -145,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars->q_empty, 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bars->s_full[x], 1);
-            mbar_init(&bars->p_full[x], 4);
+            mbar_init(&bars->p_full[x][0], 8);
+            mbar_init(&bars->p_full[x][1], 8);
             mbar_init(&bars->o_full[x], 1);
         }
         for (int k = 0; k < kClean; ++k) {
@@ -157,12 +173,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int f = 0; f < kFlags; ++f) bars->dirty[f] = 0;
         fence_mbar_init();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == kMainWarps && lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    if (warp == 9) {
+    if (warp == kMainWarps + 1) {
         tmem_alloc(&bars->tmem_base, 512);
         tmem_relinquish();
     }
@@ -177,273 +193,329 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = a.Hq / a.Hkv, tpt = kRows / G;
     const int64_t items = blocks * a.Hkv;
 
-    if (warp < 8) {
+    if (warp < kMainWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMainRegs));
         // ------------------------------------------------ softmax and output
-        const int x = warp >> 2;                       // query tile A or B
-        const int row = (warp & 3) * 32 + lane;
-        const int tok = row / G, head_in = row - tok * G;
-        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane quarter << 16
+        const int x = warp >> 3, g = lane >> 2, t = lane & 3;  // query tile A or B
+        const int row0 = (warp & 3) * 32 + (warp >> 2 & 1) * 16 + g;  // this lane's rows: row0, row0 + 8
+        const uint32_t lanes = static_cast<uint32_t>(row0 - g) << 16;
         const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * 128;
         const float c = a.scale * kLog2e;
         uint32_t s_phase = 0, o_phase = 0;
         int item_no = 0;
         bool ok = true;
-        for (int64_t n = blockIdx.x; ok && n < items; n += gridDim.x) {
+        int tok[2], head_in[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            tok[e] = (row0 + 8 * e) / G;
+            head_in[e] = row0 + 8 * e - tok[e] * G;
+        }
+        for (int64_t r = 0; ok && r * gridDim.x < items; ++r) {
+            const int64_t n = turn_of(r);
+            if (n >= items) continue;
             const Item it = find_item(n, blocks, a, tpt);
             if (!it.valid) continue;
-            const int my_tok = it.q0 + x * tpt + tok;
-            const bool mine = tok < tpt && my_tok < it.len;
+            int my_tok[2];
+            bool mine[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                my_tok[e] = it.q0 + x * tpt + tok[e];
+                mine[e] = tok[e] < tpt && my_tok[e] < it.len;
+            }
             const int tiles = it.tiles[x];
-            float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+            const int first_tok = it.q0 + x * tpt;  // no row of the tile sees less than this
+            float m[2] = {-INFINITY, -INFINITY}, l[2][2] = {};
             for (int j = 0; j < tiles; ++j) {
                 if (!(ok = warp_wait(&bars->s_full[x], s_phase, abort_flag, status))) break;
                 s_phase ^= 1u;
                 tc_fence_after();
-                uint32_t s[4][32];
+                uint32_t s[4][16];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_ld_32x32b_x32(tS + 32 * b, s[b]);
+                for (int b = 0; b < 4; ++b) tmem_ld_16x256b_x4(tS + 32 * b, s[b]);
+                tmem_ld_wait();
 #pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_ld_wait_regs(s[b]);
-                const int seen = my_tok - j * kKeys;   // keys 0 .. seen of the tile are seen
-                if (seen < kKeys - 1) {
+                for (int b = 0; b < 4; ++b)
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
+                    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(s[b][i]));  // (not before the wait)
+                if (first_tok - j * kKeys < kKeys - 1) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * b + i > seen) s[b][i] = 0xFF800000u;  // -inf
+                    for (int e = 0; e < 2; ++e) {
+                        const int seen = my_tok[e] - j * kKeys - 2 * t;  // columns up to it, from 2 t on
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (32 * b + 8 * (i >> 1) + (i & 1) > seen)
+                                    s[b][4 * (i >> 1) + 2 * e + (i & 1)] = 0xFF800000u;  // -inf
+                    }
                 }
-                float top[4];
+                bool raise[2];
+                float top[2];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    top[b] = __uint_as_float(s[b][0]);
+                for (int e = 0; e < 2; ++e) {
+                    float part[4];
 #pragma unroll
-                    for (int i = 1; i < 32; ++i) top[b] = fmaxf(top[b], __uint_as_float(s[b][i]));
+                    for (int b = 0; b < 4; ++b) {
+                        part[b] = __uint_as_float(s[b][2 * e]);
+#pragma unroll
+                        for (int i = 1; i < 8; ++i)
+                            part[b] = fmaxf(part[b], __uint_as_float(s[b][4 * (i >> 1) + 2 * e + (i & 1)]));
+                    }
+                    top[e] = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
                 }
-                const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                // (m = -inf: the first keys that are seen set it)
-                const bool raise = mine && (tile_top - m) * c > kSlack;
-                if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1) {
+                    top[0] = fmaxf(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], d));
+                    top[1] = fmaxf(top[1], __shfl_xor_sync(0xFFFFFFFFu, top[1], d));
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)  // (m = -inf: the first keys that are seen set it)
+                    raise[e] = mine[e] && (top[e] - m[e]) * c > kSlack;
+                if (__any_sync(0xFFFFFFFFu, raise[0] || raise[1])) {
                     // (row by row, so that no row's digits depend on its neighbours)
-                    const float next = raise ? tile_top : m;
-                    const float keep = !raise ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - next) * c);
-                    m = next;
-                    l0 *= keep;
-                    l1 *= keep;
+                    float keep[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        keep[e] = !raise[e] ? 1.0f : m[e] == -INFINITY ? 0.0f : ex2((m[e] - top[e]) * c);
+                        m[e] = raise[e] ? top[e] : m[e];
+                        l[e][0] *= keep[e];
+                        l[e][1] *= keep[e];
+                    }
                     if (j > 0) {
                         // S of tile j came after P V of tile j - 1: O is at rest
+#pragma unroll 1
                         for (int b = 0; b < DP / 32; ++b) {
-                            uint32_t o[32];
-                            tmem_ld_32x32b_x32(tO + 32 * b, o);
-                            tmem_ld_wait_regs(o);
+                            uint32_t o[16];
+                            tmem_ld_16x256b_x4(tO + 32 * b, o);
+                            tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                            tmem_st_32x32b_x32(tO + 32 * b, o);
+                            for (int i = 0; i < 16; ++i) {
+                                asm volatile("" : "+r"(o[i]));
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * keep[i >> 1 & 1]);
+                            }
+                            tmem_st_16x256b_x4(tO + 32 * b, o);
                         }
                     }
                 }
-                const float base = m == -INFINITY ? 0.0f : -m * c;
+                const float base[2] = {m[0] == -INFINITY ? 0.0f : -m[0] * c,
+                                       m[1] == -INFINITY ? 0.0f : -m[1] * c};
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < 2; ++b) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float y0 = base, y1 = base;
-                        fma2(y0, y1, __uint_as_float(s[b][2 * i]), __uint_as_float(s[b][2 * i + 1]), c, c);
+                        // keys 64 b + 8 (i / 2) + 2 t, + 1 of row i & 1
+                        const int e = i & 1;
+                        const uint32_t* from = &s[2 * b + (i >> 3)][4 * (i >> 1 & 3) + 2 * e];
+                        float y0 = base[e], y1 = base[e];
+                        fma2(y0, y1, __uint_as_float(from[0]), __uint_as_float(from[1]), c, c);
                         y0 = ex2(y0);
                         y1 = ex2(y1);
-                        add2(l0, l1, y0, y1);
+                        add2(l[e][0], l[e][1], y0, y1);
                         p[i] = pack_bf16(y0, y1);
                     }
-                    tmem_st_32x32b_x16(tS + 16 * b, p);
+                    tmem_st_16x128b_x8(tS + 32 * b, p);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->p_full[x][b]);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_full[x]);
             }
             if (!ok) break;
             if (tiles > 0) {
                 if (!(ok = warp_wait(&bars->o_full[x], o_phase, abort_flag, status))) break;
                 o_phase ^= 1u;
                 tc_fence_after();
-                const float l = l0 + l1;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                const int64_t t = it.start + my_tok;
-                uint16_t* dst = a.out + t * a.ldo + static_cast<int64_t>(it.head * G + head_in) * a.D;
+                float inv[2];
+                uint16_t* dst[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float sum = l[e][0] + l[e][1];
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                    inv[e] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    dst[e] = a.out + (it.start + my_tok[e]) * a.ldo +
+                             static_cast<int64_t>(it.head * G + head_in[e]) * a.D + 2 * t;
+                }
                 const bool dirty = *reinterpret_cast<volatile int*>(&bars->dirty[item_no % kFlags]) != 0;
 #pragma unroll 1
                 for (int b = 0; b < DP / 32; ++b) {
-                    uint32_t o[32];
+                    uint32_t o[16];
                     __syncwarp();
-                    tmem_ld_32x32b_x32(tO + 32 * b, o);
-                    tmem_ld_wait_regs(o);
-                    if (!mine) continue;
-                    float f[32];
+                    tmem_ld_16x256b_x4(tO + 32 * b, o);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
-                    if (dirty) {
-                        for (int j = it.masked * kKeys; j <= my_tok; ++j) {
-                            const uint16_t* v = a.v + (it.start + j) * a.ldv +
-                                                static_cast<int64_t>(it.head) * a.D + 32 * b;
+                    for (int i = 0; i < 16; ++i) {
+                        asm volatile("" : "+r"(o[i]));
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * inv[i >> 1 & 1]);
+                    }
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                if (32 * b + i < a.D) {
-                                    const float e = __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
-                                    if (!isfinite(e)) f[i] += e;
+                    for (int e = 0; e < 2; ++e) {
+                        if (!mine[e]) continue;
+                        if (dirty) {
+                            for (int j = it.masked * kKeys; j <= my_tok[e]; ++j) {
+                                const uint16_t* v = a.v + (it.start + j) * a.ldv +
+                                                    static_cast<int64_t>(it.head) * a.D + 32 * b + 2 * t;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int d = 8 * (i >> 1) + (i & 1);
+                                    if (32 * b + 2 * t + d < a.D) {
+                                        const float z = __uint_as_float(static_cast<uint32_t>(v[d]) << 16);
+                                        uint32_t& to = o[4 * (i >> 1) + 2 * e + (i & 1)];
+                                        if (!isfinite(z)) to = __float_as_uint(__uint_as_float(to) + z);
+                                    }
                                 }
                             }
                         }
-                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (32 * b + 8 * i < a.D)
-                            *reinterpret_cast<uint4*>(dst + 32 * b + 8 * i) = make_uint4(
-                                pack_bf16(f[8 * i], f[8 * i + 1]), pack_bf16(f[8 * i + 2], f[8 * i + 3]),
-                                pack_bf16(f[8 * i + 4], f[8 * i + 5]), pack_bf16(f[8 * i + 6], f[8 * i + 7]));
+                        for (int i = 0; i < 4; ++i)
+                            if (32 * b + 8 * i < a.D)
+                                *reinterpret_cast<uint32_t*>(dst[e] + 32 * b + 8 * i) =
+                                    pack_bf16(__uint_as_float(o[4 * i + 2 * e]), __uint_as_float(o[4 * i + 2 * e + 1]));
                     }
                 }
+                __syncwarp();
             }
             ++item_no;
         }
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
-      if (warp == 8) {
+      if (warp == kMainWarps) {
         // ------------------------------------------------ TMA loads
-        uint32_t stage = 0, phase = 0, q_phase = 0;
-        uint32_t loads = 0, issued = 0;
+        uint32_t loads = 0, issued = 0, q_loads = 0;
         bool ok = true;
         auto tile = [&](const CUtensorMap* tm, int head, int tokens) {
-            if (!(ok = warp_wait(&bars->empty[stage], phase ^ 1u, abort_flag, status))) return;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars->full[stage], kTile);
-                for (int x = 0; x < kCols; ++x)
-                    tma_load_3d(sKV + stage * kTile + x * kColBytes, tm, &bars->full[stage], 64 * x,
-                                head, tokens);
-            }
-            __syncwarp();
+            const uint32_t stage = loads % kStages;
+            if (!wait_bounded(&bars->empty[stage], (loads / kStages & 1u) ^ 1u, abort_flag, status))
+                return false;
+            mbar_arrive_expect_tx(&bars->full[stage], kTile);
+            for (int y = 0; y < kCols; ++y)
+                tma_load_3d(sKV + stage * kTile + y * kColBytes, tm, &bars->full[stage], 64 * y, head,
+                            tokens);
             ++loads;
-            if (++stage == kStages) stage = 0, phase ^= 1u;
+            return true;
         };
-        for (int64_t n = blockIdx.x; ok && n < items; n += gridDim.x) {
-            const Item it = find_item(n, blocks, a, tpt);
-            if (!it.valid) continue;
-            if (!(ok = warp_wait(&bars->q_empty, q_phase ^ 1u, abort_flag, status))) break;
-            q_phase ^= 1u;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars->q_full, 2u * kCols * 128u * static_cast<uint32_t>(G * tpt));
-                for (int x = 0; x < 2; ++x)
-                    for (int y = 0; y < kCols; ++y)
-                        tma_load_3d(sQ + x * kTile + y * kColBytes, &tmQ, &bars->q_full, 64 * y,
-                                    it.head * G, it.start + it.q0 + x * tpt);
-            }
-            __syncwarp();
+        auto load_item = [&](const Item& it) {
+            if (!wait_bounded(&bars->q_empty, (q_loads & 1u) ^ 1u, abort_flag, status)) return false;
+            mbar_arrive_expect_tx(&bars->q_full, 2u * kCols * 128u * static_cast<uint32_t>(G * tpt));
+            for (int x = 0; x < 2; ++x)
+                for (int y = 0; y < kCols; ++y)
+                    tma_load_3d(sQ + x * kTile + y * kColBytes, &tmQ, &bars->q_full, 64 * y, it.head * G,
+                                it.start + it.q0 + x * tpt);
+            ++q_loads;
             const int tiles = max(it.tiles[0], it.tiles[1]);
-            for (int j = 0; ok && j < tiles; ++j) {
-                tile(&tmK, it.head, it.start + j * kKeys);
-                if (ok) tile(&tmV, it.head, it.start + j * kKeys);
-                if (ok && j >= it.masked) {
-                    if (lane == 0) mbar_arrive(&bars->v_issued[issued % kClean]);
+            for (int j = 0; j < tiles; ++j) {
+                if (!tile(&tmK, it.head, it.start + j * kKeys)) return false;
+                if (!tile(&tmV, it.head, it.start + j * kKeys)) return false;
+                if (j >= it.masked) {
+                    mbar_arrive(&bars->v_issued[issued % kClean]);
                     ++issued;
                 }
             }
+            return true;
+        };
+        for (int64_t r = 0; ok && r * gridDim.x < items; ++r) {
+            const int64_t n = turn_of(r);
+            if (n >= items) continue;
+            const Item it = find_item(n, blocks, a, tpt);
+            if (!it.valid) continue;
+            if (lane == 0) ok = load_item(it);
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
-        if (!ok) {  // gave up: let the copies in flight land before the memory goes
-            const uint32_t back = loads < kStages ? loads : kStages;
-            for (uint32_t i = 0; i < back; ++i) {
-                const uint32_t k = loads - 1 - i;
-                if (lane == 0) wait_landed(&bars->full[k % kStages], (k / kStages) & 1u, status);
+        if (!ok && lane == 0) {  // gave up: let the copies in flight land before the memory goes
+            for (uint32_t i = 1; i <= kStages && i <= loads; ++i) {
+                const uint32_t k = loads - i;
+                wait_landed(&bars->full[k % kStages], k / kStages & 1u, status);
             }
-            if (lane == 0 && q_phase) wait_landed(&bars->q_full, q_phase ^ 1u, status);
-            __syncwarp();
+            if (q_loads) wait_landed(&bars->q_full, (q_loads - 1) & 1u, status);
         }
-      } else if (warp == 9) {
+        __syncwarp();
+      } else if (warp == kMainWarps + 1) {
         // ------------------------------------------------ MMA
         constexpr uint32_t idS = idesc_f16(kRows, kKeys, true, false);
         constexpr uint32_t idO = idesc_f16(kRows, DP, true, true);
+        const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(sQ));
+        const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(sKV));
+        const uint64_t v_desc = sdesc_nmajor_sw128(smem_u32(sKV), kColBytes);
         uint32_t at = 0;  // stages consumed so far
         uint32_t q_phase = 0, p_phase[2] = {0, 0}, cleaned = 0;
         bool ok = true;
         auto landed = [&](uint32_t k) {
-            ok = ok && warp_wait(&bars->full[k % kStages], (k / kStages) & 1u, abort_flag, status);
-            return ok;
+            return wait_bounded(&bars->full[k % kStages], k / kStages & 1u, abort_flag, status);
         };
-        auto mma_s = [&](int x, uint32_t k) {
-            if (lane == 0) {
-                const uint64_t q = sdesc_kmajor_sw128(smem_u32(sQ + x * kTile));
-                const uint64_t kd = sdesc_kmajor_sw128(smem_u32(sKV + (k % kStages) * kTile));
-#pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
-                    const uint32_t off = ((i / 4) * kColBytes + (i % 4) * 32) >> 4;
-                    mma_f16(tmem + x * 128, q + off, kd + off, idS, i != 0);
-                }
-                mma_commit(&bars->s_full[x]);
-            }
-            __syncwarp();
-        };
-        auto mma_o = [&](int x, uint32_t k, bool first) {
-            if (lane == 0) {
-                const uint64_t vd = sdesc_nmajor_sw128(smem_u32(sKV + (k % kStages) * kTile), kColBytes);
-#pragma unroll
-                for (int i = 0; i < kKeys / 16; ++i)
-                    mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * i, vd + i * (2048 >> 4), idO,
-                               !(first && i == 0));
-            }
-            __syncwarp();
-        };
-        for (int64_t n = blockIdx.x; ok && n < items; n += gridDim.x) {
-            const Item it = find_item(n, blocks, a, tpt);
-            if (!it.valid) continue;
+        auto run_item = [&](const Item& it) {
             const int tiles = max(it.tiles[0], it.tiles[1]);
-            if (!(ok = warp_wait(&bars->q_full, q_phase, abort_flag, status))) break;
+            if (!wait_bounded(&bars->q_full, q_phase, abort_flag, status)) return false;
             q_phase ^= 1u;
-            for (int j = 0; j <= tiles && ok; ++j) {
-                const uint32_t kk = at + 2 * j, vv = at + 2 * j - 1;  // K of tile j, V of tile j - 1
-                const bool more = j < tiles;
-                if (more && !landed(kk)) break;
-                if (j > 0) {
-                    if (!landed(vv)) break;
-                    if (j - 1 >= it.masked) {
-                        if (!(ok = warp_wait(&bars->v_clean[cleaned % kClean], (cleaned / kClean) & 1u,
-                                             abort_flag, status)))
-                            break;
+            if (!landed(at)) return false;
+            for (int j = 0; j <= tiles; ++j) {
+                // P V of tile j - 1 and S of tile j; what they read has landed
+                const uint32_t kk = (at + 2 * j) % kStages, vv = (at + 2 * j + kStages - 1) % kStages;
+                const uint64_t kd = k_desc + kk * (kTile >> 4), vd = v_desc + vv * (kTile >> 4);
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
+                    if (j > 0 && j - 1 < it.tiles[x]) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!wait_bounded(&bars->p_full[x][h], p_phase[x], abort_flag, status)) return false;
+                            tc_fence_after();
+#pragma unroll
+                            for (int i = 4 * h; i < 4 * h + 4; ++i)
+                                mma_f16_ts(tO, tS + 8 * i, vd + i * (2048 >> 4), idO, !(j == 1 && i == 0));
+                        }
+                        p_phase[x] ^= 1u;
+                        if (j == it.tiles[x]) mma_commit(&bars->o_full[x]);
+                    }
+                    if (j < it.tiles[x]) {
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i) {
+                            const uint32_t off = ((i / 4) * kColBytes + (i % 4) * 32) >> 4;
+                            mma_f16(tS, q_desc + x * (kTile >> 4) + off, kd + off, idS, i != 0);
+                        }
+                        mma_commit(&bars->s_full[x]);
+                    }
+                }
+                if (j > 0) mma_commit(&bars->empty[vv]);
+                if (j < tiles) mma_commit(&bars->empty[kk]);
+                if (j + 1 == tiles) mma_commit(&bars->q_empty);
+                // (these are there by now, as a rule: no time lost between P and its MMAs)
+                if (j + 1 < tiles && !landed(at + 2 * j + 2)) return false;
+                if (j < tiles) {
+                    if (!landed(at + 2 * j + 1)) return false;
+                    if (j >= it.masked) {
+                        if (!wait_bounded(&bars->v_clean[cleaned % kClean], cleaned / kClean & 1u, abort_flag,
+                                          status))
+                            return false;
                         ++cleaned;
                     }
                 }
-                tc_fence_after();
-                for (int x = 0; x < 2; ++x) {
-                    if (j > 0 && j - 1 < it.tiles[x]) {
-                        if (!(ok = warp_wait(&bars->p_full[x], p_phase[x], abort_flag, status))) break;
-                        p_phase[x] ^= 1u;
-                        tc_fence_after();
-                        mma_o(x, vv, j == 1);
-                        if (j == it.tiles[x] && lane == 0) mma_commit(&bars->o_full[x]);
-                        __syncwarp();
-                    }
-                    if (j < it.tiles[x]) mma_s(x, kk);
-                }
-                if (!ok) break;
-                if (lane == 0) {
-                    if (j > 0) mma_commit(&bars->empty[vv % kStages]);
-                    if (more) mma_commit(&bars->empty[kk % kStages]);
-                    if (j + 1 == tiles) mma_commit(&bars->q_empty);
-                }
-                __syncwarp();
             }
             at += 2 * tiles;
+            return true;
+        };
+        for (int64_t r = 0; ok && r * gridDim.x < items; ++r) {
+            const int64_t n = turn_of(r);
+            if (n >= items) continue;
+            const Item it = find_item(n, blocks, a, tpt);
+            if (!it.valid) continue;
+            if (lane == 0) ok = run_item(it);
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
         if (lane == 0) {
             mma_commit(&bars->drain);
             wait_drain(&bars->drain, status);
         }
         __syncwarp();
-      } else if (warp == 10) {
+      } else if (warp == kMainWarps + 2) {
         // ------------------------------------------------ values that some row masks
         uint32_t at = 0, cleaned = 0;
         int item_no = 0;
         bool ok = true;
-        for (int64_t n = blockIdx.x; ok && n < items; n += gridDim.x) {
+        for (int64_t r = 0; ok && r * gridDim.x < items; ++r) {
+            const int64_t n = turn_of(r);
+            if (n >= items) continue;
             const Item it = find_item(n, blocks, a, tpt);
             if (!it.valid) continue;
             const int tiles = max(it.tiles[0], it.tiles[1]);
@@ -486,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kMainWarps + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
