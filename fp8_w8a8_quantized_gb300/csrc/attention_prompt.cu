@@ -434,76 +434,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ MMA
         constexpr uint32_t idS = idesc_f16(kRows, kKeys, true, false);
         constexpr uint32_t idO = idesc_f16(kRows, DP, true, true);
-        const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(sQ));
-        const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(sKV));
-        const uint64_t v_desc = sdesc_nmajor_sw128(smem_u32(sKV), kColBytes);
+        // (the warp stays converged and every operand of an MMA is uniform: see elect_one)
+        const uint32_t tm = uniform(tmem);
+        const uint32_t base_q = uniform(smem_u32(sQ)), base_kv = uniform(smem_u32(sKV));
         uint32_t at = 0;  // stages consumed so far
         uint32_t q_phase = 0, p_phase[2] = {0, 0}, cleaned = 0;
         bool ok = true;
-        auto landed = [&](uint32_t k) {
-            return wait_bounded(&bars->full[k % kStages], k / kStages & 1u, abort_flag, status);
+        auto ready = [&](uint64_t* bar, uint32_t parity) {
+            return warp_ready(bar, parity & 1u, abort_flag, status);
         };
-        auto run_item = [&](const Item& it) {
-            const int tiles = max(it.tiles[0], it.tiles[1]);
-            if (!wait_bounded(&bars->q_full, q_phase, abort_flag, status)) return false;
-            q_phase ^= 1u;
-            if (!landed(at)) return false;
-            for (int j = 0; j <= tiles; ++j) {
-                // P V of tile j - 1 and S of tile j; what they read has landed
-                const uint32_t kk = (at + 2 * j) % kStages, vv = (at + 2 * j + kStages - 1) % kStages;
-                const uint64_t kd = k_desc + kk * (kTile >> 4), vd = v_desc + vv * (kTile >> 4);
-                tc_fence_after();
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
-                    if (j > 0 && j - 1 < it.tiles[x]) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!wait_bounded(&bars->p_full[x][h], p_phase[x], abort_flag, status)) return false;
-                            tc_fence_after();
-#pragma unroll
-                            for (int i = 4 * h; i < 4 * h + 4; ++i)
-                                mma_f16_ts(tO, tS + 8 * i, vd + i * (2048 >> 4), idO, !(j == 1 && i == 0));
-                        }
-                        p_phase[x] ^= 1u;
-                        if (j == it.tiles[x]) mma_commit(&bars->o_full[x]);
-                    }
-                    if (j < it.tiles[x]) {
-#pragma unroll
-                        for (int i = 0; i < DP / 16; ++i) {
-                            const uint32_t off = ((i / 4) * kColBytes + (i % 4) * 32) >> 4;
-                            mma_f16(tS, q_desc + x * (kTile >> 4) + off, kd + off, idS, i != 0);
-                        }
-                        mma_commit(&bars->s_full[x]);
-                    }
-                }
-                if (j > 0) mma_commit(&bars->empty[vv]);
-                if (j < tiles) mma_commit(&bars->empty[kk]);
-                if (j + 1 == tiles) mma_commit(&bars->q_empty);
-                // (these are there by now, as a rule: no time lost between P and its MMAs)
-                if (j + 1 < tiles && !landed(at + 2 * j + 2)) return false;
-                if (j < tiles) {
-                    if (!landed(at + 2 * j + 1)) return false;
-                    if (j >= it.masked) {
-                        if (!wait_bounded(&bars->v_clean[cleaned % kClean], cleaned / kClean & 1u, abort_flag,
-                                          status))
-                            return false;
-                        ++cleaned;
-                    }
-                }
-            }
-            at += 2 * tiles;
-            return true;
-        };
+        auto landed = [&](uint32_t k) { return ready(&bars->full[k % kStages], k / kStages); };
         for (int64_t r = 0; ok && r * gridDim.x < items; ++r) {
             const int64_t n = turn_of(r);
             if (n >= items) continue;
             const Item it = find_item(n, blocks, a, tpt);
             if (!it.valid) continue;
-            if (lane == 0) ok = run_item(it);
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            const int tiles_a = uniform(it.tiles[0]), tiles_b = uniform(it.tiles[1]);
+            const int tiles = max(tiles_a, tiles_b), masked = uniform(it.masked);
+            if (!(ok = ready(&bars->q_full, q_phase) && landed(at))) break;
+            q_phase ^= 1u;
+            for (int j = 0; j <= tiles; ++j) {
+                // P V of tile j - 1 and S of tile j; what they read has landed
+                const uint32_t kk = (at + 2 * j) % kStages, vv = (at + 2 * j + kStages - 1) % kStages;
+                const uint64_t kd = sdesc_kmajor_sw128(base_kv + uniform(kk) * kTile);
+                const uint64_t vd = sdesc_nmajor_sw128(base_kv + uniform(vv) * kTile, kColBytes);
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t tS = tm + x * 128, tO = tm + 256 + x * 128;
+                    const uint64_t qd = sdesc_kmajor_sw128(base_q + x * kTile);
+                    const int mine = x == 0 ? tiles_a : tiles_b;
+                    if (j > 0 && j - 1 < mine) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!(ok = ready(&bars->p_full[x][h], p_phase[x]))) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 4 * h; i < 4 * h + 4; ++i)
+                                    mma_f16_ts(tO, tS + 8 * i, vd + i * (2048 >> 4), idO, !(j == 1 && i == 0));
+                                if (h == 1 && j == mine) mma_commit(&bars->o_full[x]);
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        p_phase[x] ^= 1u;
+                    }
+                    if (j < mine) {
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = 0; i < DP / 16; ++i) {
+                                const uint32_t off = ((i / 4) * kColBytes + (i % 4) * 32) >> 4;
+                                mma_f16(tS, qd + off, kd + off, idS, i != 0);
+                            }
+                            mma_commit(&bars->s_full[x]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    if (j > 0) mma_commit(&bars->empty[vv]);
+                    if (j < tiles) mma_commit(&bars->empty[kk]);
+                    if (j + 1 == tiles) mma_commit(&bars->q_empty);
+                }
+                __syncwarp();
+                // (these are there by now, as a rule: no time lost between P and its MMAs)
+                if (j + 1 < tiles && !(ok = landed(at + 2 * j + 2))) break;
+                if (j < tiles) {
+                    if (!(ok = landed(at + 2 * j + 1))) break;
+                    if (j >= masked) {
+                        if (!(ok = ready(&bars->v_clean[cleaned % kClean], cleaned / kClean))) break;
+                        ++cleaned;
+                    }
+                }
+            }
+            at += 2 * tiles;
         }
-        if (lane == 0) {
+        __syncwarp();
+        if (elect_one()) {  // (the lane that issued the MMAs)
             mma_commit(&bars->drain);
             wait_drain(&bars->drain, status);
         }
