@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int first_tok = it.q0 + x * tpt;  // no row of the tile sees less than this
             float m[2] = {-INFINITY, -INFINITY}, l[2][2] = {};
             for (int j = 0; j < tiles; ++j) {
-                if (!(ok = warp_wait(&bars->s_full[x], s_phase, abort_flag, status))) break;
+                if (!(ok = warp_ready(&bars->s_full[x], s_phase, abort_flag, status))) break;
                 s_phase ^= 1u;
                 tc_fence_after();
                 uint32_t s[4][16];
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             if (tiles > 0) {
-                if (!(ok = warp_wait(&bars->o_full[x], o_phase, abort_flag, status))) break;
+                if (!(ok = warp_ready(&bars->o_full[x], o_phase, abort_flag, status))) break;
                 o_phase ^= 1u;
                 tc_fence_after();
                 float inv[2];
@@ -491,6 +491,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         __syncwarp();
                     }
+                    if (x == 1) break;
+                    // What the next turn reads is there by now, as a rule; a look takes some 100
+                    // clocks all the same, which pass while the tensor core is busy with tile A.
+                    if (j + 1 < tiles && !(ok = landed(at + 2 * j + 2))) break;
+                    if (j < tiles) {
+                        if (!(ok = landed(at + 2 * j + 1))) break;
+                        if (j >= masked) {
+                            if (!(ok = ready(&bars->v_clean[cleaned % kClean], cleaned / kClean))) break;
+                            ++cleaned;
+                        }
+                    }
                 }
                 if (!ok) break;
                 if (elect_one()) {
@@ -499,15 +510,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 1 == tiles) mma_commit(&bars->q_empty);
                 }
                 __syncwarp();
-                // (these are there by now, as a rule: no time lost between P and its MMAs)
-                if (j + 1 < tiles && !(ok = landed(at + 2 * j + 2))) break;
-                if (j < tiles) {
-                    if (!(ok = landed(at + 2 * j + 1))) break;
-                    if (j >= masked) {
-                        if (!(ok = ready(&bars->v_clean[cleaned % kClean], cleaned / kClean))) break;
-                        ++cleaned;
-                    }
-                }
             }
             at += 2 * tiles;
         }
@@ -531,9 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool dirty = false;
             for (int j = it.masked; j < tiles; ++j) {
                 const uint32_t k = at + 2 * j + 1;
-                if (!(ok = warp_wait(&bars->v_issued[cleaned % kClean], (cleaned / kClean) & 1u,
+                if (!(ok = warp_ready(&bars->v_issued[cleaned % kClean], (cleaned / kClean) & 1u,
                                      abort_flag, status)) ||
-                    !(ok = warp_wait(&bars->full[k % kStages], (k / kStages) & 1u, abort_flag, status)))
+                    !(ok = warp_ready(&bars->full[k % kStages], (k / kStages) & 1u, abort_flag, status)))
                     break;
                 uint4* v = reinterpret_cast<uint4*>(sKV + (k % kStages) * kTile);
                 uint32_t found = 0;
