@@ -24,8 +24,9 @@ LIB_NAME = "libfp8w8a8.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "quant.cu", "quant_variants.cu", "norm_quant.cu", "gemm_pair.cu", "gemm_decode.cu", "gemm_blockwise.cu", "noalloc.cu",
-           "selftest.cu", "attention_api.cu", "kv_slots.cu", "norm_rope.cu", "attention_prompt.cu", "attention_decode.cu"]
-HEADERS = ["ptx.cuh", "launch.h", "quant_math.cuh", "decode_common.cuh"]
+           "selftest.cu", "attention_api.cu", "kv_slots.cu", "norm_rope.cu", "attention_prompt.cu", "attention_decode.cu",
+           "attention_prefix.cu"]
+HEADERS = ["ptx.cuh", "launch.h", "quant_math.cuh", "decode_common.cuh", "attention_tile.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

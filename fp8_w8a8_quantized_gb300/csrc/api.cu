@@ -59,7 +59,8 @@ fp8_status_t current_device(DeviceState** out) {
                    fp8k::prepare_gemm_blockwise() != cudaSuccess ||
                    fp8k::prepare_gemm_pair() != cudaSuccess ||
                    fp8k::prepare_attention_prompt() != cudaSuccess ||
-                   fp8k::prepare_attention_decode() != cudaSuccess) {
+                   fp8k::prepare_attention_decode() != cudaSuccess ||
+                   fp8k::prepare_attention_prefix() != cudaSuccess) {
             d.verdict = FP8_ERR_CUDA;
         } else {
             d.pair_clusters = fp8k::gemm_pair_resident_clusters(d.num_sms);

@@ -1,6 +1,6 @@
 // C-ABI entry points of the attention block (fp8w8a8.h): host-side argument
 // checks and the launches of kv_slots.cu, norm_rope.cu, attention_prompt.cu and
-// attention_decode.cu.
+// attention_decode.cu (with attention_prefix.cu).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -173,7 +173,7 @@ size_t fp8_attention_decode_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, i
         table_width > kMax31 / page_size || prefix_len > table_width * page_size ||
         check_heads(Hq, Hkv, D, 1.0f) != FP8_OK || B * Hkv >= (int64_t(1) << 24) || B == 0)
         return 0;
-    return fp8k::attention_decode_workspace(B, Hq, Hkv, D, table_width * page_size, prefix_len);
+    return fp8k::attention_decode_workspace(B, Hq, Hkv, D, prefix_len);
 }
 
 fp8_status_t fp8_attention_decode(const void* q, int64_t ldq, int64_t B, int64_t Hq, int64_t Hkv,
@@ -202,8 +202,7 @@ fp8_status_t fp8_attention_decode(const void* q, int64_t ldq, int64_t B, int64_t
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
         !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
         return FP8_ERR_UNSUPPORTED;
-    const size_t need = fp8k::attention_decode_workspace(B, Hq, Hkv, D, table_width * page_size,
-                                                         prefix_len);
+    const size_t need = fp8k::attention_decode_workspace(B, Hq, Hkv, D, prefix_len);
     if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
         return FP8_ERR_WORKSPACE;
     fp8k::DecodeArgs a;

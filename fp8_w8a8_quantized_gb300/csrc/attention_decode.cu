@@ -35,6 +35,7 @@
 #include <cstdint>
 #include <initializer_list>
 
+#include "attention_tile.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 #include "quant_math.cuh"
@@ -42,8 +43,6 @@
 namespace fp8k {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;       // log2 of how far p may exceed 1 before m moves
 constexpr int kTile = 32;            // tokens of a warp's step
 constexpr int kWarps = 8;            // warps of a CTA
 constexpr int kCtas = 152;           // CTAs at most (one per SM)
@@ -86,34 +85,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-
-// Two E4M3 codes (low or high half of u) -> two f16 values, exact.
-__device__ __forceinline__ uint32_t f16_lo(uint32_t u) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
-        : "=r"(r)
-        : "r"(u));
-    return r;
-}
-__device__ __forceinline__ uint32_t f16_hi(uint32_t u) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
-        : "=r"(r)
-        : "r"(u));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 2^n, for n beyond fp32's exponents too (as two factors).
-__device__ __forceinline__ float scaled(float x, int n) {
-    const int h = n / 2;
-    return x * __uint_as_float(static_cast<uint32_t>(127 + h) << 23) *
-           __uint_as_float(static_cast<uint32_t>(127 + n - h) << 23);
 }
 
 // 16 bytes into shared memory: an asynchronous copy, or zeros at once where
@@ -208,9 +179,10 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
     const int G = a.Hq / a.Hkv;
     const int64_t room = a.width * a.page;
     const int step = kTile * sh.ways;
+    // (tokens before `skip` are the prefix kernel's)
     auto length = [&](int64_t b) {
-        const int64_t n = a.lens[b];
-        return n < 0 ? int64_t(0) : n < room ? n : room;
+        const int64_t n = a.lens[b] < room ? a.lens[b] : room;
+        return n > a.skip ? n - a.skip : int64_t(0);
     };
 
     // the line of work
@@ -310,6 +282,41 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
             l[x][0] = l[x][1] = 0.0f;
         }
         if (on) {
+            if (a.splits > 0 && u0 == 0 && way == 0) {
+                // what the prefix kernel has of this request, one part after the other
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = r0 + 8 * x + 2 * t + e;
+                        if (row >= G) continue;
+                        const int64_t stride = static_cast<int64_t>(a.Hkv) * a.B * G;
+                        const int64_t at = static_cast<int64_t>(hk) * a.B * G + b * G + row;
+                        const float2* ml = a.part_ml + at;
+                        const float* src = a.part_o + at * DP + DP / 8 * g;
+                        float top = -INFINITY, sum = 0.0f;
+#pragma unroll 8
+                        for (int i = 0; i < a.splits; ++i) top = fmaxf(top, ml[i * stride].x);
+                        // (the loads of several parts on their way: nothing here waits for the part before)
+#pragma unroll 4
+                        for (int i = 0; i < a.splits; ++i) {
+                            const float2 part = ml[i * stride];
+                            const float take = part.x == -INFINITY ? 0.0f : ex2(part.x - top);
+                            sum += part.y * take;
+                            const float4* from = reinterpret_cast<const float4*>(src + i * stride * DP);
+#pragma unroll
+                            for (int y = 0; y < MT / 2; ++y) {
+                                const float4 v = from[y];
+                                o[2 * y][x][e] += v.x * take;
+                                o[2 * y][x][e + 2] += v.y * take;
+                                o[2 * y + 1][x][e] += v.z * take;
+                                o[2 * y + 1][x][e + 2] += v.w * take;
+                            }
+                        }
+                        m[x][e] = top;
+                        l[x][e] = g == 0 ? sum : 0.0f;  // (summed over the lanes in the end)
+                    }
+            }
             const int64_t row_bytes = static_cast<int64_t>(a.Hkv) * a.D;
             const uint8_t* kc = a.k_cache + static_cast<int64_t>(hk) * a.D;
             const uint8_t* vc = a.v_cache + static_cast<int64_t>(hk) * a.D;
@@ -317,8 +324,8 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
             const unsigned page = static_cast<unsigned>(a.page);
             // the slot of a lane's token of a step; -1 where there is none
             auto slot_of = [&](int64_t u) {
-                const int64_t tok = (u * sh.ways + way) * kTile + lane;
-                if (u >= u1 || tok >= len) return -1;
+                const int64_t tok = a.skip + (u * sh.ways + way) * kTile + lane;
+                if (u >= u1 || tok - a.skip >= len) return -1;
                 const unsigned pg = static_cast<unsigned>(tok) / page;
                 const int id = __ldg((tok < a.prefix ? a.table : own_row) + pg);
                 if (id < 0 || id >= a.n_pages) return -1;
@@ -365,18 +372,11 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
                         u[j][0] = src[0];
                         u[j][1] = src[1];
                     }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t w[4] = {u[j][e].x, u[j][e].y, u[j][e].z, u[j][e].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-                    }
+                    top = top_of(u[j][1], top_of(u[j][0], top));
                 }
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                // the largest element goes to [2^14, 2^15)
-                const int ex = top == 0 ? 14 : max(static_cast<int>(top >> 7), 1) - 127;
+                const int shift = query_shift(top);
 #pragma unroll
                 for (int j = 0; j < DP / 64; ++j)
 #pragma unroll
@@ -385,12 +385,12 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             // elements 8 e + 2 i, + 1 of the 16: step 4 j + (4 e + i) / 2
-                            const uint32_t h = pack_f16(scaled(bf16lo(w[i]), 14 - ex),
-                                                        scaled(bf16hi(w[i]), 14 - ex));
+                            const uint32_t h = pack_f16(scaled(bf16lo(w[i]), shift),
+                                                        scaled(bf16hi(w[i]), shift));
                             q[x][4 * j + (4 * e + i) / 2][i & 1] = h;
                         }
                     }
-                const float mine = scaled(unit, ex - 14);
+                const float mine = scaled(unit, -shift);
                 c[x][0] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t);
                 c[x][1] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t + 4);
             }
@@ -756,13 +756,28 @@ using Wide128 = Launch<2, 128>;
 
 }  // namespace
 
-size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t, int64_t) {
+size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix) {
     const int q = static_cast<int>(Hq), kv = static_cast<int>(Hkv);
-    if (Hq / Hkv <= 8) return D <= 64 ? Narrow64::workspace(B, q, kv) : Narrow128::workspace(B, q, kv);
-    return D <= 64 ? Wide64::workspace(B, q, kv) : Wide128::workspace(B, q, kv);
+    const size_t own = Hq / Hkv <= 8
+                           ? (D <= 64 ? Narrow64::workspace(B, q, kv) : Narrow128::workspace(B, q, kv))
+                           : (D <= 64 ? Wide64::workspace(B, q, kv) : Wide128::workspace(B, q, kv));
+    const PrefixPlan p = prefix_plan(B, Hq, Hkv, D, prefix);
+    return (own + 255) / 256 * 256 + p.parts_bytes();
 }
 
-cudaError_t launch_attention_decode(const DecodeArgs& a, cudaStream_t st) {
+cudaError_t launch_attention_decode(const DecodeArgs& given, cudaStream_t st) {
+    DecodeArgs a = given;
+    const PrefixPlan p = prefix_plan(a.B, a.Hq, a.Hkv, a.D, a.prefix);
+    a.skip = 0;
+    a.splits = p.splits;
+    if (p.splits > 0) {
+        a.skip = a.prefix;
+        const size_t all = attention_decode_workspace(a.B, a.Hq, a.Hkv, a.D, a.prefix);
+        a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + all - p.parts_bytes());
+        a.part_ml = reinterpret_cast<float2*>(a.part_o + p.rows() * p.dim);
+        const cudaError_t e = launch_attention_prefix(a, p, st);
+        if (e != cudaSuccess) return e;
+    }
     if (a.Hq / a.Hkv <= 8) return a.D <= 64 ? Narrow64::run(a, st) : Narrow128::run(a, st);
     return a.D <= 64 ? Wide64::run(a, st) : Wide128::run(a, st);
 }

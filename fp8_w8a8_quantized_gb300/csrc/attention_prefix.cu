@@ -1,0 +1,422 @@
+// The shared-prefix part of decode attention: the queries of all requests
+// against tokens that all of them share, which are read once for all.
+//
+//   s = q . k,  p = 2^(c s - c m),  o = sum p v     (attention_tile.cuh; c = scale
+//                                                    log2(e) k_scale of the row)
+//
+// With B requests this is a product of B G query rows a key head with the
+// prefix, bound by the tensor cores once B G is some 100 rows, where reading
+// the prefix anew for each request would be bound by B times its bytes.  So
+// it runs like prompt attention: tiles of 128 rows (128 / G requests with all
+// heads of the group), two of them a CTA, key tiles of 128, S, P and O in
+// tensor memory.  What differs:
+//   * keys and values are E4M3 in pages.  Three warps (17-19), which take the
+//     tiles of keys and of values in turn, read the codes (a page look-up a
+//     token, 16-byte loads, 32 tokens on their way while 32 are converted),
+//     convert them to f16, which is exact, and write them to shared memory in
+//     the layout that the MMA reads;
+//   * queries go to f16 with their exponent taken out (query_shift), P is f16;
+//   * the prefix is cut into parts so that the CTAs fill the SMs; each leaves
+//     (m, l, o) in the workspace, from where the decode kernel goes on.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attention_tile.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+#include "quant_math.cuh"
+
+namespace fp8k {
+namespace {
+
+constexpr int kStages = 5;
+constexpr int kMainWarps = 16;                 // softmax: 8 a query tile
+constexpr int kLoadWarps = 3;
+constexpr int kThreads = 32 * (kMainWarps + 1 + kLoadWarps);
+constexpr int kFillSms = 152;                  // CTAs that the parts should come to
+
+struct Bars {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t q_full;
+    uint64_t s_full[2], p_full[2][2], o_full[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    uint32_t there[kStages][4];  // which tokens of a key tile exist
+};
+
+template <int DP>
+constexpr size_t smem_bytes() {
+    return 1024 + (2 * kRows + kStages * kKeys) * DP * 2 + sizeof(Bars);
+}
+
+// Byte offset of 16-byte chunk `c` (of DP / 8) of row r in a tile of 128 rows:
+// columns of 64 elements, 128-byte rows, chunks permuted by the row.
+__device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
+    return static_cast<uint32_t>((c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// 16 bytes, loaded where it stands (not sunk to the first use).
+__device__ __forceinline__ uint4 ld_now(const uint8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs a, const PrefixPlan plan) {
+    constexpr uint32_t kColBytes = 128 * 128;
+    constexpr uint32_t kTile = DP / 64 * kColBytes;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sQ = smem_u32(smem), sKV = sQ + 2 * kTile;
+    Bars* bars = reinterpret_cast<Bars*>(smem + (2 + kStages) * kTile);
+    const int warp = threadIdx.x >> 5, lane = lane_id();
+    unsigned* status = a.status;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        mbar_init(&bars->q_full, kMainWarps);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&bars->s_full[x], 1);
+            mbar_init(&bars->p_full[x][0], kMainWarps / 2);
+            mbar_init(&bars->p_full[x][1], kMainWarps / 2);
+            mbar_init(&bars->o_full[x], 1);
+        }
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMainWarps) {
+        tmem_alloc(&bars->tmem_base, 512);
+        tmem_relinquish();
+    }
+    pdl_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    volatile int* abort_flag = &bars->abort;
+    pdl_wait_primary();
+
+    // this CTA's part of the prefix, key head and requests
+    const int split = static_cast<int>(blockIdx.x % plan.splits);
+    const int64_t rest = blockIdx.x / plan.splits;
+    const int hk = static_cast<int>(rest % a.Hkv);
+    const int64_t block = rest / a.Hkv;
+    const int G = a.Hq / a.Hkv, tpt = kRows / G;
+    const int64_t b0 = block * 2 * tpt;  // first request of tile A; B: b0 + tpt
+    const int tile0 = split * plan.tiles;
+    const int all_tiles = static_cast<int>((a.prefix + kKeys - 1) / kKeys);
+    const int tiles = min(plan.tiles, all_tiles - tile0);
+    const bool two = b0 + tpt < a.B;     // tile B has requests
+
+    if (warp < kMainWarps) {
+        // ------------------------------------------------ queries, softmax, output
+        const int x = warp >> 3, g = lane >> 2, t = lane & 3;
+        const int row0 = (warp & 3) * 32 + (warp >> 2 & 1) * 16 + g;
+        const uint32_t lanes = static_cast<uint32_t>(row0 - g) << 16;
+        const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * 128;
+        const float unit = a.scale * kLog2e * a.k_scale[hk * a.scale_stride];
+        float c[2];
+        bool real[2];
+        int limit[2], least = static_cast<int>(a.prefix);
+        int64_t at[2];  // rows of the parts
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = row0 + 8 * e, tok = r / G;
+            const int64_t b = b0 + x * tpt + tok;
+            real[e] = tok < tpt && b < a.B;
+            at[e] = ((static_cast<int64_t>(split) * a.Hkv + hk) * a.B + b) * G + (r - tok * G);
+            limit[e] = real[e] ? max(0, min(a.lens[b], static_cast<int>(a.prefix))) : static_cast<int>(a.prefix);
+            least = min(least, limit[e]);
+            uint4 u[DP / 32];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) {
+                const int ch = 4 * i + t;
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (real[e] && 8 * ch < a.D)
+                    u[i] = *reinterpret_cast<const uint4*>(
+                        a.q + b * a.ldq + static_cast<int64_t>(hk * G + (r - tok * G)) * a.D + 8 * ch);
+                top = top_of(u[i], top);
+            }
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const int shift = query_shift(top);
+            c[e] = scaled(unit, -shift);
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) {
+                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = pack_f16(scaled(bf16lo(w[k]), shift), scaled(bf16hi(w[k]), shift));
+                st_shared16(sQ + x * kTile + tile_chunk(r, 4 * i + t), h[0], h[1], h[2], h[3]);
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, d));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full);
+
+        SoftmaxRows rows;
+        bool ok = true;
+        if (x == 0 || two) {
+            for (int j = 0; j < tiles; ++j) {
+                if (!(ok = warp_ready(&bars->s_full[x], j & 1, abort_flag, status))) break;
+                tc_fence_after();
+                uint32_t s[4][16];
+                load_scores(tS, s);
+                const int key0 = (tile0 + j) * kKeys + 2 * t;
+                if ((tile0 + j + 1) * kKeys > least) {
+                    hide_after(s, 0, limit[0] - 1 - key0);
+                    hide_after(s, 1, limit[1] - 1 - key0);
+                }
+                const volatile uint32_t* there = bars->there[2 * j % kStages];
+                const uint32_t word[4] = {there[0], there[1], there[2], there[3]};
+                if ((word[0] & word[1] & word[2] & word[3]) != 0xFFFFFFFFu) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (!(word[b] >> (2 * t + 8 * (i >> 1) + (i & 1)) & 1u))
+                                s[b][4 * (i >> 1) + (i & 1)] = s[b][4 * (i >> 1) + 2 + (i & 1)] = 0xFF800000u;
+                }
+                softmax_tile<false, DP>(s, tS, tO, rows, c, real, j > 0, [&](int h) {
+                    if (lane == 0) mbar_arrive(&bars->p_full[x][h]);
+                });
+            }
+            if (ok && (ok = warp_ready(&bars->o_full[x], 0, abort_flag, status))) {
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float sum = rows.sum(e);
+                    if (real[e] && t == 0)
+                        a.part_ml[at[e]] = make_float2(rows.m[e] == -INFINITY ? -INFINITY : rows.m[e] * c[e], sum);
+                }
+#pragma unroll 1
+                for (int b = 0; b < DP / 32; ++b) {
+                    uint32_t o[16];
+                    __syncwarp();
+                    tmem_ld_16x256b_x4(tO + 32 * b, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[i]));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (!real[e]) continue;
+                        float* dst = a.part_o + at[e] * DP + 32 * b + 2 * t;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<float2*>(dst + 8 * i) = make_float2(
+                                __uint_as_float(o[4 * i + 2 * e]), __uint_as_float(o[4 * i + 2 * e + 1]));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp == kMainWarps) {
+        // ------------------------------------------------ MMA
+        constexpr uint32_t idS = idesc_f16(kRows, kKeys, false, false);
+        constexpr uint32_t idO = idesc_f16(kRows, DP, false, true);
+        // (the warp stays converged and every operand of an MMA is uniform: see elect_one)
+        const uint32_t tm = uniform(tmem), base_q = uniform(sQ), base_kv = uniform(sKV);
+        const int n = uniform(tiles), both = uniform(two ? 2 : 1);
+        auto ready = [&](uint64_t* bar, uint32_t parity) {
+            return warp_ready(bar, parity & 1u, abort_flag, status);
+        };
+        auto landed = [&](uint32_t k) { return ready(&bars->full[k % kStages], k / kStages); };
+        bool ok = ready(&bars->q_full, 0) && landed(0);
+        for (int j = 0; ok && j <= n; ++j) {
+            // P V of tile j - 1 and S of tile j; what they read is there
+            const uint32_t kk = 2 * j % kStages, vv = (2 * j + kStages - 1) % kStages;
+            const uint64_t kd = sdesc_kmajor_sw128(base_kv + uniform(kk) * kTile);
+            const uint64_t vd = sdesc_nmajor_sw128(base_kv + uniform(vv) * kTile, kColBytes);
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (x < both) {
+                    const uint32_t dS = tm + x * 128, dO = tm + 256 + x * 128;
+                    const uint64_t qd = sdesc_kmajor_sw128(base_q + x * kTile);
+                    if (j > 0) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!(ok = ready(&bars->p_full[x][h], j - 1))) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 4 * h; i < 4 * h + 4; ++i)
+                                    mma_f16_ts(dO, dS + 8 * i, vd + i * (2048 >> 4), idO, !(j == 1 && i == 0));
+                                if (h == 1 && j == n) mma_commit(&bars->o_full[x]);
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                    }
+                    if (j < n) {
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = 0; i < DP / 16; ++i) {
+                                const uint32_t off = ((i / 4) * kColBytes + (i % 4) * 32) >> 4;
+                                mma_f16(dS, qd + off, kd + off, idS, i != 0);
+                            }
+                            mma_commit(&bars->s_full[x]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (x == 1) break;
+                if (j + 1 < n && !(ok = landed(2 * j + 2))) break;
+                if (j < n && !(ok = landed(2 * j + 1))) break;
+            }
+            if (!ok) break;
+            if (elect_one()) {
+                if (j > 0) mma_commit(&bars->empty[vv]);
+                if (j < n) mma_commit(&bars->empty[kk]);
+            }
+            __syncwarp();
+        }
+        __syncwarp();
+        if (elect_one()) {
+            mma_commit(&bars->drain);
+            wait_drain(&bars->drain, status);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ codes -> f16 tiles
+        constexpr int kChunks = DP / 16;  // 16-code chunks of a token
+        const int64_t row_bytes = static_cast<int64_t>(a.Hkv) * a.D;
+        const int64_t head_off = static_cast<int64_t>(hk) * a.D;
+        const unsigned page = static_cast<unsigned>(a.page);
+        // the slots of this lane's four tokens (32 q + lane) of key tile j; -1: none, or not in the prefix
+        auto slots_of = [&](int (&slot)[4], int j) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t tok = static_cast<int64_t>(tile0 + j) * kKeys + 32 * q + lane;
+                slot[q] = -1;
+                if (j < tiles && tok < a.prefix) {
+                    const unsigned pg = static_cast<unsigned>(tok) / page;
+                    const int id = __ldg(a.table + pg);
+                    if (id >= 0 && id < a.n_pages)
+                        slot[q] = static_cast<int>(id * page + (static_cast<unsigned>(tok) - pg * page));
+                }
+            }
+        };
+        auto load = [&](uint4 (&r)[kChunks], const uint8_t* from, int slots) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int s = __shfl_sync(0xFFFFFFFFu, slots, (32 * i + lane) / kChunks);
+                const int ch = lane % kChunks;
+                r[i] = make_uint4(0, 0, 0, 0);
+                if (s >= 0 && 16 * ch < a.D) r[i] = ld_now(from + s * row_bytes + 16 * ch);
+            }
+        };
+        // A warp has no registers for more loads on their way: the lines of
+        // its next tile come to L2 while it converts this one.
+        auto prefetch = [&](const int (&slot)[4], const uint8_t* at) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (slot[q] >= 0)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(at + slot[q] * row_bytes) : "memory");
+        };
+        auto store = [&](const uint4 (&r)[kChunks], int stage, int q) {
+            const uint32_t dst = sKV + stage * kTile;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int row = 32 * q + (32 * i + lane) / kChunks, ch = lane % kChunks;
+                st_shared16(dst + tile_chunk(row, 2 * ch), f16_lo(r[i].x), f16_hi(r[i].x), f16_lo(r[i].y),
+                            f16_hi(r[i].y));
+                st_shared16(dst + tile_chunk(row, 2 * ch + 1), f16_lo(r[i].z), f16_hi(r[i].z), f16_lo(r[i].w),
+                            f16_hi(r[i].w));
+            }
+        };
+        int n = warp - kMainWarps - 1;  // tile 2 j: keys of key tile j, 2 j + 1: its values
+        int now[4], next[4];
+        uint4 r[2][kChunks];
+        slots_of(now, n / 2);
+        const uint8_t* from = (n & 1 ? a.v_cache : a.k_cache) + head_off;
+        prefetch(now, from);
+        load(r[0], from, now[0]);
+        for (; n < 2 * tiles; n += kLoadWarps) {
+            const int stage = n % kStages;
+            slots_of(next, (n + kLoadWarps) / 2);
+            prefetch(next, ((n + kLoadWarps) & 1 ? a.v_cache : a.k_cache) + head_off);
+            if (!warp_ready(&bars->empty[stage], (n / kStages & 1u) ^ 1u, abort_flag, status)) break;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const unsigned votes = __ballot_sync(0xFFFFFFFFu, now[q] >= 0);
+                if (lane == 0 && !(n & 1)) *const_cast<volatile uint32_t*>(&bars->there[stage][q]) = votes;
+                if (q == 3) from = ((n + kLoadWarps) & 1 ? a.v_cache : a.k_cache) + head_off;
+                load(r[q + 1 & 1], from, q < 3 ? now[q + 1 & 3] : next[0]);
+                store(r[q & 1], stage, q);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->full[stage]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) now[q] = next[q];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMainWarps) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+PrefixPlan prefix_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix) {
+    PrefixPlan p = {};
+    p.dim = D <= 64 ? 64 : 128;
+    p.all_rows = B * Hq;
+    // Worth its launch and its parts where it saves reading this many bytes.
+    constexpr int64_t kWorth = int64_t(16) << 20;
+    if (B < 2 || prefix < kKeys || (B - 1) * prefix < kWorth / (2 * Hkv * D)) return p;
+    const int64_t tpt = kRows / (Hq / Hkv);
+    p.row_blocks = (B + 2 * tpt - 1) / (2 * tpt);
+    const int64_t tiles = (prefix + kKeys - 1) / kKeys, items = p.row_blocks * Hkv;
+    int64_t splits = items >= kFillSms ? 1 : kFillSms / items;
+    if (splits > tiles) splits = tiles;
+    p.tiles = static_cast<int>((tiles + splits - 1) / splits);
+    p.splits = static_cast<int>((tiles + p.tiles - 1) / p.tiles);
+    return p;
+}
+
+cudaError_t launch_attention_prefix(const DecodeArgs& a, const PrefixPlan& plan, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.row_blocks * a.Hkv * plan.splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = plan.dim == 64 ? smem_bytes<64>() : smem_bytes<128>();
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, plan.dim == 64 ? attention_prefix<64> : attention_prefix<128>, a, plan);
+}
+
+cudaError_t prepare_attention_prefix() {
+    const cudaError_t e = cudaFuncSetAttribute(attention_prefix<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem_bytes<64>()));
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(attention_prefix<128>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem_bytes<128>()));
+}
+
+}  // namespace fp8k

@@ -1,13 +1,6 @@
 // Causal attention over packed prompts, grouped heads, bf16:
 //   out_i = sum_{j <= i} w_ij v_j / sum_j w_ij,  w_ij = exp(scale q_i . k_j - m_i)
-// in one pass over the keys.  With the running maximum m and sum l of a row,
-// a tile of keys adds
-//   p_j = 2^(c s_j - c m),  l += sum_j p_j,  o += sum_j p_j v_j    (c = scale log2 e)
-// and where a tile raises the maximum, l and o are first multiplied by
-// 2^(c m_old - c m_new).  o only needs m to be near the maximum: it stays
-// where it is until a tile exceeds it by 2^8 (p then reaches 256, which costs
-// neither bf16 p nor the fp32 sums any digits), so o is rescaled a few times
-// per row and not once per tile.
+// in one pass over the keys (the softmax of a tile: attention_tile.cuh).
 //
 // Tiles.  A row is a (token, query head) pair: the G = Hq / Hkv query heads
 // that share a key head lie next to one another, so a tile of 128 rows is
@@ -42,16 +35,13 @@
 
 #include <cstdint>
 
+#include "attention_tile.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 
 namespace fp8k {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;  // log2 of how far p may exceed 1 before m moves
-constexpr int kRows = 128;      // rows of a query tile
-constexpr int kKeys = 128;      // keys of a tile
 constexpr int kStages = 5;
 constexpr int kMainWarps = 16;
 constexpr int kThreads = 32 * (kMainWarps + 4);
@@ -131,11 +121,6 @@ __device__ __forceinline__ Item find_item(int64_t n, int64_t blocks, const Promp
     return it;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_prompt(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -200,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row0 = (warp & 3) * 32 + (warp >> 2 & 1) * 16 + g;  // this lane's rows: row0, row0 + 8
         const uint32_t lanes = static_cast<uint32_t>(row0 - g) << 16;
         const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * 128;
-        const float c = a.scale * kLog2e;
+        const float c[2] = {a.scale * kLog2e, a.scale * kLog2e};
         uint32_t s_phase = 0, o_phase = 0;
         int item_no = 0;
         bool ok = true;
@@ -224,102 +209,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int tiles = it.tiles[x];
             const int first_tok = it.q0 + x * tpt;  // no row of the tile sees less than this
-            float m[2] = {-INFINITY, -INFINITY}, l[2][2] = {};
+            SoftmaxRows rows;
             for (int j = 0; j < tiles; ++j) {
                 if (!(ok = warp_ready(&bars->s_full[x], s_phase, abort_flag, status))) break;
                 s_phase ^= 1u;
                 tc_fence_after();
                 uint32_t s[4][16];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_ld_16x256b_x4(tS + 32 * b, s[b]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(s[b][i]));  // (not before the wait)
+                load_scores(tS, s);
                 if (first_tok - j * kKeys < kKeys - 1) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int seen = my_tok[e] - j * kKeys - 2 * t;  // columns up to it, from 2 t on
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (32 * b + 8 * (i >> 1) + (i & 1) > seen)
-                                    s[b][4 * (i >> 1) + 2 * e + (i & 1)] = 0xFF800000u;  // -inf
-                    }
+                    hide_after(s, 0, my_tok[0] - j * kKeys - 2 * t);
+                    hide_after(s, 1, my_tok[1] - j * kKeys - 2 * t);
                 }
-                bool raise[2];
-                float top[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float part[4];
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        part[b] = __uint_as_float(s[b][2 * e]);
-#pragma unroll
-                        for (int i = 1; i < 8; ++i)
-                            part[b] = fmaxf(part[b], __uint_as_float(s[b][4 * (i >> 1) + 2 * e + (i & 1)]));
-                    }
-                    top[e] = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-                }
-#pragma unroll
-                for (int d = 1; d < 4; d <<= 1) {
-                    top[0] = fmaxf(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], d));
-                    top[1] = fmaxf(top[1], __shfl_xor_sync(0xFFFFFFFFu, top[1], d));
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e)  // (m = -inf: the first keys that are seen set it)
-                    raise[e] = mine[e] && (top[e] - m[e]) * c > kSlack;
-                if (__any_sync(0xFFFFFFFFu, raise[0] || raise[1])) {
-                    // (row by row, so that no row's digits depend on its neighbours)
-                    float keep[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        keep[e] = !raise[e] ? 1.0f : m[e] == -INFINITY ? 0.0f : ex2((m[e] - top[e]) * c);
-                        m[e] = raise[e] ? top[e] : m[e];
-                        l[e][0] *= keep[e];
-                        l[e][1] *= keep[e];
-                    }
-                    if (j > 0) {
-                        // S of tile j came after P V of tile j - 1: O is at rest
-#pragma unroll 1
-                        for (int b = 0; b < DP / 32; ++b) {
-                            uint32_t o[16];
-                            tmem_ld_16x256b_x4(tO + 32 * b, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                asm volatile("" : "+r"(o[i]));
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * keep[i >> 1 & 1]);
-                            }
-                            tmem_st_16x256b_x4(tO + 32 * b, o);
-                        }
-                    }
-                }
-                const float base[2] = {m[0] == -INFINITY ? 0.0f : -m[0] * c,
-                                       m[1] == -INFINITY ? 0.0f : -m[1] * c};
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        // keys 64 b + 8 (i / 2) + 2 t, + 1 of row i & 1
-                        const int e = i & 1;
-                        const uint32_t* from = &s[2 * b + (i >> 3)][4 * (i >> 1 & 3) + 2 * e];
-                        float y0 = base[e], y1 = base[e];
-                        fma2(y0, y1, __uint_as_float(from[0]), __uint_as_float(from[1]), c, c);
-                        y0 = ex2(y0);
-                        y1 = ex2(y1);
-                        add2(l[e][0], l[e][1], y0, y1);
-                        p[i] = pack_bf16(y0, y1);
-                    }
-                    tmem_st_16x128b_x8(tS + 32 * b, p);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->p_full[x][b]);
-                }
+                softmax_tile<true, DP>(s, tS, tO, rows, c, mine, j > 0, [&](int h) {
+                    if (lane == 0) mbar_arrive(&bars->p_full[x][h]);
+                });
             }
             if (!ok) break;
             if (tiles > 0) {
@@ -330,9 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint16_t* dst[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float sum = l[e][0] + l[e][1];
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                    const float sum = rows.sum(e);
                     inv[e] = sum == 0.0f ? 0.0f : 1.0f / sum;
                     dst[e] = a.out + (it.start + my_tok[e]) * a.ldo +
                              static_cast<int64_t>(it.head * G + head_in[e]) * a.D + 2 * t;

@@ -169,10 +169,28 @@ struct DecodeArgs {
     void* workspace;
     unsigned* status;
     int num_sms;
+    // set by launch_attention_decode: tokens that the prefix kernel does, its
+    // parts (m, l) and o of [split][Hkv][B * Hq / Hkv]
+    int64_t skip;
+    int splits;
+    float2* part_ml;
+    float* part_o;
 };
 cudaError_t launch_attention_decode(const DecodeArgs& a, cudaStream_t st);
-size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t room,
-                                  int64_t prefix);
+size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix);
+
+// The tokens that all requests share, read once for all (attention_prefix.cu).
+struct PrefixPlan {
+    int splits;          // parts of the prefix (0: not worth it, the decode kernel reads it)
+    int tiles;           // key tiles of a part
+    int dim;             // D rounded up to 64 or 128
+    int64_t row_blocks;  // blocks of query rows
+    int64_t all_rows;    // B * Hq
+    int64_t rows() const { return splits * all_rows; }
+    size_t parts_bytes() const { return static_cast<size_t>(rows()) * (dim * 4 + 8); }
+};
+PrefixPlan prefix_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix);
+cudaError_t launch_attention_prefix(const DecodeArgs& a, const PrefixPlan& plan, cudaStream_t st);
 
 // The current device's SM count and status word, after the same checks as
 // every other entry point (api.cu).
@@ -195,5 +213,6 @@ cudaError_t prepare_gemm_blockwise();
 cudaError_t prepare_gemm_pair();
 cudaError_t prepare_attention_prompt();
 cudaError_t prepare_attention_decode();
+cudaError_t prepare_attention_prefix();
 
 }  // namespace fp8k
