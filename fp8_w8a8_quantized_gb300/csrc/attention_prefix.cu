@@ -10,11 +10,11 @@
 // it runs like prompt attention: tiles of 128 rows (128 / G requests with all
 // heads of the group), two of them a CTA, key tiles of 128, S, P and O in
 // tensor memory.  What differs:
-//   * keys and values are E4M3 in pages.  Three warps (17-19), which take the
-//     tiles of keys and of values in turn, read the codes (a page look-up a
-//     token, 16-byte loads, 32 tokens on their way while 32 are converted),
-//     convert them to f16, which is exact, and write them to shared memory in
-//     the layout that the MMA reads;
+//   * keys and values are E4M3 in pages.  Seven warps (17-23) bring them in 32
+//     tokens at a time: a page look-up a token, asynchronous copies of the
+//     codes into a buffer of the warp's own, conversion to f16, which is
+//     exact, and a store to shared memory in the layout that the MMA reads.
+//     (Three warps that kept the codes in registers took 7 us a tile);
 //   * queries go to f16 with their exponent taken out (query_shift), P is f16;
 //   * the prefix is cut into parts so that the CTAs fill the SMs; each leaves
 //     (m, l, o) in the workspace, from where the decode kernel goes on.
@@ -30,9 +30,10 @@
 namespace fp8k {
 namespace {
 
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kMainWarps = 16;                 // softmax: 8 a query tile
-constexpr int kLoadWarps = 3;
+constexpr int kLoadWarps = 7;
+constexpr int kMainRegs = 96, kSideRegs = 48;  // 512 x 96 + 256 x 48 = 768 x 80, the launch's
 constexpr int kThreads = 32 * (kMainWarps + 1 + kLoadWarps);
 constexpr int kFillSms = 152;                  // CTAs that the parts should come to
 
@@ -48,7 +49,7 @@ struct Bars {
 
 template <int DP>
 constexpr size_t smem_bytes() {
-    return 1024 + (2 * kRows + kStages * kKeys) * DP * 2 + sizeof(Bars);
+    return 1024 + (2 * kRows + kStages * kKeys) * DP * 2 + kLoadWarps * 32 * DP + sizeof(Bars);
 }
 
 // Byte offset of 16-byte chunk `c` (of DP / 8) of row r in a tile of 128 rows:
@@ -62,15 +63,6 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
                  : "memory");
 }
 
-// 16 bytes, loaded where it stands (not sunk to the first use).
-__device__ __forceinline__ uint4 ld_now(const uint8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs a, const PrefixPlan plan) {
     constexpr uint32_t kColBytes = 128 * 128;
@@ -78,13 +70,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sQ = smem_u32(smem), sKV = sQ + 2 * kTile;
-    Bars* bars = reinterpret_cast<Bars*>(smem + (2 + kStages) * kTile);
+    const uint32_t sRaw = sKV + kStages * kTile;  // the load warps' codes
+    Bars* bars = reinterpret_cast<Bars*>(smem + (2 + kStages) * kTile + kLoadWarps * 32 * DP);
     const int warp = threadIdx.x >> 5, lane = lane_id();
     unsigned* status = a.status;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->full[s], 4);  // 32 tokens each
             mbar_init(&bars->empty[s], 1);
         }
         mbar_init(&bars->q_full, kMainWarps);
@@ -123,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
     const bool two = b0 + tpt < a.B;     // tile B has requests
 
     if (warp < kMainWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMainRegs));
         // ------------------------------------------------ queries, softmax, output
         const int x = warp >> 3, g = lane >> 2, t = lane & 3;
         const int row0 = (warp & 3) * 32 + (warp >> 2 & 1) * 16 + g;
@@ -132,13 +126,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
         float c[2];
         bool real[2];
         int limit[2], least = static_cast<int>(a.prefix);
-        int64_t at[2];  // rows of the parts
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = row0 + 8 * e, tok = r / G;
             const int64_t b = b0 + x * tpt + tok;
             real[e] = tok < tpt && b < a.B;
-            at[e] = ((static_cast<int64_t>(split) * a.Hkv + hk) * a.B + b) * G + (r - tok * G);
             limit[e] = real[e] ? max(0, min(a.lens[b], static_cast<int>(a.prefix))) : static_cast<int>(a.prefix);
             least = min(least, limit[e]);
             uint4 u[DP / 32];
@@ -200,8 +192,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             }
             if (ok && (ok = warp_ready(&bars->o_full[x], 0, abort_flag, status))) {
                 tc_fence_after();
+                int64_t at[2];  // rows of the parts
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    const int r = row0 + 8 * e, tok = r / G;
+                    at[e] = ((static_cast<int64_t>(split) * a.Hkv + hk) * a.B + b0 + x * tpt + tok) * G + (r - tok * G);
                     const float sum = rows.sum(e);
                     if (real[e] && t == 0)
                         a.part_ml[at[e]] = make_float2(rows.m[e] == -INFINITY ? -INFINITY : rows.m[e] * c[e], sum);
@@ -227,7 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
                 __syncwarp();
             }
         }
-    } else if (warp == kMainWarps) {
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
+      if (warp == kMainWarps) {
         // ------------------------------------------------ MMA
         constexpr uint32_t idS = idesc_f16(kRows, kKeys, false, false);
         constexpr uint32_t idO = idesc_f16(kRows, DP, false, true);
@@ -294,80 +291,69 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             wait_drain(&bars->drain, status);
         }
         __syncwarp();
-    } else {
+      } else {
         // ------------------------------------------------ codes -> f16 tiles
         constexpr int kChunks = DP / 16;  // 16-code chunks of a token
         const int64_t row_bytes = static_cast<int64_t>(a.Hkv) * a.D;
-        const int64_t head_off = static_cast<int64_t>(hk) * a.D;
         const unsigned page = static_cast<unsigned>(a.page);
-        // the slots of this lane's four tokens (32 q + lane) of key tile j; -1: none, or not in the prefix
-        auto slots_of = [&](int (&slot)[4], int j) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t tok = static_cast<int64_t>(tile0 + j) * kKeys + 32 * q + lane;
-                slot[q] = -1;
-                if (j < tiles && tok < a.prefix) {
-                    const unsigned pg = static_cast<unsigned>(tok) / page;
-                    const int id = __ldg(a.table + pg);
-                    if (id >= 0 && id < a.n_pages)
-                        slot[q] = static_cast<int>(id * page + (static_cast<unsigned>(tok) - pg * page));
-                }
-            }
+        const int jobs = 8 * tiles;  // job 8 j + q: keys of tokens 32 q + ... of key tile j; + 4: their values
+        // the slot of this lane's token of a job; -1: none, or not in the prefix
+        auto slot_of = [&](int job) {
+            const int64_t tok = static_cast<int64_t>(tile0 + (job >> 3)) * kKeys + 32 * (job & 3) + lane;
+            if (job >= jobs || tok >= a.prefix) return -1;
+            const unsigned pg = static_cast<unsigned>(tok) / page;
+            const int id = __ldg(a.table + pg);
+            if (id < 0 || id >= a.n_pages) return -1;
+            return static_cast<int>(id * page + (static_cast<unsigned>(tok) - pg * page));
         };
-        auto load = [&](uint4 (&r)[kChunks], const uint8_t* from, int slots) {
+        const uint32_t raw = sRaw + (warp - kMainWarps - 1) * 32 * DP;
+        const uint32_t ch = lane % kChunks;
+        auto copy = [&](int job, int slots) {
+            const uint8_t* from = (job & 4 ? a.v_cache : a.k_cache) + static_cast<int64_t>(hk) * a.D + 16 * ch;
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int s = __shfl_sync(0xFFFFFFFFu, slots, (32 * i + lane) / kChunks);
-                const int ch = lane % kChunks;
-                r[i] = make_uint4(0, 0, 0, 0);
-                if (s >= 0 && 16 * ch < a.D) r[i] = ld_now(from + s * row_bytes + 16 * ch);
+                copy_async16(raw + 512 * i + 16 * lane, from + s * row_bytes, s >= 0 && 16 * ch < a.D);
             }
+            copy_commit();
         };
-        // A warp has no registers for more loads on their way: the lines of
-        // its next tile come to L2 while it converts this one.
-        auto prefetch = [&](const int (&slot)[4], const uint8_t* at) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (slot[q] >= 0)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(at + slot[q] * row_bytes) : "memory");
-        };
-        auto store = [&](const uint4 (&r)[kChunks], int stage, int q) {
+        int job = warp - kMainWarps - 1;
+        int now = slot_of(job), next = slot_of(job + kLoadWarps);
+        if (job < jobs) copy(job, now);
+        for (; job < jobs; job += kLoadWarps) {
+            const int n = job >> 2, stage = n % kStages;  // tile 2 j: keys, 2 j + 1: values of key tile j
+            const int later = slot_of(job + 2 * kLoadWarps);
+            if (!warp_ready(&bars->empty[stage], (n / kStages & 1u) ^ 1u, abort_flag, status)) break;
+            copy_wait<0>();
+            __syncwarp();
+            const unsigned votes = __ballot_sync(0xFFFFFFFFu, now >= 0);
+            if (lane == 0 && !(n & 1)) *const_cast<volatile uint32_t*>(&bars->there[stage][job & 3]) = votes;
             const uint32_t dst = sKV + stage * kTile;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int row = 32 * q + (32 * i + lane) / kChunks, ch = lane % kChunks;
-                st_shared16(dst + tile_chunk(row, 2 * ch), f16_lo(r[i].x), f16_hi(r[i].x), f16_lo(r[i].y),
-                            f16_hi(r[i].y));
-                st_shared16(dst + tile_chunk(row, 2 * ch + 1), f16_lo(r[i].z), f16_hi(r[i].z), f16_lo(r[i].w),
-                            f16_hi(r[i].w));
+            for (int i = 0; i < kChunks; i += 2) {
+                const uint4 u = ld_shared16(raw + 512 * i + 16 * lane);
+                const uint4 v = ld_shared16(raw + 512 * (i + 1) + 16 * lane);
+                const int row = 32 * (job & 3) + (32 * i + lane) / kChunks, row2 = row + 32 / kChunks;
+                st_shared16(dst + tile_chunk(row, 2 * ch), f16_lo(u.x), f16_hi(u.x), f16_lo(u.y), f16_hi(u.y));
+                st_shared16(dst + tile_chunk(row, 2 * ch + 1), f16_lo(u.z), f16_hi(u.z), f16_lo(u.w), f16_hi(u.w));
+                st_shared16(dst + tile_chunk(row2, 2 * ch), f16_lo(v.x), f16_hi(v.x), f16_lo(v.y), f16_hi(v.y));
+                st_shared16(dst + tile_chunk(row2, 2 * ch + 1), f16_lo(v.z), f16_hi(v.z), f16_lo(v.w), f16_hi(v.w));
             }
-        };
-        int n = warp - kMainWarps - 1;  // tile 2 j: keys of key tile j, 2 j + 1: its values
-        int now[4], next[4];
-        uint4 r[2][kChunks];
-        slots_of(now, n / 2);
-        const uint8_t* from = (n & 1 ? a.v_cache : a.k_cache) + head_off;
-        prefetch(now, from);
-        load(r[0], from, now[0]);
-        for (; n < 2 * tiles; n += kLoadWarps) {
-            const int stage = n % kStages;
-            slots_of(next, (n + kLoadWarps) / 2);
-            prefetch(next, ((n + kLoadWarps) & 1 ? a.v_cache : a.k_cache) + head_off);
-            if (!warp_ready(&bars->empty[stage], (n / kStages & 1u) ^ 1u, abort_flag, status)) break;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const unsigned votes = __ballot_sync(0xFFFFFFFFu, now[q] >= 0);
-                if (lane == 0 && !(n & 1)) *const_cast<volatile uint32_t*>(&bars->there[stage][q]) = votes;
-                if (q == 3) from = ((n + kLoadWarps) & 1 ? a.v_cache : a.k_cache) + head_off;
-                load(r[q + 1 & 1], from, q < 3 ? now[q + 1 & 3] : next[0]);
-                store(r[q & 1], stage, q);
-            }
+            __syncwarp();  // the codes are read: the next ones may come
+            if (job + kLoadWarps < jobs) copy(job + kLoadWarps, next);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->full[stage]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) now[q] = next[q];
+            if (later >= 0) {
+                const int far = job + 2 * kLoadWarps;
+                const uint8_t* from = (far & 4 ? a.v_cache : a.k_cache) + static_cast<int64_t>(hk) * a.D;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(from + later * row_bytes) : "memory");
+            }
+            now = next;
+            next = later;
         }
+        copy_wait<0>();
+      }
     }
     tc_fence_before();
     __syncthreads();
