@@ -47,6 +47,7 @@ constexpr int kTile = 32;            // tokens of a warp's step
 constexpr int kWarps = 8;            // warps of a CTA
 constexpr int kCtas = 152;           // CTAs at most (one per SM)
 constexpr int64_t kMaxPlan = 4096;   // requests up to which the work is cut by tokens
+constexpr int kBatch = 4;            // parts of a row that are loaded at a time
 constexpr int kMinTokens = 64;       // tokens of a request that are worth a CTA
 
 // A request whose steps several CTAs share, for the kernel that joins them.
@@ -260,41 +261,21 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
             l[x][0] = l[x][1] = 0.0f;
         }
         if (on) {
-            if (a.splits > 0 && u0 == 0 && way == 0) {
-                // what the prefix kernel has of this request, one part after the other
+            const float unit = a.scale * kLog2e * a.k_scale[hk * a.scale_stride];
+            uint4 u[NT][DP / 64][2];  // the queries, on their way while the first tokens are
 #pragma unroll
-                for (int x = 0; x < NT; ++x)
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = r0 + 8 * x + 2 * t + e;
-                        if (row >= G) continue;
-                        const int64_t stride = static_cast<int64_t>(a.Hkv) * a.B * G;
-                        const int64_t at = static_cast<int64_t>(hk) * a.B * G + b * G + row;
-                        const float2* ml = a.part_ml + at;
-                        const float* src = a.part_o + at * DP + DP / 8 * g;
-                        float top = -INFINITY, sum = 0.0f;
-#pragma unroll 8
-                        for (int i = 0; i < a.splits; ++i) top = fmaxf(top, ml[i * stride].x);
-                        // (the loads of several parts on their way: nothing here waits for the part before)
-#pragma unroll 4
-                        for (int i = 0; i < a.splits; ++i) {
-                            const float2 part = ml[i * stride];
-                            const float take = part.x == -INFINITY ? 0.0f : ex2(part.x - top);
-                            sum += part.y * take;
-                            const float4* from = reinterpret_cast<const float4*>(src + i * stride * DP);
-#pragma unroll
-                            for (int y = 0; y < MT / 2; ++y) {
-                                const float4 v = from[y];
-                                o[2 * y][x][e] += v.x * take;
-                                o[2 * y][x][e + 2] += v.y * take;
-                                o[2 * y + 1][x][e] += v.z * take;
-                                o[2 * y + 1][x][e + 2] += v.w * take;
-                            }
-                        }
-                        m[x][e] = top;
-                        l[x][e] = g == 0 ? sum : 0.0f;  // (summed over the lanes in the end)
+                for (int j = 0; j < DP / 64; ++j) {
+                    const int row = r0 + 8 * x + g, d = 64 * j + 16 * t;
+                    u[x][j][0] = u[x][j][1] = make_uint4(0, 0, 0, 0);
+                    if (row < G && d < a.D) {
+                        const uint4* src = reinterpret_cast<const uint4*>(
+                            a.q + b * a.ldq + static_cast<int64_t>(hk * G + row) * a.D + d);
+                        u[x][j][0] = src[0];
+                        u[x][j][1] = src[1];
                     }
-            }
+                }
             const int64_t row_bytes = static_cast<int64_t>(a.Hkv) * a.D;
             const uint8_t* kc = a.k_cache + static_cast<int64_t>(hk) * a.D;
             const uint8_t* vc = a.v_cache + static_cast<int64_t>(hk) * a.D;
@@ -332,26 +313,72 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
                 copy_commit();
             }
             int next = ahead[ST - 1];
+            if (a.splits > 0 && u0 == 0 && way == 0) {
+                // what the prefix kernel has of this request
+                const int64_t stride = static_cast<int64_t>(a.Hkv) * a.B * G;
+                const int64_t at0 = static_cast<int64_t>(hk) * a.B * G + b * G + r0;
+                for (int i0 = 0; i0 < a.splits; i0 += kBatch) {
+                    float2 ml[NT][2][kBatch];
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i) {
+                                const int row = 8 * x + 2 * t + e;
+                                ml[x][e][i] = make_float2(-INFINITY, 0.0f);
+                                if (r0 + row < G && i0 + i < a.splits)
+                                    ml[x][e][i] = a.part_ml[at0 + row + (i0 + i) * stride];
+                            }
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int row = 8 * x + 2 * t + e;
+                            if (r0 + row >= G) continue;
+                            const float* src = a.part_o + (at0 + row + i0 * stride) * DP + DP / 8 * g;
+                            float4 v[kBatch][MT / 2];
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                                for (int y = 0; y < MT / 2; ++y)
+                                    v[i][y] = i0 + i < a.splits
+                                                  ? reinterpret_cast<const float4*>(src + i * stride * DP)[y]
+                                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            float top = m[x][e];
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[x][e][i].x);
+                            const float keep = m[x][e] == -INFINITY ? 0.0f : ex2(m[x][e] - top);
+                            m[x][e] = top;
+                            l[x][e] *= keep;
+#pragma unroll
+                            for (int y = 0; y < MT; ++y) {
+                                o[y][x][e] *= keep;
+                                o[y][x][e + 2] *= keep;
+                            }
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i) {
+                                const float take = ml[x][e][i].x == -INFINITY ? 0.0f : ex2(ml[x][e][i].x - top);
+                                if (g == 0) l[x][e] += ml[x][e][i].y * take;  // (summed over the lanes in the end)
+#pragma unroll
+                                for (int y = 0; y < MT / 2; ++y) {
+                                    o[2 * y][x][e] += v[i][y].x * take;
+                                    o[2 * y][x][e + 2] += v[i][y].y * take;
+                                    o[2 * y + 1][x][e] += v[i][y].z * take;
+                                    o[2 * y + 1][x][e + 2] += v[i][y].w * take;
+                                }
+                            }
+                        }
+                }
+            }
+
 
             // queries: row g of each tile, the elements that this lane's keys meet
-            const float unit = a.scale * kLog2e * a.k_scale[hk * a.scale_stride];
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-                const int row = r0 + 8 * x + g;
-                uint4 u[DP / 64][2];
                 uint32_t top = 0;
 #pragma unroll
-                for (int j = 0; j < DP / 64; ++j) {
-                    u[j][0] = u[j][1] = make_uint4(0, 0, 0, 0);
-                    const int d = 64 * j + 16 * t;
-                    if (row < G && d < a.D) {
-                        const uint4* src = reinterpret_cast<const uint4*>(
-                            a.q + b * a.ldq + static_cast<int64_t>(hk * G + row) * a.D + d);
-                        u[j][0] = src[0];
-                        u[j][1] = src[1];
-                    }
-                    top = top_of(u[j][1], top_of(u[j][0], top));
-                }
+                for (int j = 0; j < DP / 64; ++j) top = top_of(u[x][j][1], top_of(u[x][j][0], top));
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
                 const int shift = query_shift(top);
@@ -359,7 +386,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
                 for (int j = 0; j < DP / 64; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t w[4] = {u[j][e].x, u[j][e].y, u[j][e].z, u[j][e].w};
+                        const uint32_t w[4] = {u[x][j][e].x, u[x][j][e].y, u[x][j][e].z, u[x][j][e].w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             // elements 8 e + 2 i, + 1 of the 16: step 4 j + (4 e + i) / 2
@@ -595,7 +622,6 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
 // row that has many are dealt to the CTA's warps, whose sums are then added in
 // the warps' order.
 constexpr int kJoinWarps = 16;
-constexpr int kBatch = 4;  // parts in flight a warp
 template <int NT, int DP, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const DecodeArgs a) {
     constexpr int R = 8 * NT;
@@ -747,7 +773,7 @@ cudaError_t launch_attention_decode(const DecodeArgs& given, cudaStream_t st) {
     DecodeArgs a = given;
     const PrefixPlan p = prefix_plan(a.B, a.Hq, a.Hkv, a.D, a.prefix);
     a.skip = 0;
-    a.splits = p.splits;
+    a.splits = p.parts();
     if (p.splits > 0) {
         a.skip = a.prefix;
         const size_t all = attention_decode_workspace(a.B, a.Hq, a.Hkv, a.D, a.prefix);

@@ -16,8 +16,11 @@
 //     exact, and a store to shared memory in the layout that the MMA reads.
 //     (Three warps that kept the codes in registers took 7 us a tile);
 //   * queries go to f16 with their exponent taken out (query_shift), P is f16;
-//   * the prefix is cut into parts so that the CTAs fill the SMs; each leaves
-//     (m, l, o) in the workspace, from where the decode kernel goes on.
+//   * the prefix is cut into parts so that the CTAs fill the SMs; the CTAs of a
+//     cluster have parts of the same rows, and add them up through
+//     distributed shared memory: one (m, l, o) a row and cluster goes to the
+//     workspace, from where the decode kernel goes on.  (With a part a CTA the
+//     decode kernel spent 7 us a request on 16 of them.)
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -35,6 +38,7 @@ constexpr int kMainWarps = 16;                 // softmax: 8 a query tile
 constexpr int kLoadWarps = 7;
 constexpr int kMainRegs = 96, kSideRegs = 48;  // 512 x 96 + 256 x 48 = 768 x 80, the launch's
 constexpr int kThreads = 32 * (kMainWarps + 1 + kLoadWarps);
+constexpr int kMaxCluster = 4;  // (clusters of 8 found room for fewer CTAs: 71 us instead of 47)
 constexpr int kFillSms = 152;                  // CTAs that the parts should come to
 
 struct Bars {
@@ -45,6 +49,7 @@ struct Bars {
     uint32_t tmem_base;
     int abort;
     uint32_t there[kStages][4];  // which tokens of a key tile exist
+    float2 ml[2 * kRows];        // (m, l) of this CTA's part, m in log2 units
 };
 
 template <int DP>
@@ -75,6 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
     const int warp = threadIdx.x >> 5, lane = lane_id();
     unsigned* status = a.status;
 
+    if (threadIdx.x < 2 * kRows) bars->ml[threadIdx.x] = make_float2(-INFINITY, 0.0f);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars->full[s], 4);  // 32 tokens each
@@ -112,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
     const int64_t b0 = block * 2 * tpt;  // first request of tile A; B: b0 + tpt
     const int tile0 = split * plan.tiles;
     const int all_tiles = static_cast<int>((a.prefix + kKeys - 1) / kKeys);
-    const int tiles = min(plan.tiles, all_tiles - tile0);
+    const int tiles = max(min(plan.tiles, all_tiles - tile0), 0);
     const bool two = b0 + tpt < a.B;     // tile B has requests
 
     if (warp < kMainWarps) {
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
 
         SoftmaxRows rows;
         bool ok = true;
-        if (x == 0 || two) {
+        if (tiles > 0 && (x == 0 || two)) {
             for (int j = 0; j < tiles; ++j) {
                 if (!(ok = warp_ready(&bars->s_full[x], j & 1, abort_flag, status))) break;
                 tc_fence_after();
@@ -192,14 +198,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             }
             if (ok && (ok = warp_ready(&bars->o_full[x], 0, abort_flag, status))) {
                 tc_fence_after();
-                int64_t at[2];  // rows of the parts
+                // Tile A's part goes where the queries were (S of both tiles is complete by
+                // now), B's where keys and values were (it is the last MMA that reads them).
+                float* part = reinterpret_cast<float*>(smem + (x == 0 ? 0 : 2 * kTile));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = row0 + 8 * e, tok = r / G;
-                    at[e] = ((static_cast<int64_t>(split) * a.Hkv + hk) * a.B + b0 + x * tpt + tok) * G + (r - tok * G);
                     const float sum = rows.sum(e);
-                    if (real[e] && t == 0)
-                        a.part_ml[at[e]] = make_float2(rows.m[e] == -INFINITY ? -INFINITY : rows.m[e] * c[e], sum);
+                    if (t == 0)
+                        bars->ml[x * kRows + row0 + 8 * e] =
+                            make_float2(rows.m[e] == -INFINITY ? -INFINITY : rows.m[e] * c[e], sum);
                 }
 #pragma unroll 1
                 for (int b = 0; b < DP / 32; ++b) {
@@ -211,12 +218,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
                     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[i]));
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (!real[e]) continue;
-                        float* dst = a.part_o + at[e] * DP + 32 * b + 2 * t;
+                        // (16-byte chunks permuted by the row, against bank conflicts)
+                        float* dst = part + (row0 + 8 * e) * DP;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<float2*>(dst + 8 * i) = make_float2(
+                        for (int i = 0; i < 4; ++i) {
+                            const int ch = (8 * b + 2 * i + (t >> 1)) ^ (row0 & 7);
+                            *reinterpret_cast<float2*>(dst + 4 * ch + 2 * (t & 1)) = make_float2(
                                 __uint_as_float(o[4 * i + 2 * e]), __uint_as_float(o[4 * i + 2 * e + 1]));
+                        }
                     }
                 }
                 __syncwarp();
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             return warp_ready(bar, parity & 1u, abort_flag, status);
         };
         auto landed = [&](uint32_t k) { return ready(&bars->full[k % kStages], k / kStages); };
-        bool ok = ready(&bars->q_full, 0) && landed(0);
+        bool ok = n > 0 && ready(&bars->q_full, 0) && landed(0);
         for (int j = 0; ok && j <= n; ++j) {
             // P V of tile j - 1 and S of tile j; what they read is there
             const uint32_t kk = 2 * j % kStages, vv = (2 * j + kStages - 1) % kStages;
@@ -356,7 +365,44 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
       }
     }
     tc_fence_before();
-    __syncthreads();
+    // The parts of the cluster's CTAs, added up in the order of the prefix:
+    // each CTA does its share of the rows.  (Whatever happened above, every
+    // thread comes by here: no CTA waits for one that gave up.)
+    cluster_sync_all();
+    {
+        const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
+        const int per = 2 * kRows / ctas;
+        const uint32_t ml0 = smem_u32(bars->ml), parts[2] = {sQ, sKV};
+        for (int i = threadIdx.x; i < per * (DP / 4); i += kThreads) {
+            const int r = rank * per + i / (DP / 4), ch = i % (DP / 4);
+            const int x = r / kRows, row = r - x * kRows, tok = row / G;
+            const int64_t b = b0 + x * tpt + tok;
+            if (tok >= tpt || b >= a.B) continue;
+            float m[kMaxCluster], l[kMaxCluster];
+            float4 v[kMaxCluster];
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) {  // all of them on their way at once
+                const int from = min(k, ctas - 1);
+                m[k] = ld_dsmem_f32(map_to_rank(ml0 + 8 * r, from));
+                l[k] = ld_dsmem_f32(map_to_rank(ml0 + 8 * r + 4, from));
+                v[k] = ld_dsmem_v4(map_to_rank(parts[x] + 4 * DP * row + 16 * (ch ^ (row & 7)), from));
+            }
+            float top = -INFINITY, sum = 0.0f, o[4] = {};
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) top = k < ctas ? fmaxf(top, m[k]) : top;
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) {
+                if (k >= ctas || m[k] == -INFINITY) continue;  // (an empty part has written nothing)
+                const float take = ex2(m[k] - top);
+                sum += l[k] * take;
+                o[0] += v[k].x * take, o[1] += v[k].y * take, o[2] += v[k].z * take, o[3] += v[k].w * take;
+            }
+            const int64_t at = ((static_cast<int64_t>(split / ctas) * a.Hkv + hk) * a.B + b) * G + (row - tok * G);
+            *reinterpret_cast<float4*>(a.part_o + at * DP + 4 * ch) = make_float4(o[0], o[1], o[2], o[3]);
+            if (ch == 0) a.part_ml[at] = make_float2(top, sum);
+        }
+    }
+    cluster_sync_all();  // (nobody's memory goes while it is read)
     if (warp == kMainWarps) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -377,22 +423,29 @@ PrefixPlan prefix_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t pr
     const int64_t tiles = (prefix + kKeys - 1) / kKeys, items = p.row_blocks * Hkv;
     int64_t splits = items >= kFillSms ? 1 : kFillSms / items;
     if (splits > tiles) splits = tiles;
+    p.cluster = splits >= kMaxCluster ? kMaxCluster : splits >= 2 ? 2 : 1;
+    splits = splits / p.cluster * p.cluster;
     p.tiles = static_cast<int>((tiles + splits - 1) / splits);
-    p.splits = static_cast<int>((tiles + p.tiles - 1) / p.tiles);
+    // whole clusters (the last parts may be empty), and no empty ones
+    const int64_t used = (tiles + p.tiles - 1) / p.tiles;
+    p.splits = static_cast<int>((used + p.cluster - 1) / p.cluster * p.cluster);
     return p;
 }
 
 cudaError_t launch_attention_prefix(const DecodeArgs& a, const PrefixPlan& plan, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(static_cast<unsigned>(plan.row_blocks * a.Hkv * plan.splits));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = plan.dim == 64 ? smem_bytes<64>() : smem_bytes<128>();
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(plan.cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, plan.dim == 64 ? attention_prefix<64> : attention_prefix<128>, a, plan);
 }
 

@@ -555,6 +555,12 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
 // Non-aligned cluster barrier: every thread of every CTA of the cluster
 // arrives (release) and waits (acquire).
 // Split form of the cluster barrier: every thread of the cluster arrives,
