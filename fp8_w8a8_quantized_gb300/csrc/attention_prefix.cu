@@ -36,7 +36,7 @@ namespace {
 constexpr int kStages = 4;
 constexpr int kMainWarps = 16;                 // softmax: 8 a query tile
 constexpr int kLoadWarps = 7;
-constexpr int kMainRegs = 96, kSideRegs = 48;  // 512 x 96 + 256 x 48 = 768 x 80, the launch's
+constexpr int kMainRegs = 88, kSideRegs = 64;  // 512 x 88 + 256 x 64 = 768 x 80, the launch's
 constexpr int kThreads = 32 * (kMainWarps + 1 + kLoadWarps);
 constexpr int kMaxCluster = 4;  // (clusters of 8 found room for fewer CTAs: 71 us instead of 47)
 constexpr int kFillSms = 152;                  // CTAs that the parts should come to
@@ -283,9 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
                         __syncwarp();
                     }
                 }
-                if (x == 1) break;
-                if (j + 1 < n && !(ok = landed(2 * j + 2))) break;
-                if (j < n && !(ok = landed(2 * j + 1))) break;
             }
             if (!ok) break;
             if (elect_one()) {
@@ -293,6 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
                 if (j < n) mma_commit(&bars->empty[kk]);
             }
             __syncwarp();
+            if (j + 1 < n && !(ok = landed(2 * j + 2))) break;
+            if (j < n && !(ok = landed(2 * j + 1))) break;
         }
         __syncwarp();
         if (elect_one()) {
@@ -317,39 +316,54 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
         };
         const uint32_t raw = sRaw + (warp - kMainWarps - 1) * 32 * DP;
         const uint32_t ch = lane % kChunks;
-        auto copy = [&](int job, int slots) {
+        // Half a job's codes at a time, so that one half is on its way while the
+        // other one is converted.
+        auto copy = [&](int job, int slots, int h) {
             const uint8_t* from = (job & 4 ? a.v_cache : a.k_cache) + static_cast<int64_t>(hk) * a.D + 16 * ch;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
+            for (int i = h * kChunks / 2; i < (h + 1) * kChunks / 2; ++i) {
                 const int s = __shfl_sync(0xFFFFFFFFu, slots, (32 * i + lane) / kChunks);
                 copy_async16(raw + 512 * i + 16 * lane, from + s * row_bytes, s >= 0 && 16 * ch < a.D);
             }
             copy_commit();
         };
+        // where this lane's chunks go in a tile: the first of the job's row
+        // lane / kChunks and of the next row that another permutation meets
+        constexpr int kStep = 32 / kChunks;           // rows between two chunks of a lane
+        const int r0 = lane / kChunks;
+        const uint32_t at[2][2] = {{tile_chunk(r0, 2 * ch), tile_chunk(r0, 2 * ch + 1)},
+                                   {tile_chunk(r0 + kStep, 2 * ch), tile_chunk(r0 + kStep, 2 * ch + 1)}};
         int job = warp - kMainWarps - 1;
         int now = slot_of(job), next = slot_of(job + kLoadWarps);
-        if (job < jobs) copy(job, now);
+        if (job < jobs) {
+            copy(job, now, 0);
+            copy(job, now, 1);
+        }
         for (; job < jobs; job += kLoadWarps) {
             const int n = job >> 2, stage = n % kStages;  // tile 2 j: keys, 2 j + 1: values of key tile j
             const int later = slot_of(job + 2 * kLoadWarps);
+            const bool more = job + kLoadWarps < jobs;
             if (!warp_ready(&bars->empty[stage], (n / kStages & 1u) ^ 1u, abort_flag, status)) break;
-            copy_wait<0>();
-            __syncwarp();
             const unsigned votes = __ballot_sync(0xFFFFFFFFu, now >= 0);
             if (lane == 0 && !(n & 1)) *const_cast<volatile uint32_t*>(&bars->there[stage][job & 3]) = votes;
-            const uint32_t dst = sKV + stage * kTile;
+            const uint32_t dst = sKV + stage * kTile + (job & 3) * 32 * 128;
 #pragma unroll
-            for (int i = 0; i < kChunks; i += 2) {
-                const uint4 u = ld_shared16(raw + 512 * i + 16 * lane);
-                const uint4 v = ld_shared16(raw + 512 * (i + 1) + 16 * lane);
-                const int row = 32 * (job & 3) + (32 * i + lane) / kChunks, row2 = row + 32 / kChunks;
-                st_shared16(dst + tile_chunk(row, 2 * ch), f16_lo(u.x), f16_hi(u.x), f16_lo(u.y), f16_hi(u.y));
-                st_shared16(dst + tile_chunk(row, 2 * ch + 1), f16_lo(u.z), f16_hi(u.z), f16_lo(u.w), f16_hi(u.w));
-                st_shared16(dst + tile_chunk(row2, 2 * ch), f16_lo(v.x), f16_hi(v.x), f16_lo(v.y), f16_hi(v.y));
-                st_shared16(dst + tile_chunk(row2, 2 * ch + 1), f16_lo(v.z), f16_hi(v.z), f16_lo(v.w), f16_hi(v.w));
+            for (int h = 0; h < 2; ++h) {
+                copy_wait<1>();
+                __syncwarp();
+#pragma unroll
+                for (int i = h * kChunks / 2; i < (h + 1) * kChunks / 2; ++i) {
+                    const uint4 u = ld_shared16(raw + 512 * i + 16 * lane);
+                    // rows 8 apart have the same permutation
+                    const int odd = kStep < 8 ? i & 1 : 0;
+                    const uint32_t down = dst + 128 * kStep * (i - odd);
+                    st_shared16(down + at[odd][0], f16_lo(u.x), f16_hi(u.x), f16_lo(u.y), f16_hi(u.y));
+                    st_shared16(down + at[odd][1], f16_lo(u.z), f16_hi(u.z), f16_lo(u.w), f16_hi(u.w));
+                }
+                __syncwarp();  // the codes are read: the next ones may come
+                if (more) copy(job + kLoadWarps, next, h);
+                else copy_commit();
             }
-            __syncwarp();  // the codes are read: the next ones may come
-            if (job + kLoadWarps < jobs) copy(job + kLoadWarps, next);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->full[stage]);
@@ -369,37 +383,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
     // each CTA does its share of the rows.  (Whatever happened above, every
     // thread comes by here: no CTA waits for one that gave up.)
     cluster_sync_all();
-    {
+    if (warp < kMainWarps) {
         const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
         const int per = 2 * kRows / ctas;
-        const uint32_t ml0 = smem_u32(bars->ml), parts[2] = {sQ, sKV};
-        for (int i = threadIdx.x; i < per * (DP / 4); i += kThreads) {
+        const uint32_t ml0 = smem_u32(bars->ml);
+#pragma unroll 2
+        for (int i = threadIdx.x; i < per * (DP / 4); i += 32 * kMainWarps) {
             const int r = rank * per + i / (DP / 4), ch = i % (DP / 4);
             const int x = r / kRows, row = r - x * kRows, tok = row / G;
+            const uint32_t at = (x == 0 ? sQ : sKV) + 4 * DP * row + 16 * (ch ^ (row & 7));
             const int64_t b = b0 + x * tpt + tok;
-            if (tok >= tpt || b >= a.B) continue;
-            float m[kMaxCluster], l[kMaxCluster];
+            float2 ml[kMaxCluster];
             float4 v[kMaxCluster];
 #pragma unroll
             for (int k = 0; k < kMaxCluster; ++k) {  // all of them on their way at once
                 const int from = min(k, ctas - 1);
-                m[k] = ld_dsmem_f32(map_to_rank(ml0 + 8 * r, from));
-                l[k] = ld_dsmem_f32(map_to_rank(ml0 + 8 * r + 4, from));
-                v[k] = ld_dsmem_v4(map_to_rank(parts[x] + 4 * DP * row + 16 * (ch ^ (row & 7)), from));
+                ml[k] = ld_dsmem_v2(map_to_rank(ml0 + 8 * r, from));
+                v[k] = ld_dsmem_v4(map_to_rank(at, from));
             }
             float top = -INFINITY, sum = 0.0f, o[4] = {};
 #pragma unroll
-            for (int k = 0; k < kMaxCluster; ++k) top = k < ctas ? fmaxf(top, m[k]) : top;
+            for (int k = 0; k < kMaxCluster; ++k) top = k < ctas ? fmaxf(top, ml[k].x) : top;
 #pragma unroll
             for (int k = 0; k < kMaxCluster; ++k) {
-                if (k >= ctas || m[k] == -INFINITY) continue;  // (an empty part has written nothing)
-                const float take = ex2(m[k] - top);
-                sum += l[k] * take;
+                if (k >= ctas || ml[k].x == -INFINITY) continue;  // (an empty part has written nothing)
+                const float take = ex2(ml[k].x - top);
+                sum += ml[k].y * take;
                 o[0] += v[k].x * take, o[1] += v[k].y * take, o[2] += v[k].z * take, o[3] += v[k].w * take;
             }
-            const int64_t at = ((static_cast<int64_t>(split / ctas) * a.Hkv + hk) * a.B + b) * G + (row - tok * G);
-            *reinterpret_cast<float4*>(a.part_o + at * DP + 4 * ch) = make_float4(o[0], o[1], o[2], o[3]);
-            if (ch == 0) a.part_ml[at] = make_float2(top, sum);
+            if (tok >= tpt || b >= a.B) continue;
+            const int64_t to = ((static_cast<int64_t>(split / ctas) * a.Hkv + hk) * a.B + b) * G + (row - tok * G);
+            *reinterpret_cast<float4*>(a.part_o + to * DP + 4 * ch) = make_float4(o[0], o[1], o[2], o[3]);
+            if (ch == 0) a.part_ml[to] = make_float2(top, sum);
         }
     }
     cluster_sync_all();  // (nobody's memory goes while it is read)

@@ -677,6 +677,12 @@ __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float2 ld_dsmem_v2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
 // Four consecutive floats (16-byte aligned) from a cluster peer's shared memory.
 __device__ __forceinline__ float4 ld_dsmem_v4(uint32_t addr) {
     float4 v;
