@@ -430,9 +430,7 @@ PrefixPlan prefix_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t pr
     PrefixPlan p = {};
     p.dim = D <= 64 ? 64 : 128;
     p.all_rows = B * Hq;
-    // Worth its launch and its parts where it saves reading this many bytes.
-    constexpr int64_t kWorth = int64_t(16) << 20;
-    if (B < 2 || prefix < kKeys || (B - 1) * prefix < kWorth / (2 * Hkv * D)) return p;
+    if (B < 2 || prefix < kKeys) return p;
     const int64_t tpt = kRows / (Hq / Hkv);
     p.row_blocks = (B + 2 * tpt - 1) / (2 * tpt);
     const int64_t tiles = (prefix + kKeys - 1) / kKeys, items = p.row_blocks * Hkv;
@@ -441,6 +439,18 @@ PrefixPlan prefix_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t pr
     p.cluster = splits >= kMaxCluster ? kMaxCluster : splits >= 2 ? 2 : 1;
     splits = splits / p.cluster * p.cluster;
     p.tiles = static_cast<int>((tiles + splits - 1) / splits);
+    // Worth it where it is faster than the decode kernel on the same tokens, by
+    // what both were measured to need (page size 16, 300 tokens beside the
+    // prefix): that one reads B times the prefix, out of L2 mostly, at 8.6
+    // bytes/ps with 8 heads of 128, 5 with heads of 64; this one costs 18 us
+    // and 2.4 us a key tile of a CTA.  At 32/8 heads of 128, own reading
+    // against this: B = 16, 8192 tokens 45 / 35 us, 2048 tokens 22 / 29; B = 64,
+    // 2048 tokens 43 / 31, 512 tokens 21 / 29; B = 4, 32768 tokens 44 / 59.
+    const double own_us = static_cast<double>(B) * prefix * 2 * Hkv * D / (D > 64 ? 8.6e6 : 5.0e6);
+    if (own_us < 18.0 + 2.4 * p.tiles) {
+        p.tiles = 0;
+        return p;
+    }
     // whole clusters (the last parts may be empty), and no empty ones
     const int64_t used = (tiles + p.tiles - 1) / p.tiles;
     p.splits = static_cast<int>((used + p.cluster - 1) / p.cluster * p.cluster);

@@ -349,9 +349,10 @@ PREFIXES = [([300, 310, 257, 256], 8, 2, 64, 16, 256), ([1030] * 5, 32, 8, 128, 
             ([200 + i for i in range(70)], 4, 2, 96, 16, 192), ([700], 4, 1, 128, 64, 640),
             ([400 + i % 3 for i in range(150)], 2, 2, 64, 16, 400), ([257, 258], 7, 1, 112, 1, 250),
             ([2300 + 5 * i for i in range(20)], 16, 2, 128, 64, 2240), ([90, 90], 64, 1, 128, 16, 64),
-            ([530 + i % 70 for i in range(160)], 24, 8, 80, 16, 512), ([900 + i for i in range(130)], 8, 8, 128, 20, 880),
-            ([2000 + i for i in range(70)], 14, 2, 64, 1, 1999), ([3000 + 9 * i for i in range(9)], 32, 4, 128, 32, 2976),
-            ([1500 + i for i in range(12)], 64, 2, 112, 16, 1488)]
+            # (from here on enough requests for the shared-prefix kernel)
+            ([900 + i for i in range(170)], 8, 8, 128, 20, 880), ([710 + i % 70 for i in range(260)], 24, 8, 80, 16, 704),
+            ([2101 + i % 40 for i in range(200)], 14, 2, 64, 1, 2100), ([2020 + 9 * i for i in range(66)], 32, 8, 128, 32, 2016),
+            ([3710 + i % 7 for i in range(120)], 64, 2, 112, 16, 3700), ([4003 + i % 50 for i in range(100)], 32, 2, 128, 64, 4001)]
 
 
 @pytest.mark.parametrize("lens,Hq,Hkv,D,page,prefix", PREFIXES)
@@ -374,16 +375,16 @@ def test_decode_prefix_inside_a_page_and_beyond_every_request():
 
 
 def test_decode_long_shared_prefix_with_hidden_pages_and_short_requests():
-    lens = [1300 + 3 * i for i in range(30)]
-    args = cached(gen(31), lens, 32, 8, 64, 16, 1280)
+    lens = [1700 + 3 * i for i in range(80)]
+    args = cached(gen(31), lens, 32, 8, 64, 16, 1696)
     args[5][0, 3] = -1               # a page of the shared part that does not exist
     args[5][0, 79] = 2 ** 31 - 1
     args[6][4], args[6][5], args[6][6], args[6][7] = 0, 1, 1000, -3
-    check_decode(args, 16, 1280)
+    check_decode(args, 16, 1696)
     args[0][2, 3] = 0                # a zero query: all weights alike
-    check_decode(args, 16, 1277)
+    check_decode(args, 16, 1677)
     args[5][0, :] = -1               # nothing of the shared part exists
-    check_decode(args, 16, 1280)
+    check_decode(args, 16, 1696)
 
 
 def test_decode_bad_pages_and_lengths_are_hidden():
