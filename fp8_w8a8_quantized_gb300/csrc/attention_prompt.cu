@@ -6,7 +6,8 @@
 // that share a key head lie next to one another, so a tile of 128 rows is
 // 128 / G tokens with all their heads, keys and values are read once for the
 // group, and short prompts fill the tile.  A CTA works on two such tiles (A
-// and B) and walks over the keys in tiles of 128:
+// and B; where prompts are short or few, on one, with two CTAs an SM) and
+// walks over the keys in tiles of 128:
 //   warps 0-7, 8-15 softmax of tile A and B: a warp holds 16 rows of S, four
 //                   lanes a row, writes P as bf16 over S, rescales O where
 //                   needed and finally writes the rows' output.  (Four warps a
@@ -25,6 +26,12 @@
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each: all 512.  While one tile is in
 // its softmax the tensor core works on the other one.
 //
+//   warp 19         finds the CTA's next item.  The grid has a CTA for each
+//                   item, the longest of a sequence first; a running CTA takes
+//                   over the next one that has not started (cluster launch
+//                   control), so that all end at about the same time.
+// (With one tile a CTA: softmax in warps 0-7, the others are warps 8-11.)
+//
 // A masked weight is 0, but 0 * inf is NaN: in tiles where some row masks some
 // key, warp 18 sets non-finite values to 0 in shared memory before the MMA
 // reads them and remembers that it did; the rows that do see such a value get
@@ -34,6 +41,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "attention_tile.cuh"
 #include "launch.h"
@@ -42,29 +50,8 @@
 namespace fp8k {
 namespace {
 
-constexpr int kStages = 5;
-constexpr int kMainWarps = 16;
-constexpr int kThreads = 32 * (kMainWarps + 4);
-constexpr int kMainRegs = 104, kSideRegs = 64;  // 512 x 104 + 128 x 64 = 640 x 96, the launch's
-constexpr int kClean = 4;       // (the ring holds two tiles of values at most)
-constexpr int kFlags = 4;       // items whose "values were set to 0" flag is kept
-
-struct Bars {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2][2], o_full[2];
-    uint64_t v_issued[kClean];  // such a tile of values is on its way (its stage's phase is current)
-    uint64_t v_clean[kClean];   // warp 18 is done with it
-    uint64_t drain;
-    uint32_t tmem_base;
-    int abort;
-    int dirty[kFlags];
-};
-
-template <int DP>
-constexpr size_t smem_bytes() {
-    return 1024 + (2 * kRows + kStages * kKeys) * DP * 2 + sizeof(Bars);
-}
+constexpr int kClean = 4;  // (the ring holds two tiles of values at most)
+constexpr int kFlags = 4;  // items whose "values were set to 0" flag is kept
 
 // A work item: the tokens of one sequence's block and one key head.
 struct Item {
@@ -73,25 +60,49 @@ struct Item {
     int head;        // key head
     int tiles[2];    // key tiles of query tile A and B (0: empty)
     int masked;      // first key tile in which some row masks some key
-    bool valid;
+    int valid;
 };
 
-// Item `n` of the launch.  Blocks of `per` = 2 * tokens_per_tile tokens are
-// numbered so that sequence b's begin at cu[b] / per + b (there is room for
-// all of them, with some numbers unused), the last block first, since it has
-// the most keys.
-//
-// CTAs take items in turn, every other round from the other end, so that
-// none gets the longer one each time.
-__device__ __forceinline__ int64_t turn_of(int64_t round) {
-    return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+// NQ: query tiles of a CTA.
+template <int DP, int NQ>
+struct Config {
+    static constexpr int kStages = NQ == 2 ? 5 : 2;
+    static constexpr int kMainWarps = 8 * NQ;
+    static constexpr int kThreads = 32 * (kMainWarps + 4);
+    static constexpr int kCtas = 3 - NQ;  // an SM
+    // 512 x 104 + 128 x 64 = 640 x 96 and 256 x 88 + 128 x 64 = 384 x 80, the launch's
+    static constexpr int kMainRegs = NQ == 2 ? 104 : 88, kSideRegs = 64;
+};
+
+template <int kStages>
+struct Bars {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2][2], o_full[2];
+    uint64_t v_issued[kClean];  // such a tile of values is on its way (its stage's phase is current)
+    uint64_t v_clean[kClean];   // warp 18 is done with it
+    uint64_t drain;
+    uint64_t item_full, item_empty, next_cta;
+    alignas(16) uint4 response;  // of the request for the next item
+    Item item;
+    uint32_t tmem_base;
+    int abort;
+    int dirty[kFlags];
+};
+
+template <int DP, int NQ>
+constexpr size_t smem_bytes() {
+    using C = Config<DP, NQ>;
+    return 1024 + (NQ * kRows + C::kStages * kKeys) * DP * 2 + sizeof(Bars<C::kStages>);
 }
 
-__device__ __forceinline__ Item find_item(int64_t n, int64_t blocks, const PromptArgs& a, int tpt) {
+// Item `n` of the launch.  Blocks of `per` tokens are numbered so that
+// sequence b's begin at cu[b] / per + b (there is room for all of them, with
+// some numbers unused), the last block first, since it has the most keys.
+__device__ __forceinline__ Item find_item(int64_t n, int64_t blocks, const PromptArgs& a, int tpt, int per) {
     Item it;
     const int64_t i = blocks - 1 - n / a.Hkv;
     it.head = static_cast<int>(n % a.Hkv);
-    const int per = 2 * tpt;
     const int T = static_cast<int>(a.T);
     // the last sequence whose base is <= i: 32 candidates a step
     int64_t lo = 0, count = a.B;
@@ -114,25 +125,28 @@ __device__ __forceinline__ Item find_item(int64_t n, int64_t blocks, const Promp
     const int64_t q0 = (i - (it.start / per + lo)) * per;
     it.valid = q0 >= 0 && q0 < it.len;
     it.q0 = static_cast<int>(q0);
-    const int end_a = min(it.q0 + tpt, it.len), end_b = min(it.q0 + 2 * tpt, it.len);
+    const int end_a = min(it.q0 + tpt, it.len), end_b = min(it.q0 + per, it.len);
     it.tiles[0] = (end_a + kKeys - 1) / kKeys;
-    it.tiles[1] = it.q0 + tpt < it.len ? (end_b + kKeys - 1) / kKeys : 0;
+    it.tiles[1] = end_b > it.q0 + tpt ? (end_b + kKeys - 1) / kKeys : 0;
     it.masked = it.q0 / kKeys;
     return it;
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DP, int NQ>
+__global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCtas)
     attention_prompt(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const PromptArgs a, int64_t blocks) {
+    using C = Config<DP, NQ>;
+    constexpr int kStages = C::kStages, kMainWarps = C::kMainWarps;
+    constexpr uint32_t kTmem = 256 * NQ;           // columns: S of the tiles, then O
     constexpr int kCols = DP / 64;                 // 64-element columns of a tile
     constexpr uint32_t kColBytes = 128 * 128;      // 128 rows of 128 bytes
     constexpr uint32_t kTile = kCols * kColBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* sQ = smem;                            // [2][kCols][128][128 B]
-    uint8_t* sKV = smem + 2 * kTile;               // [kStages][kCols][128][128 B]
-    Bars* bars = reinterpret_cast<Bars*>(sKV + kStages * kTile);
+    uint8_t* sQ = smem;                            // [NQ][kCols][128][128 B]
+    uint8_t* sKV = smem + NQ * kTile;              // [kStages][kCols][128][128 B]
+    auto* bars = reinterpret_cast<Bars<kStages>*>(sKV + kStages * kTile);
     const int warp = threadIdx.x >> 5, lane = lane_id();
     unsigned* status = a.status;
 
@@ -143,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < NQ; ++x) {
             mbar_init(&bars->s_full[x], 1);
             mbar_init(&bars->p_full[x][0], 8);
             mbar_init(&bars->p_full[x][1], 8);
@@ -154,6 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->v_clean[k], 1);
         }
         mbar_init(&bars->drain, 1);
+        mbar_init(&bars->item_full, 1);
+        mbar_init(&bars->item_empty, kMainWarps + 3);
+        mbar_init(&bars->next_cta, 1);
         bars->abort = 0;
         for (int f = 0; f < kFlags; ++f) bars->dirty[f] = 0;
         fence_mbar_init();
@@ -164,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmV);
     }
     if (warp == kMainWarps + 1) {
-        tmem_alloc(&bars->tmem_base, 512);
+        tmem_alloc(&bars->tmem_base, kTmem);
         tmem_relinquish();
     }
     pdl_launch_dependents();
@@ -176,15 +193,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait_primary();
 
     const int G = a.Hq / a.Hkv, tpt = kRows / G;
-    const int64_t items = blocks * a.Hkv;
+    // The next item, for a whole warp: false where there is none (left).
+    uint32_t items_taken = 0;
+    auto take_item = [&](Item& it, bool& ok) {
+        if (!(ok = warp_ready(&bars->item_full, items_taken & 1u, abort_flag, status))) return false;
+        const volatile Item& from = bars->item;
+        it.start = from.start, it.len = from.len, it.q0 = from.q0, it.head = from.head;
+        it.tiles[0] = from.tiles[0], it.tiles[1] = from.tiles[1];
+        it.masked = from.masked, it.valid = from.valid;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_empty);
+        ++items_taken;
+        return it.valid != 0;
+    };
 
     if (warp < kMainWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMainRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMainRegs));
         // ------------------------------------------------ softmax and output
         const int x = warp >> 3, g = lane >> 2, t = lane & 3;  // query tile A or B
         const int row0 = (warp & 3) * 32 + (warp >> 2 & 1) * 16 + g;  // this lane's rows: row0, row0 + 8
         const uint32_t lanes = static_cast<uint32_t>(row0 - g) << 16;
-        const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * 128;
+        const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + kTmem / 2 + x * 128;
         const float c[2] = {a.scale * kLog2e, a.scale * kLog2e};
         uint32_t s_phase = 0, o_phase = 0;
         int item_no = 0;
@@ -195,11 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tok[e] = (row0 + 8 * e) / G;
             head_in[e] = row0 + 8 * e - tok[e] * G;
         }
-        for (int64_t r = 0; ok && r * gridDim.x < items; ++r) {
-            const int64_t n = turn_of(r);
-            if (n >= items) continue;
-            const Item it = find_item(n, blocks, a, tpt);
-            if (!it.valid) continue;
+        Item it;
+        while (ok && take_item(it, ok)) {
             int my_tok[2];
             bool mine[2];
 #pragma unroll
@@ -280,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++item_no;
         }
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kSideRegs));
       if (warp == kMainWarps) {
         // ------------------------------------------------ TMA loads
         uint32_t loads = 0, issued = 0, q_loads = 0;
@@ -296,10 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++loads;
             return true;
         };
-        auto load_item = [&](const Item& it) {
+        Item it;
+        auto load_item = [&]() {
             if (!wait_bounded(&bars->q_empty, (q_loads & 1u) ^ 1u, abort_flag, status)) return false;
-            mbar_arrive_expect_tx(&bars->q_full, 2u * kCols * 128u * static_cast<uint32_t>(G * tpt));
-            for (int x = 0; x < 2; ++x)
+            mbar_arrive_expect_tx(&bars->q_full, NQ * kCols * 128u * static_cast<uint32_t>(G * tpt));
+            for (int x = 0; x < NQ; ++x)
                 for (int y = 0; y < kCols; ++y)
                     tma_load_3d(sQ + x * kTile + y * kColBytes, &tmQ, &bars->q_full, 64 * y, it.head * G,
                                 it.start + it.q0 + x * tpt);
@@ -315,12 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return true;
         };
-        for (int64_t r = 0; ok && r * gridDim.x < items; ++r) {
-            const int64_t n = turn_of(r);
-            if (n >= items) continue;
-            const Item it = find_item(n, blocks, a, tpt);
-            if (!it.valid) continue;
-            if (lane == 0) ok = load_item(it);
+        while (ok && take_item(it, ok)) {
+            if (lane == 0) ok = load_item();
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
         if (!ok && lane == 0) {  // gave up: let the copies in flight land before the memory goes
@@ -345,13 +368,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             return warp_ready(bar, parity & 1u, abort_flag, status);
         };
         auto landed = [&](uint32_t k) { return ready(&bars->full[k % kStages], k / kStages); };
-        for (int64_t r = 0; ok && r * gridDim.x < items; ++r) {
-            const int64_t n = turn_of(r);
-            if (n >= items) continue;
-            const Item it = find_item(n, blocks, a, tpt);
-            if (!it.valid) continue;
+        Item it;
+        while (ok && take_item(it, ok)) {
             const int tiles_a = uniform(it.tiles[0]), tiles_b = uniform(it.tiles[1]);
             const int tiles = max(tiles_a, tiles_b), masked = uniform(it.masked);
+            // keys of tile j + 1 and (clean) values of tile j
+            auto next_there = [&](int j) {
+                if (j + 1 < tiles && !landed(at + 2 * j + 2)) return false;
+                if (j >= tiles) return true;
+                if (!landed(at + 2 * j + 1)) return false;
+                if (j < masked) return true;
+                const uint32_t c = cleaned++;
+                return ready(&bars->v_clean[c % kClean], c / kClean);
+            };
             if (!(ok = ready(&bars->q_full, q_phase) && landed(at))) break;
             q_phase ^= 1u;
             for (int j = 0; j <= tiles; ++j) {
@@ -361,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t vd = sdesc_nmajor_sw128(base_kv + uniform(vv) * kTile, kColBytes);
                 tc_fence_after();
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t tS = tm + x * 128, tO = tm + 256 + x * 128;
+                for (int x = 0; x < NQ; ++x) {
+                    const uint32_t tS = tm + x * 128, tO = tm + kTmem / 2 + x * 128;
                     const uint64_t qd = sdesc_kmajor_sw128(base_q + x * kTile);
                     const int mine = x == 0 ? tiles_a : tiles_b;
                     if (j > 0 && j - 1 < mine) {
@@ -392,17 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         __syncwarp();
                     }
-                    if (x == 1) break;
                     // What the next turn reads is there by now, as a rule; a look takes some 100
                     // clocks all the same, which pass while the tensor core is busy with tile A.
-                    if (j + 1 < tiles && !(ok = landed(at + 2 * j + 2))) break;
-                    if (j < tiles) {
-                        if (!(ok = landed(at + 2 * j + 1))) break;
-                        if (j >= masked) {
-                            if (!(ok = ready(&bars->v_clean[cleaned % kClean], cleaned / kClean))) break;
-                            ++cleaned;
-                        }
-                    }
+                    if (NQ == 2 && x == 0 && j + 1 < tiles && j < masked && !(ok = next_there(j))) break;
                 }
                 if (!ok) break;
                 if (elect_one()) {
@@ -411,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 1 == tiles) mma_commit(&bars->q_empty);
                 }
                 __syncwarp();
+                if ((NQ == 1 || j + 1 >= tiles || j >= masked) && !(ok = next_there(j))) break;
             }
             at += 2 * tiles;
         }
@@ -425,11 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t at = 0, cleaned = 0;
         int item_no = 0;
         bool ok = true;
-        for (int64_t r = 0; ok && r * gridDim.x < items; ++r) {
-            const int64_t n = turn_of(r);
-            if (n >= items) continue;
-            const Item it = find_item(n, blocks, a, tpt);
-            if (!it.valid) continue;
+        Item it;
+        while (ok && take_item(it, ok)) {
             const int tiles = max(it.tiles[0], it.tiles[1]);
             bool dirty = false;
             for (int j = it.masked; j < tiles; ++j) {
@@ -466,53 +485,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             at += 2 * tiles;
             ++item_no;
         }
+      } else {
+        // ------------------------------------------------ items
+        int64_t n = blockIdx.x;
+        uint32_t published = 0, asked = 0;
+        while (true) {
+            Item it = {};
+            if (n >= 0) it = find_item(n, blocks, a, tpt, NQ * tpt);
+            if (n < 0 || it.valid) {  // (an invalid one tells that there are no more)
+                if (!warp_ready(&bars->item_empty, (published & 1u) ^ 1u, abort_flag, status)) break;
+                if (lane == 0) bars->item = it;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->item_full);
+                ++published;
+                if (n < 0) break;
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars->next_cta, 16);
+                cancel_next_cta(&bars->response, &bars->next_cta);
+            }
+            __syncwarp();
+            if (!warp_ready(&bars->next_cta, asked & 1u, abort_flag, status)) break;
+            ++asked;
+            n = cancelled_cta(&bars->response);
+            fence_proxy_async_smem();  // (read, before the next answer is written)
+            __syncwarp();
+        }
       }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kMainWarps + 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, kTmem);
     }
 }
 
-template <int DP>
-cudaError_t launch_dim(const PromptArgs& a, cudaStream_t st) {
+template <int DP, int NQ>
+cudaError_t launch_tiles(const PromptArgs& a, cudaStream_t st) {
+    using C = Config<DP, NQ>;
     const int G = a.Hq / a.Hkv, tpt = kRows / G;
-    const int64_t blocks = a.T / (2 * tpt) + a.B;
+    const int64_t blocks = a.T / (NQ * tpt) + a.B, items = blocks * a.Hkv;
+    if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
     CUtensorMap tq, tk, tv;
     const uint64_t T = static_cast<uint64_t>(a.T), D = static_cast<uint64_t>(a.D);
     if (!encode_tmap_heads(&tq, a.q, T, a.Hq, D, 2 * a.ldq, 64, G, tpt) ||
         !encode_tmap_heads(&tk, a.k, T, a.Hkv, D, 2 * a.ldk, 64, 1, kKeys) ||
         !encode_tmap_heads(&tv, a.v, T, a.Hkv, D, 2 * a.ldv, 64, 1, kKeys))
         return cudaErrorInvalidValue;
-    const int64_t items = blocks * a.Hkv;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(items < a.num_sms ? items : a.num_sms));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<DP>();
+    cfg.gridDim = dim3(static_cast<unsigned>(items));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<DP, NQ>();
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_prompt<DP>, tq, tk, tv, a, blocks);
+    return cudaLaunchKernelEx(&cfg, attention_prompt<DP, NQ>, tq, tk, tv, a, blocks);
+}
+
+template <int DP, int NQ>
+cudaError_t prepare() {
+    return cudaFuncSetAttribute(attention_prompt<DP, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(smem_bytes<DP, NQ>()));
 }
 
 }  // namespace
 
 cudaError_t launch_attention_prompt(const PromptArgs& a, cudaStream_t st) {
-    return a.D <= 64 ? launch_dim<64>(a, st) : launch_dim<128>(a, st);
+    const bool one = a.T <= 256 * a.B;
+    if (a.D <= 64) return one ? launch_tiles<64, 1>(a, st) : launch_tiles<64, 2>(a, st);
+    return one ? launch_tiles<128, 1>(a, st) : launch_tiles<128, 2>(a, st);
 }
 
 cudaError_t prepare_attention_prompt() {
-    const cudaError_t e = cudaFuncSetAttribute(attention_prompt<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem_bytes<64>()));
-    return e != cudaSuccess ? e
-                            : cudaFuncSetAttribute(attention_prompt<128>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem_bytes<128>()));
+    for (cudaError_t e : {prepare<64, 1>(), prepare<64, 2>(), prepare<128, 1>(), prepare<128, 2>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
 }  // namespace fp8k

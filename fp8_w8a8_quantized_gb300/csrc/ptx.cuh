@@ -701,4 +701,33 @@ __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// ---------------------------------------------------------------------------
+// cluster launch control: a running CTA takes over one that has not started
+// ---------------------------------------------------------------------------
+// Asks for a CTA of this grid that is still to be launched; the 16-byte answer
+// goes to `response` in shared memory and is counted on `bar`.
+__device__ __forceinline__ void cancel_next_cta(void* response, uint64_t* bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(response)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// blockIdx.x of the CTA that was taken over, or -1: there was none left.
+__device__ __forceinline__ int64_t cancelled_cta(const void* response) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(response))
+        : "memory");
+    return got ? static_cast<int64_t>(x) : -1;
+}
+
 }  // namespace fp8k
