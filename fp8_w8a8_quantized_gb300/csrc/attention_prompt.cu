@@ -132,6 +132,58 @@ __device__ __forceinline__ Item find_item(int64_t n, int64_t blocks, const Promp
     return it;
 }
 
+// Adds to O the infinities and NaN of the values that a lane's rows see and
+// that warp 18 took out of shared memory (rare, and slow): tokens `first` ..
+// last of the sequence's values v.
+template <int DP>
+__device__ __noinline__ void add_unfinite(uint32_t tO, const uint16_t* v, int64_t ldv, int D, int first, int last0,
+                                          int last1) {
+    const int t = lane_id() & 3;
+#pragma unroll 1
+    for (int b = 0; b < DP / 32; ++b) {
+        uint32_t o[16];
+        __syncwarp();
+        tmem_ld_16x256b_x4(tO + 32 * b, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[i]));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            for (int j = first; j <= (e ? last1 : last0); ++j) {
+                const uint16_t* at = v + j * ldv + 32 * b + 2 * t;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int d = 8 * (i >> 1) + (i & 1);
+                    if (32 * b + 2 * t + d < D) {
+                        const float z = __uint_as_float(static_cast<uint32_t>(at[d]) << 16);
+                        uint32_t& to = o[4 * (i >> 1) + 2 * e + (i & 1)];
+                        if (!isfinite(z)) to = __float_as_uint(__uint_as_float(to) + z);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        tmem_st_16x256b_x4(tO + 32 * b, o);
+    }
+    tmem_st_wait();
+}
+
+// w[i] of lane t -> w[t] of lane i, within each quad of lanes.
+__device__ __forceinline__ void transpose_quad(uint32_t (&w)[4], int t) {
+    // the 2 x 2 blocks' off-diagonal, then within the blocks
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        const bool up = t & d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & d) continue;
+            const uint32_t give = up ? w[i] : w[i | d];
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, d);
+            if (up) w[i] = got; else w[i | d] = got;
+        }
+    }
+}
+
 template <int DP, int NQ>
 __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCtas)
     attention_prompt(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -255,50 +307,39 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
                 if (!(ok = warp_ready(&bars->o_full[x], o_phase, abort_flag, status))) break;
                 o_phase ^= 1u;
                 tc_fence_after();
+                if (*reinterpret_cast<volatile int*>(&bars->dirty[item_no % kFlags]) != 0)
+                    add_unfinite<DP>(tO, a.v + it.start * a.ldv + static_cast<int64_t>(it.head) * a.D, a.ldv, a.D,
+                                     it.masked * kKeys, mine[0] ? my_tok[0] : -1, mine[1] ? my_tok[1] : -1);
                 float inv[2];
-                uint16_t* dst[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float sum = rows.sum(e);
                     inv[e] = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    dst[e] = a.out + (it.start + my_tok[e]) * a.ldo +
-                             static_cast<int64_t>(it.head * G + head_in[e]) * a.D + 2 * t;
                 }
-                const bool dirty = *reinterpret_cast<volatile int*>(&bars->dirty[item_no % kFlags]) != 0;
-#pragma unroll 1
-                for (int b = 0; b < DP / 32; ++b) {
-                    uint32_t o[16];
-                    __syncwarp();
-                    tmem_ld_16x256b_x4(tO + 32 * b, o);
-                    tmem_ld_wait();
+                uint32_t o[DP / 32][16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        asm volatile("" : "+r"(o[i]));
-                        o[i] = __float_as_uint(__uint_as_float(o[i]) * inv[i >> 1 & 1]);
-                    }
+                for (int b = 0; b < DP / 32; ++b) tmem_ld_16x256b_x4(tO + 32 * b, o[b]);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (!mine[e]) continue;
-                        if (dirty) {
-                            for (int j = it.masked * kKeys; j <= my_tok[e]; ++j) {
-                                const uint16_t* v = a.v + (it.start + j) * a.ldv +
-                                                    static_cast<int64_t>(it.head) * a.D + 32 * b + 2 * t;
+                for (int b = 0; b < DP / 32; ++b)
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const int d = 8 * (i >> 1) + (i & 1);
-                                    if (32 * b + 2 * t + d < a.D) {
-                                        const float z = __uint_as_float(static_cast<uint32_t>(v[d]) << 16);
-                                        uint32_t& to = o[4 * (i >> 1) + 2 * e + (i & 1)];
-                                        if (!isfinite(z)) to = __float_as_uint(__uint_as_float(to) + z);
-                                    }
-                                }
-                            }
-                        }
+                    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[b][i]));  // (no use before the wait)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint16_t* dst = a.out + (it.start + my_tok[e]) * a.ldo +
+                                    static_cast<int64_t>(it.head * G + head_in[e]) * a.D + 8 * t;
+#pragma unroll
+                    for (int b = 0; b < DP / 32; ++b) {
+                        // w[i]: elements 8 i + 2 t, + 1; the quad's lanes exchange them so
+                        // that lane t has elements 8 t .. 8 t + 7 for one 16-byte store
+                        uint32_t w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (32 * b + 8 * i < a.D)
-                                *reinterpret_cast<uint32_t*>(dst[e] + 32 * b + 8 * i) =
-                                    pack_bf16(__uint_as_float(o[4 * i + 2 * e]), __uint_as_float(o[4 * i + 2 * e + 1]));
+                            w[i] = pack_bf16(__uint_as_float(o[b][4 * i + 2 * e]) * inv[e],
+                                             __uint_as_float(o[b][4 * i + 2 * e + 1]) * inv[e]);
+                        transpose_quad(w, t);
+                        if (mine[e] && 32 * b + 8 * t < a.D)
+                            *reinterpret_cast<uint4*>(dst + 32 * b) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 __syncwarp();
@@ -555,7 +596,11 @@ cudaError_t prepare() {
 }  // namespace
 
 cudaError_t launch_attention_prompt(const PromptArgs& a, cudaStream_t st) {
-    const bool one = a.T <= 256 * a.B;
+    // Too few items for the SMs: smaller ones.  (32 heads on 8 of 128: one prompt
+    // of 128 tokens 7.3 us with one tile a CTA, 9.3 with two; of 1024 tokens 23.6
+    // and 20.3, of 4096 tokens 143 and 119.)
+    const int64_t two_tiles = (a.T / (2 * (kRows / (a.Hq / a.Hkv))) + a.B) * a.Hkv;
+    const bool one = two_tiles <= a.num_sms / 2;
     if (a.D <= 64) return one ? launch_tiles<64, 1>(a, st) : launch_tiles<64, 2>(a, st);
     return one ? launch_tiles<128, 1>(a, st) : launch_tiles<128, 2>(a, st);
 }
