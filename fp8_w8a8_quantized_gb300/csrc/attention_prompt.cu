@@ -409,72 +409,88 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
             return warp_ready(bar, parity & 1u, abort_flag, status);
         };
         auto landed = [&](uint32_t k) { return ready(&bars->full[k % kStages], k / kStages); };
+        auto k_desc = [&](uint32_t stage) { return sdesc_kmajor_sw128(base_kv + uniform(stage) * kTile); };
+        auto v_desc = [&](uint32_t stage) {
+            return sdesc_nmajor_sw128(base_kv + uniform(stage) * kTile, kColBytes);
+        };
         Item it;
         while (ok && take_item(it, ok)) {
             const int tiles_a = uniform(it.tiles[0]), tiles_b = uniform(it.tiles[1]);
             const int tiles = max(tiles_a, tiles_b), masked = uniform(it.masked);
-            // keys of tile j + 1 and (clean) values of tile j
-            auto next_there = [&](int j) {
-                if (j + 1 < tiles && !landed(at + 2 * j + 2)) return false;
-                if (j >= tiles) return true;
-                if (!landed(at + 2 * j + 1)) return false;
-                if (j < masked) return true;
-                const uint32_t c = cleaned++;
-                return ready(&bars->v_clean[c % kClean], c / kClean);
-            };
-            if (!(ok = ready(&bars->q_full, q_phase) && landed(at))) break;
+            // The tensor core takes about 64 clocks an MMA and holds some five of
+            // them; what the warp does beside issuing (a look at a barrier: 100
+            // clocks or more) is where MMAs are queued up, and between S of tile B
+            // and P V of tile A there is nothing but the wait for P.
+            if (!(ok = ready(&bars->q_full, q_phase))) break;
             q_phase ^= 1u;
-            for (int j = 0; j <= tiles; ++j) {
-                // P V of tile j - 1 and S of tile j; what they read has landed
-                const uint32_t kk = (at + 2 * j) % kStages, vv = (at + 2 * j + kStages - 1) % kStages;
-                const uint64_t kd = sdesc_kmajor_sw128(base_kv + uniform(kk) * kTile);
-                const uint64_t vd = sdesc_nmajor_sw128(base_kv + uniform(vv) * kTile, kColBytes);
-                tc_fence_after();
-#pragma unroll
-                for (int x = 0; x < NQ; ++x) {
-                    const uint32_t tS = tm + x * 128, tO = tm + kTmem / 2 + x * 128;
-                    const uint64_t qd = sdesc_kmajor_sw128(base_q + x * kTile);
-                    const int mine = x == 0 ? tiles_a : tiles_b;
-                    if (j > 0 && j - 1 < mine) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!(ok = ready(&bars->p_full[x][h], p_phase[x]))) break;
-                            tc_fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int i = 4 * h; i < 4 * h + 4; ++i)
-                                    mma_f16_ts(tO, tS + 8 * i, vd + i * (2048 >> 4), idO, !(j == 1 && i == 0));
-                                if (h == 1 && j == mine) mma_commit(&bars->o_full[x]);
-                            }
-                            __syncwarp();
-                        }
-                        if (!ok) break;
-                        p_phase[x] ^= 1u;
-                    }
-                    if (j < mine) {
-                        if (elect_one()) {
-#pragma unroll
-                            for (int i = 0; i < DP / 16; ++i) {
-                                const uint32_t off = ((i / 4) * kColBytes + (i % 4) * 32) >> 4;
-                                mma_f16(tS, qd + off, kd + off, idS, i != 0);
-                            }
-                            mma_commit(&bars->s_full[x]);
-                        }
-                        __syncwarp();
-                    }
-                    // What the next turn reads is there by now, as a rule; a look takes some 100
-                    // clocks all the same, which pass while the tensor core is busy with tile A.
-                    if (NQ == 2 && x == 0 && j + 1 < tiles && j < masked && !(ok = next_there(j))) break;
-                }
-                if (!ok) break;
+            uint32_t kk = at % kStages, vv = 0;  // stages of K of tile j, V of tile j - 1
+            uint64_t kd = k_desc(kk), vd = 0;
+            auto release = [&](int j) {  // what turn j has read
                 if (elect_one()) {
                     if (j > 0) mma_commit(&bars->empty[vv]);
                     if (j < tiles) mma_commit(&bars->empty[kk]);
-                    if (j + 1 == tiles) mma_commit(&bars->q_empty);
                 }
                 __syncwarp();
-                if ((NQ == 1 || j + 1 >= tiles || j >= masked) && !(ok = next_there(j))) break;
+            };
+            // Values of tile j - 1 and keys of tile j for query tile x.
+            auto turn = [&](int x, int j) {
+                const uint32_t tS = tm + x * 128, tO = tm + kTmem / 2 + x * 128;
+                const int mine = x == 0 ? tiles_a : tiles_b;
+                if (j > 0 && j - 1 < mine) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!ready(&bars->p_full[x][h], p_phase[x])) return false;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = 4 * h; i < 4 * h + 4; ++i)
+                                mma_f16_ts(tO, tS + 8 * i, vd + i * (2048 >> 4), idO, !(j == 1 && i == 0));
+                            if (h == 1 && j == mine) mma_commit(&bars->o_full[x]);
+                        }
+                        __syncwarp();
+                    }
+                    p_phase[x] ^= 1u;
+                }
+                if (x == 0 && j < tiles && !landed(at + 2 * j)) return false;
+                if (j < mine) {
+                    tc_fence_after();
+                    const uint64_t qd = sdesc_kmajor_sw128(base_q + x * kTile);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i) {
+                            const uint32_t off = ((i / 4) * kColBytes + (i % 4) * 32) >> 4;
+                            mma_f16(tS, qd + off, kd + off, idS, i != 0);
+                        }
+                        mma_commit(&bars->s_full[x]);
+                    }
+                    __syncwarp();
+                }
+                return true;
+            };
+            for (int j = 0; j <= tiles; ++j) {
+                if (!(ok = turn(0, j))) break;
+                const uint32_t next_k = (at + 2 * j + 2) % kStages, next_v = (at + 2 * j + 1) % kStages;
+                const uint64_t next_kd = k_desc(next_k), next_vd = v_desc(next_v);
+                if (NQ == 2) {
+                    // the values that the next turn reads (with a look at them, they may take longer)
+                    if (j < tiles && j < masked && !(ok = landed(at + 2 * j + 1))) break;
+                    if (!(ok = turn(1, j))) break;
+                }
+                release(j);
+                if (j + 1 == tiles) {
+                    if (elect_one()) mma_commit(&bars->q_empty);
+                    __syncwarp();
+                }
+                if (j < tiles && (NQ == 1 || j >= masked)) {
+                    if (!(ok = landed(at + 2 * j + 1))) break;
+                    if (j >= masked) {
+                        if (!(ok = ready(&bars->v_clean[cleaned % kClean], cleaned / kClean))) break;
+                        ++cleaned;
+                    }
+                }
+                kk = next_k, vv = next_v, kd = next_kd, vd = next_vd;
             }
+            if (!ok) break;
             at += 2 * tiles;
         }
         __syncwarp();
