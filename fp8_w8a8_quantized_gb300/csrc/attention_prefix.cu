@@ -248,14 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
         for (int j = 0; ok && j <= n; ++j) {
             // P V of tile j - 1 and S of tile j; what they read is there
             const uint32_t kk = 2 * j % kStages, vv = (2 * j + kStages - 1) % kStages;
-            const uint64_t kd = sdesc_kmajor_sw128(base_kv + uniform(kk) * kTile);
-            const uint64_t vd = sdesc_nmajor_sw128(base_kv + uniform(vv) * kTile, kColBytes);
+            const uint32_t kd = desc_kmajor(base_kv + uniform(kk) * kTile);
+            const uint32_t vd = desc_nmajor(base_kv + uniform(vv) * kTile, kColBytes);
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 if (x < both) {
                     const uint32_t dS = tm + x * 128, dO = tm + 256 + x * 128;
-                    const uint64_t qd = sdesc_kmajor_sw128(base_q + x * kTile);
+                    const uint32_t qd = desc_kmajor(base_q + x * kTile);
                     if (j > 0) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {

@@ -14,22 +14,22 @@
 //                   tile, a lane a row, took 1450 clocks a tile, mostly
 //                   latency; the tensor core waits for S -> P of one tile
 //                   once it is done with the other one's MMAs, 1024 clocks);
-//   warp 16         TMA loads: Q once per item, K and V through a ring;
-//   warp 17         issues the MMAs: S = Q K^T (both from shared memory) and
-//                   O += P V (P from tensor memory), tile A's and tile B's in
-//                   turn, so that one tile is in its softmax while the tensor
-//                   core has the other one (with an issuer for each tile they
-//                   fell into step and both waited).  P comes in two halves,
-//                   the MMAs of the first 64 keys start with the first;
-//   warp 18         looks for infinities and NaN in values that some row of
-//                   the item must not see (below).
-// TMEM: S_A, S_B, O_A, O_B, 128 columns each: all 512.  While one tile is in
-// its softmax the tensor core works on the other one.
-//
-//   warp 19         finds the CTA's next item.  The grid has a CTA for each
+//   warp 16         finds the CTA's items and loads them by TMA: Q once per
+//                   item, K and V through a ring.  The grid has a CTA for each
 //                   item, the longest of a sequence first; a running CTA takes
 //                   over the next one that has not started (cluster launch
-//                   control), so that all end at about the same time.
+//                   control), so that all end at about the same time;
+//   warps 17, 19    issue the MMAs of tile A and of tile B: S = Q K^T (both
+//                   from shared memory) and O += P V (P from tensor memory).
+//                   They take turns, so that one tile is in its softmax while
+//                   the tensor core has the other one (without turns the tiles
+//                   fell into step and both waited).  An MMA takes the tensor
+//                   core 64 clocks and a thread about 50 to issue, and a look
+//                   at a barrier 100: a single issuer for both tiles took 2830
+//                   clocks for 2048 clocks of MMAs.  P comes in two halves, the
+//                   MMAs of the first 64 keys start with the first;
+//   warp 18         looks for infinities and NaN in values that some row of
+//                   the item must not see (below).
 // (With one tile a CTA: softmax in warps 0-7, the others are warps 8-11.)
 //
 // A masked weight is 0, but 0 * inf is NaN: in tiles where some row masks some
@@ -77,11 +77,12 @@ struct Config {
 template <int kStages>
 struct Bars {
     uint64_t full[kStages], empty[kStages];
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2][2], o_full[2];
     uint64_t v_issued[kClean];  // such a tile of values is on its way (its stage's phase is current)
     uint64_t v_clean[kClean];   // warp 18 is done with it
-    uint64_t drain;
+    uint64_t turn[2];  // an issuer may go on
+    uint64_t drain[2];
     uint64_t item_full, item_empty, next_cta;
     alignas(16) uint4 response;  // of the request for the next item
     Item item;
@@ -205,23 +206,24 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
+            mbar_init(&bars->empty[s], NQ);  // (of each issuer)
         }
-        mbar_init(&bars->q_full, 1);
-        mbar_init(&bars->q_empty, 1);
         for (int x = 0; x < NQ; ++x) {
             mbar_init(&bars->s_full[x], 1);
             mbar_init(&bars->p_full[x][0], 8);
             mbar_init(&bars->p_full[x][1], 8);
             mbar_init(&bars->o_full[x], 1);
+            mbar_init(&bars->q_full[x], 1);
+            mbar_init(&bars->q_empty[x], 1);
+            mbar_init(&bars->turn[x], 1);
+            mbar_init(&bars->drain[x], 1);
         }
         for (int k = 0; k < kClean; ++k) {
             mbar_init(&bars->v_issued[k], 1);
             mbar_init(&bars->v_clean[k], 1);
         }
-        mbar_init(&bars->drain, 1);
         mbar_init(&bars->item_full, 1);
-        mbar_init(&bars->item_empty, kMainWarps + 3);
+        mbar_init(&bars->item_empty, kMainWarps + 1 + NQ);
         mbar_init(&bars->next_cta, 1);
         bars->abort = 0;
         for (int f = 0; f < kFlags; ++f) bars->dirty[f] = 0;
@@ -350,8 +352,32 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kSideRegs));
       if (warp == kMainWarps) {
         // ------------------------------------------------ TMA loads
-        uint32_t loads = 0, issued = 0, q_loads = 0;
+        uint32_t loads = 0, issued = 0, q_loads = 0, q_issued[2] = {0, 0}, published = 0, asked = 0;
         bool ok = true;
+        Item it;
+        auto ask = [&]() {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars->next_cta, 16);
+                cancel_next_cta(&bars->response, &bars->next_cta);
+            }
+            __syncwarp();
+        };
+        auto answer = [&](int64_t& n) {
+            if (!warp_ready(&bars->next_cta, asked & 1u, abort_flag, status)) return false;
+            ++asked;
+            n = cancelled_cta(&bars->response);
+            fence_proxy_async_smem();  // (read, before the next answer is written)
+            __syncwarp();
+            return true;
+        };
+        auto publish = [&]() {  // (an invalid item tells that there are no more)
+            if (!warp_ready(&bars->item_empty, (published & 1u) ^ 1u, abort_flag, status)) return false;
+            if (lane == 0) bars->item = it;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->item_full);
+            ++published;
+            return true;
+        };
         auto tile = [&](const CUtensorMap* tm, int head, int tokens) {
             const uint32_t stage = loads % kStages;
             if (!wait_bounded(&bars->empty[stage], (loads / kStages & 1u) ^ 1u, abort_flag, status))
@@ -363,18 +389,23 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
             ++loads;
             return true;
         };
-        Item it;
+        auto queries = [&](int x) {
+            if (!wait_bounded(&bars->q_empty[x], (q_loads & 1u) ^ 1u, abort_flag, status)) return false;
+            mbar_arrive_expect_tx(&bars->q_full[x], kCols * 128u * static_cast<uint32_t>(G * tpt));
+            for (int y = 0; y < kCols; ++y)
+                tma_load_3d(sQ + x * kTile + y * kColBytes, &tmQ, &bars->q_full[x], 64 * y, it.head * G,
+                            it.start + it.q0 + x * tpt);
+            ++q_issued[x];
+            return true;
+        };
         auto load_item = [&]() {
-            if (!wait_bounded(&bars->q_empty, (q_loads & 1u) ^ 1u, abort_flag, status)) return false;
-            mbar_arrive_expect_tx(&bars->q_full, NQ * kCols * 128u * static_cast<uint32_t>(G * tpt));
-            for (int x = 0; x < NQ; ++x)
-                for (int y = 0; y < kCols; ++y)
-                    tma_load_3d(sQ + x * kTile + y * kColBytes, &tmQ, &bars->q_full, 64 * y, it.head * G,
-                                it.start + it.q0 + x * tpt);
-            ++q_loads;
             const int tiles = max(it.tiles[0], it.tiles[1]);
             for (int j = 0; j < tiles; ++j) {
+                // the queries of tile A are wanted first: before the last turn's of tile B are done with
+                if (j == 0 && !queries(0)) return false;
                 if (!tile(&tmK, it.head, it.start + j * kKeys)) return false;
+                if (j == 0 && NQ == 2 && !queries(1)) return false;
+                if (j == 0) ++q_loads;
                 if (!tile(&tmV, it.head, it.start + j * kKeys)) return false;
                 if (j >= it.masked) {
                     mbar_arrive(&bars->v_issued[issued % kClean]);
@@ -383,78 +414,90 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
             }
             return true;
         };
-        while (ok && take_item(it, ok)) {
+        int64_t n = blockIdx.x;
+        while (true) {
+            // the next item: its number may belong to no block of any sequence
+            while (n >= 0 && !(it = find_item(n, blocks, a, tpt, NQ * tpt)).valid) {
+                ask();
+                if (!(ok = answer(n))) break;
+            }
+            if (!ok) break;
+            if (n < 0) it.valid = 0;
+            if (!(ok = publish()) || n < 0) break;
+            ask();  // (answered while this one is loaded)
             if (lane == 0) ok = load_item();
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            if (!(ok = answer(n))) break;
         }
         if (!ok && lane == 0) {  // gave up: let the copies in flight land before the memory goes
             for (uint32_t i = 1; i <= kStages && i <= loads; ++i) {
                 const uint32_t k = loads - i;
                 wait_landed(&bars->full[k % kStages], k / kStages & 1u, status);
             }
-            if (q_loads) wait_landed(&bars->q_full, (q_loads - 1) & 1u, status);
+            for (int x = 0; x < NQ; ++x)
+                if (q_issued[x]) wait_landed(&bars->q_full[x], (q_issued[x] - 1) & 1u, status);
         }
         __syncwarp();
-      } else if (warp == kMainWarps + 1) {
+      } else if (warp == kMainWarps + 1 || (NQ == 2 && warp == kMainWarps + 3)) {
         // ------------------------------------------------ MMA
+        const int x = uniform(warp == kMainWarps + 1 ? 0 : 1);  // query tile A or B
         constexpr uint32_t idS = idesc_f16(kRows, kKeys, true, false);
         constexpr uint32_t idO = idesc_f16(kRows, DP, true, true);
         // (the warp stays converged and every operand of an MMA is uniform: see elect_one)
         const uint32_t tm = uniform(tmem);
         const uint32_t base_q = uniform(smem_u32(sQ)), base_kv = uniform(smem_u32(sKV));
         uint32_t at = 0;  // stages consumed so far
-        uint32_t q_phase = 0, p_phase[2] = {0, 0}, cleaned = 0;
+        uint32_t q_phase = 0, p_phase = 0, cleaned = 0, turns = 0;
         bool ok = true;
+        const uint32_t tS = tm + x * 128, tO = tm + kTmem / 2 + x * 128;
+        const uint32_t qd = desc_kmajor(base_q + x * kTile);
         auto ready = [&](uint64_t* bar, uint32_t parity) {
             return warp_ready(bar, parity & 1u, abort_flag, status);
         };
         auto landed = [&](uint32_t k) { return ready(&bars->full[k % kStages], k / kStages); };
-        auto k_desc = [&](uint32_t stage) { return sdesc_kmajor_sw128(base_kv + uniform(stage) * kTile); };
+        auto k_desc = [&](uint32_t stage) { return desc_kmajor(base_kv + uniform(stage) * kTile); };
         auto v_desc = [&](uint32_t stage) {
-            return sdesc_nmajor_sw128(base_kv + uniform(stage) * kTile, kColBytes);
+            return desc_nmajor(base_kv + uniform(stage) * kTile, kColBytes);
         };
         Item it;
         while (ok && take_item(it, ok)) {
-            const int tiles_a = uniform(it.tiles[0]), tiles_b = uniform(it.tiles[1]);
-            const int tiles = max(tiles_a, tiles_b), masked = uniform(it.masked);
-            // The tensor core takes about 64 clocks an MMA and holds some five of
-            // them; what the warp does beside issuing (a look at a barrier: 100
-            // clocks or more) is where MMAs are queued up, and between S of tile B
-            // and P V of tile A there is nothing but the wait for P.
-            if (!(ok = ready(&bars->q_full, q_phase))) break;
+            const int tiles = uniform(max(it.tiles[0], it.tiles[1])), masked = uniform(it.masked);
+            const int mine = uniform(it.tiles[x]);
+            if (!(ok = ready(&bars->q_full[x], q_phase))) break;
             q_phase ^= 1u;
-            uint32_t kk = at % kStages, vv = 0;  // stages of K of tile j, V of tile j - 1
-            uint64_t kd = k_desc(kk), vd = 0;
-            auto release = [&](int j) {  // what turn j has read
-                if (elect_one()) {
-                    if (j > 0) mma_commit(&bars->empty[vv]);
-                    if (j < tiles) mma_commit(&bars->empty[kk]);
+            for (int j = 0; j <= tiles; ++j) {
+                // P V of key tile j - 1 and S of key tile j.  All looks at barriers but one
+                // come before the turn, all looks ahead after it.
+                const uint32_t kk = (at + 2 * j) % kStages, vv = (at + 2 * j + kStages - 1) % kStages;
+                const uint32_t kd = desc_kmajor(base_kv + uniform(kk) * kTile);
+                const uint32_t vd = desc_nmajor(base_kv + uniform(vv) * kTile, kColBytes);
+                const bool pv = j > 0 && j - 1 < mine;
+                if (j < tiles && !(ok = landed(at + 2 * j))) break;
+                if (pv && !(ok = ready(&bars->p_full[x][0], p_phase))) break;
+                if (NQ == 2) {
+                    if (!(ok = ready(&bars->turn[x], x == 0 ? turns ^ 1u : turns))) break;
+                    turns ^= 1u;
                 }
-                __syncwarp();
-            };
-            // Values of tile j - 1 and keys of tile j for query tile x.
-            auto turn = [&](int x, int j) {
-                const uint32_t tS = tm + x * 128, tO = tm + kTmem / 2 + x * 128;
-                const int mine = x == 0 ? tiles_a : tiles_b;
-                if (j > 0 && j - 1 < mine) {
+                tc_fence_after();
+                if (pv) {
+                    if (elect_one()) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (!ready(&bars->p_full[x][h], p_phase[x])) return false;
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int i = 4 * h; i < 4 * h + 4; ++i)
-                                mma_f16_ts(tO, tS + 8 * i, vd + i * (2048 >> 4), idO, !(j == 1 && i == 0));
-                            if (h == 1 && j == mine) mma_commit(&bars->o_full[x]);
-                        }
-                        __syncwarp();
+                        for (int i = 0; i < 4; ++i)
+                            mma_f16_ts(tO, tS + 8 * i, vd + i * (2048 >> 4), idO, !(j == 1 && i == 0));
                     }
-                    p_phase[x] ^= 1u;
-                }
-                if (x == 0 && j < tiles && !landed(at + 2 * j)) return false;
-                if (j < mine) {
+                    __syncwarp();
+                    if (!(ok = ready(&bars->p_full[x][1], p_phase))) break;
+                    p_phase ^= 1u;
                     tc_fence_after();
-                    const uint64_t qd = sdesc_kmajor_sw128(base_q + x * kTile);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 4; i < 8; ++i) mma_f16_ts(tO, tS + 8 * i, vd + i * (2048 >> 4), idO, 1);
+                        if (j == mine) mma_commit(&bars->o_full[x]);
+                    }
+                    __syncwarp();
+                }
+                if (j < mine) {
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < DP / 16; ++i) {
@@ -465,38 +508,28 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
                     }
                     __syncwarp();
                 }
-                return true;
-            };
-            for (int j = 0; j <= tiles; ++j) {
-                if (!(ok = turn(0, j))) break;
-                const uint32_t next_k = (at + 2 * j + 2) % kStages, next_v = (at + 2 * j + 1) % kStages;
-                const uint64_t next_kd = k_desc(next_k), next_vd = v_desc(next_v);
-                if (NQ == 2) {
-                    // the values that the next turn reads (with a look at them, they may take longer)
-                    if (j < tiles && j < masked && !(ok = landed(at + 2 * j + 1))) break;
-                    if (!(ok = turn(1, j))) break;
+                if (elect_one()) {
+                    if (NQ == 2) mbar_arrive(&bars->turn[x ^ 1]);
+                    if (j > 0) mma_commit(&bars->empty[vv]);
+                    if (j < tiles) mma_commit(&bars->empty[kk]);
+                    if (j + 1 == tiles) mma_commit(&bars->q_empty[x]);
                 }
-                release(j);
-                if (j + 1 == tiles) {
-                    if (elect_one()) mma_commit(&bars->q_empty);
-                    __syncwarp();
-                }
-                if (j < tiles && (NQ == 1 || j >= masked)) {
+                __syncwarp();
+                if (j < tiles) {
                     if (!(ok = landed(at + 2 * j + 1))) break;
                     if (j >= masked) {
                         if (!(ok = ready(&bars->v_clean[cleaned % kClean], cleaned / kClean))) break;
                         ++cleaned;
                     }
                 }
-                kk = next_k, vv = next_v, kd = next_kd, vd = next_vd;
             }
             if (!ok) break;
             at += 2 * tiles;
         }
         __syncwarp();
         if (elect_one()) {  // (the lane that issued the MMAs)
-            mma_commit(&bars->drain);
-            wait_drain(&bars->drain, status);
+            mma_commit(&bars->drain[x]);
+            wait_drain(&bars->drain[x], status);
         }
         __syncwarp();
       } else if (warp == kMainWarps + 2) {
@@ -541,32 +574,6 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
             }
             at += 2 * tiles;
             ++item_no;
-        }
-      } else {
-        // ------------------------------------------------ items
-        int64_t n = blockIdx.x;
-        uint32_t published = 0, asked = 0;
-        while (true) {
-            Item it = {};
-            if (n >= 0) it = find_item(n, blocks, a, tpt, NQ * tpt);
-            if (n < 0 || it.valid) {  // (an invalid one tells that there are no more)
-                if (!warp_ready(&bars->item_empty, (published & 1u) ^ 1u, abort_flag, status)) break;
-                if (lane == 0) bars->item = it;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->item_full);
-                ++published;
-                if (n < 0) break;
-            }
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars->next_cta, 16);
-                cancel_next_cta(&bars->response, &bars->next_cta);
-            }
-            __syncwarp();
-            if (!warp_ready(&bars->next_cta, asked & 1u, abort_flag, status)) break;
-            ++asked;
-            n = cancelled_cta(&bars->response);
-            fence_proxy_async_smem();  // (read, before the next answer is written)
-            __syncwarp();
         }
       }
     }

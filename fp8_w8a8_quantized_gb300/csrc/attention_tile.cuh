@@ -134,32 +134,67 @@ __device__ __forceinline__ void hide_after(uint32_t (&s)[4][16], int e, int seen
                 s[b][4 * (i >> 1) + 2 * e + (i & 1)] = 0xFF800000u;  // -inf
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// P of 64 keys (half b of the tile) from their scores, and its sums.
+template <bool kBf16>
+__device__ __forceinline__ void weights_of(const uint32_t (&s)[4][16], int b, const float (&c)[2],
+                                           const float (&base)[2], uint32_t (&p)[16], float (&sum)[2][2]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        // keys 64 b + 8 (i / 2) + 2 t, + 1 of row i & 1
+        const int e = i & 1;
+        const uint32_t* from = &s[2 * b + (i >> 3)][4 * (i >> 1 & 3) + 2 * e];
+        float y0 = base[e], y1 = base[e];
+        fma2(y0, y1, __uint_as_float(from[0]), __uint_as_float(from[1]), c[e], c[e]);
+        y0 = ex2(y0);
+        y1 = ex2(y1);
+        add2(sum[e][0], sum[e][1], y0, y1);
+        p[i] = kBf16 ? pack_bf16(y0, y1) : pack_f16(y0, y1);
+    }
+}
+
 // P of the tile from its scores; `started`: O holds earlier tiles.  c: scale
 // log2(e) of each row; real: rows that count.  `half` is called when the P of
 // 64 keys is in tensor memory.
+//
+// The maximum as a rule stays where it is, so the first half's P is taken with
+// the old one while the tile's maximum is still being found (300 clocks of
+// comparisons and shuffles, which the tensor core would wait for), and taken
+// again if that turns out too small.
 template <bool kBf16, int DP, typename Half>
 __device__ __forceinline__ void softmax_tile(uint32_t (&s)[4][16], uint32_t tS, uint32_t tO,
                                              SoftmaxRows& rows, const float (&c)[2],
                                              const bool (&real)[2], bool started, Half half) {
-    bool raise[2];
+    float base[2] = {rows.m[0] == -INFINITY ? 0.0f : -rows.m[0] * c[0],
+                     rows.m[1] == -INFINITY ? 0.0f : -rows.m[1] * c[1]};
+    uint32_t p[16];
+    float sum[2][2] = {};
+    weights_of<kBf16>(s, 0, c, base, p, sum);
     float top[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         float part[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            part[b] = __uint_as_float(s[b][2 * e]);
+            part[b] = fmaxf(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1]));
 #pragma unroll
-            for (int i = 1; i < 8; ++i)
-                part[b] = fmaxf(part[b], __uint_as_float(s[b][4 * (i >> 1) + 2 * e + (i & 1)]));
+            for (int i = 2; i < 8; i += 2)
+                part[b] = max3(part[b], __uint_as_float(s[b][4 * (i >> 1) + 2 * e]),
+                               __uint_as_float(s[b][4 * (i >> 1) + 2 * e + 1]));
         }
-        top[e] = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+        top[e] = fmaxf(max3(part[0], part[1], part[2]), part[3]);
     }
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) {
         top[0] = fmaxf(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], d));
         top[1] = fmaxf(top[1], __shfl_xor_sync(0xFFFFFFFFu, top[1], d));
     }
+    bool raise[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e)  // (m = -inf: the first keys that are seen set it)
         raise[e] = real[e] && (top[e] - rows.m[e]) * c[e] > kSlack;
@@ -172,6 +207,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&s)[4][16], uint32_t tS, 
             rows.m[e] = raise[e] ? top[e] : rows.m[e];
             rows.l[e][0] *= keep[e];
             rows.l[e][1] *= keep[e];
+            base[e] = rows.m[e] == -INFINITY ? 0.0f : -rows.m[e] * c[e];
+            sum[e][0] = sum[e][1] = 0.0f;
         }
         if (started) {
             // S of this tile came after P V of the one before: O is at rest
@@ -188,29 +225,21 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&s)[4][16], uint32_t tS, 
                 tmem_st_16x256b_x4(tO + 32 * b, o);
             }
         }
+        weights_of<kBf16>(s, 0, c, base, p, sum);
     }
-    const float base[2] = {rows.m[0] == -INFINITY ? 0.0f : -rows.m[0] * c[0],
-                           rows.m[1] == -INFINITY ? 0.0f : -rows.m[1] * c[1]};
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            // keys 64 b + 8 (i / 2) + 2 t, + 1 of row i & 1
-            const int e = i & 1;
-            const uint32_t* from = &s[2 * b + (i >> 3)][4 * (i >> 1 & 3) + 2 * e];
-            float y0 = base[e], y1 = base[e];
-            fma2(y0, y1, __uint_as_float(from[0]), __uint_as_float(from[1]), c[e], c[e]);
-            y0 = ex2(y0);
-            y1 = ex2(y1);
-            add2(rows.l[e][0], rows.l[e][1], y0, y1);
-            p[i] = kBf16 ? pack_bf16(y0, y1) : pack_f16(y0, y1);
-        }
+        if (b == 1) weights_of<kBf16>(s, 1, c, base, p, sum);
         tmem_st_16x128b_x8(tS + 32 * b, p);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         half(b);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        rows.l[e][0] += sum[e][0];
+        rows.l[e][1] += sum[e][1];
     }
 }
 

@@ -287,40 +287,47 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n, bool bf
            ((b_nmajor ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// Descriptor of an operand tile stored [k][n] with n contiguous (N-major):
-// columns of 64 16-bit elements, each column's k rows 128 bytes apart in the
-// 128-byte-swizzled layout (8-row atoms of 1024 bytes).  Leading byte offset:
-// from one column of 64 to the next; stride byte offset: 8 rows of k.
-__device__ __forceinline__ uint64_t sdesc_nmajor_sw128(uint32_t saddr, uint32_t column_bytes) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(column_bytes >> 4) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
+// The low word of a descriptor; the high word is the same for all operands
+// here (8-row groups 1024 bytes apart, bit 46 set, 128-byte swizzle).  The
+// low word alone is carried and advanced: with 64-bit descriptors a thread
+// needed 63 clocks to issue an MMA beside busy warps, with these 55.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// K-major operand: rows of 128 bytes (64 16-bit elements of k).
+__device__ __forceinline__ uint32_t desc_kmajor(uint32_t saddr) {
+    return ((saddr & 0x3FFFFu) >> 4) | (1u << 16);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T.
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                        uint32_t idesc, uint32_t accumulate) {
+// Operand tile stored [k][n] with n contiguous (N-major): columns of 64
+// 16-bit elements, each column's k rows 128 bytes apart; the leading byte
+// offset goes from one column of 64 to the next.
+__device__ __forceinline__ uint32_t desc_nmajor(uint32_t saddr, uint32_t column_bytes) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((column_bytes >> 4) << 16);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T; descriptors' low words.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(adesc), "r"(bdesc), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: A's rows are TMEM lanes, two 16-bit
 // elements of k in each 32-bit column.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(bdesc), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
 
