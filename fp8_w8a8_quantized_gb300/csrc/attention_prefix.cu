@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
                             if (!(word[b] >> (2 * t + 8 * (i >> 1) + (i & 1)) & 1u))
                                 s[b][4 * (i >> 1) + (i & 1)] = s[b][4 * (i >> 1) + 2 + (i & 1)] = 0xFF800000u;
                 }
-                softmax_tile<false, DP>(s, tS, tO, rows, c, real, j > 0, [&](int h) {
+                softmax_tile<false, DP, false>(s, tS, tO, rows, c, real, j > 0, [&](int h) {
                     if (lane == 0) mbar_arrive(&bars->p_full[x][h]);
                 });
             }

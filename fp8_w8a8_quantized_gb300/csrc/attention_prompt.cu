@@ -70,8 +70,8 @@ struct Config {
     static constexpr int kMainWarps = 8 * NQ;
     static constexpr int kThreads = 32 * (kMainWarps + 4);
     static constexpr int kCtas = 3 - NQ;  // an SM
-    // 512 x 104 + 128 x 64 = 640 x 96 and 256 x 88 + 128 x 64 = 384 x 80, the launch's
-    static constexpr int kMainRegs = NQ == 2 ? 104 : 88, kSideRegs = 64;
+    // 512 x 104 + 128 x 64 = 640 x 96 and 256 x 96 + 128 x 48 = 384 x 80, the launch's
+    static constexpr int kMainRegs = NQ == 2 ? 104 : 96, kSideRegs = NQ == 2 ? 64 : 48;
 };
 
 template <int kStages>
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
                     hide_after(s, 0, my_tok[0] - j * kKeys - 2 * t);
                     hide_after(s, 1, my_tok[1] - j * kKeys - 2 * t);
                 }
-                softmax_tile<true, DP>(s, tS, tO, rows, c, mine, j > 0, [&](int h) {
+                softmax_tile<true, DP, true>(s, tS, tO, rows, c, mine, j > 0, [&](int h) {
                     if (lane == 0) mbar_arrive(&bars->p_full[x][h]);
                 });
             }

@@ -162,11 +162,11 @@ __device__ __forceinline__ void weights_of(const uint32_t (&s)[4][16], int b, co
 // log2(e) of each row; real: rows that count.  `half` is called when the P of
 // 64 keys is in tensor memory.
 //
-// The maximum as a rule stays where it is, so the first half's P is taken with
-// the old one while the tile's maximum is still being found (300 clocks of
-// comparisons and shuffles, which the tensor core would wait for), and taken
-// again if that turns out too small.
-template <bool kBf16, int DP, typename Half>
+// kAhead: the maximum as a rule stays where it is, so the first half's P is
+// taken with the old one while the tile's maximum is still being found (300
+// clocks of comparisons and shuffles, which the tensor core would wait for),
+// and taken again if that turns out too small.  It costs some 20 registers.
+template <bool kBf16, int DP, bool kAhead, typename Half>
 __device__ __forceinline__ void softmax_tile(uint32_t (&s)[4][16], uint32_t tS, uint32_t tO,
                                              SoftmaxRows& rows, const float (&c)[2],
                                              const bool (&real)[2], bool started, Half half) {
@@ -174,7 +174,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&s)[4][16], uint32_t tS, 
                      rows.m[1] == -INFINITY ? 0.0f : -rows.m[1] * c[1]};
     uint32_t p[16];
     float sum[2][2] = {};
-    weights_of<kBf16>(s, 0, c, base, p, sum);
+    if (kAhead) weights_of<kBf16>(s, 0, c, base, p, sum);
     float top[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -225,11 +225,11 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&s)[4][16], uint32_t tS, 
                 tmem_st_16x256b_x4(tO + 32 * b, o);
             }
         }
-        weights_of<kBf16>(s, 0, c, base, p, sum);
+        if (kAhead) weights_of<kBf16>(s, 0, c, base, p, sum);
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        if (b == 1) weights_of<kBf16>(s, 1, c, base, p, sum);
+        if (b == 1 || !kAhead) weights_of<kBf16>(s, b, c, base, p, sum);
         tmem_st_16x128b_x8(tS + 32 * b, p);
         tmem_st_wait();
         tc_fence_before();
