@@ -150,7 +150,7 @@ fp8_status_t fp8_attention_prompt(const void* q, int64_t ldq, const void* k, int
         (st = check_tokens(v, ldv, Hkv, D)) != FP8_OK ||
         (st = check_tokens(out, ldo, Hq, D)) != FP8_OK)
         return st;
-    if (!aligned(cu_seqlens, 4)) return FP8_ERR_UNSUPPORTED;
+    if (!aligned(cu_seqlens, 4) || T + S > kMax31 / Hkv) return FP8_ERR_UNSUPPORTED;
     fp8k::PromptArgs a;
     if ((st = fp8k::device_info(&a.num_sms, &a.status)) != FP8_OK) return st;
     a.q = static_cast<const uint16_t*>(q);

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
                 const int64_t tok = a.skip + (u * sh.ways + way) * kTile + lane;
                 if (u >= u1 || tok - a.skip >= len) return -1;
                 const unsigned pg = static_cast<unsigned>(tok) / page;
-                const int id = __ldg((tok < a.prefix ? a.table : own_row) + pg);
+                const int id = (tok < a.prefix ? a.table : own_row)[pg];
                 if (id < 0 || id >= a.n_pages) return -1;
                 return static_cast<int>(id * page + (static_cast<unsigned>(tok) - pg * page));
             };

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             const int64_t tok = static_cast<int64_t>(tile0 + (job >> 3)) * kKeys + 32 * (job & 3) + lane;
             if (job >= jobs || tok >= a.prefix) return -1;
             const unsigned pg = static_cast<unsigned>(tok) / page;
-            const int id = __ldg(a.table + pg);
+            const int id = a.table[pg];
             if (id < 0 || id >= a.n_pages) return -1;
             return static_cast<int>(id * page + (static_cast<unsigned>(tok) - pg * page));
         };

@@ -112,7 +112,7 @@ __device__ __forceinline__ Item find_item(int64_t n, int64_t blocks, const Promp
         const int64_t at = lo + step * lane_id();
         bool below = false;
         if (at < lo + count) {
-            const int c = min(max(__ldg(a.cu + at), 0), T);
+            const int c = min(max(a.cu[at], 0), T);
             below = c / per + at <= i;
         }
         const unsigned votes = __ballot_sync(0xFFFFFFFFu, below);
@@ -121,8 +121,8 @@ __device__ __forceinline__ Item find_item(int64_t n, int64_t blocks, const Promp
         count = min(step, lo + count - next);
         lo = next;
     }
-    it.start = min(max(__ldg(a.cu + lo), 0), T);
-    it.len = min(max(__ldg(a.cu + lo + 1), it.start), T) - it.start;
+    it.start = min(max(a.cu[lo], 0), T);
+    it.len = min(max(a.cu[lo + 1], it.start), T) - it.start;
     const int64_t q0 = (i - (it.start / per + lo)) * per;
     it.valid = q0 >= 0 && q0 < it.len;
     it.q0 = static_cast<int>(q0);

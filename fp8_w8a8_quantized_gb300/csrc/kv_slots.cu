@@ -14,7 +14,8 @@
 // range of tokens and its share of the pages taken, a thread each, which finds
 // its request by bisection in shared memory.  A token on a page that this very
 // call takes looks the page up in `free`, not in the table, so no CTA reads
-// what another one writes.  Division by the page size is a multiplication
+// what another one writes.  (Loads go past L1: the lines that this grid's start
+// found there may be older than what the kernel before it wrote.)  Division by the page size is a multiplication
 // (64-bit divisions alone took 6 of 11 us for 256 requests).
 #include <cuda_runtime.h>
 
@@ -85,9 +86,8 @@ __device__ __forceinline__ int find_start(const int64_t* starts, int n, int64_t 
 // kPer: requests a thread; the lengths are scanned kThreads * kPer at a time.
 template <int kPer>
 __global__ void __launch_bounds__(kThreads)
-    kv_slots(const int32_t* __restrict__ ctx, const int32_t* __restrict__ fresh, int64_t B,
-             const int32_t* __restrict__ free_pages, int64_t n_free, const Pages page,
-             int32_t* __restrict__ table, int64_t ld_table, int64_t T, int64_t per_cta,
+    kv_slots(const int32_t* ctx, const int32_t* fresh, int64_t B, const int32_t* free_pages,
+             int64_t n_free, const Pages page, int32_t* table, int64_t ld_table, int64_t T, int64_t per_cta,
              int64_t* __restrict__ slot, int32_t* __restrict__ pos, int32_t* __restrict__ cu,
              int32_t* __restrict__ lens, int32_t* __restrict__ used) {
     constexpr int kChunk = kThreads * kPer;
@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int r = threadIdx.x * kPer + i;
-            c[i] = r < n ? max(ctx[b0 + r], 0) : 0;
-            f[i] = r < n ? max(fresh[b0 + r], 0) : 0;
+            c[i] = r < n ? max(__ldcg(ctx + b0 + r), 0) : 0;
+            f[i] = r < n ? max(__ldcg(fresh + b0 + r), 0) : 0;
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads)
              k < s_first[n]; k += static_cast<int64_t>(gridDim.x) * kThreads) {
             const int a = find_start(s_first, n, k);
             table[(b0 + a) * ld_table + page.needed(s_ctx[a]) + (k - s_first[a])] =
-                k < n_free ? free_pages[k] : -1;
+                k < n_free ? __ldcg(free_pages + k) : -1;
         }
         // this CTA's tokens that belong to the chunk's requests
         const int64_t lo = t_lo > s_cu[0] ? t_lo : s_cu[0];
@@ -160,10 +160,10 @@ __global__ void __launch_bounds__(kThreads)
             const uint32_t pg = page.of(at), have = page.needed(s_ctx[a]);
             int64_t id = -1;
             if (pg < have) {
-                id = table[(b0 + a) * ld_table + pg];
+                id = __ldcg(table + (b0 + a) * ld_table + pg);
             } else if (pg < page.width) {
                 const int64_t i = s_first[a] + (pg - have);
-                if (i < n_free) id = free_pages[i];
+                if (i < n_free) id = __ldcg(free_pages + i);
             }
             slot[k] = id < 0 ? -1 : id * page.size + (at - pg * page.size);
             pos[k] = static_cast<int32_t>(min(at, 0x7FFFFFFFu));

@@ -461,7 +461,7 @@ FP8_API fp8_status_t fp8_qk_norm_rope(const void* q, int64_t ldq, const void* k,
  *   out    [device, out]  bf16 [T, Hq, D], ldo; overlaps no input
  * Requirements: Hq % Hkv == 0, Hq / Hkv <= 64; D % 16 == 0, 16 <= D <= 128;
  * leading dimensions >= heads * D and % 8 == 0; 16-byte aligned tensors;
- * scale > 0 finite; Hkv <= 65535.
+ * scale > 0 finite; Hkv <= 65535; (T + S) * Hkv < 2^31.
  */
 FP8_API fp8_status_t fp8_attention_prompt(const void* q, int64_t ldq, const void* k, int64_t ldk,
                                           const void* v, int64_t ldv, int64_t T, int64_t Hq,

@@ -69,7 +69,7 @@ HEADS = [(dict(Hq=7), INVALID), (dict(Hkv=0), INVALID), (dict(Hq=0), INVALID), (
 @pytest.mark.parametrize("changed,want", HEADS + [
     (dict(T=-1), INVALID), (dict(S=-1), INVALID), (dict(cu=None), INVALID), (dict(cu=P + 2), UNSUP),
     (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(ldk=120), INVALID), (dict(ldv=132), UNSUP),
-    (dict(k=P + 8), UNSUP), (dict(T=0), 0), (dict(S=0), 0)])
+    (dict(k=P + 8), UNSUP), (dict(T=(1 << 31) - 1), UNSUP), (dict(T=0), 0), (dict(S=0), 0)])
 def test_prompt_refusals(L, changed, want):
     assert call(L.fp8_attention_prompt, PROMPT, **changed) == want
 

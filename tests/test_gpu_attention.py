@@ -398,6 +398,69 @@ def test_decode_bad_pages_and_lengths_are_hidden():
         check_decode(args, page, prefix)
 
 
+def test_decode_more_requests_than_are_cut_by_tokens():
+    lens = [(7 * i) % 23 for i in range(4100)]
+    check_decode(cached(gen(41), lens, 2, 1, 16, 8), 8)
+    lens[17] = 700
+    check_decode(cached(gen(42), lens, 18, 1, 32, 16), 16)
+
+
+def test_decode_one_long_request_among_many_short_ones():
+    lens = [5 + i % 90 for i in range(200)]
+    lens[77] = 6001
+    check_decode(cached(gen(43), lens, 8, 8, 64, 16), 16)
+    check_decode(cached(gen(44), lens, 8, 1, 128, 16), 16)
+
+
+def test_decode_cache_beyond_32_bits():
+    # 5 GB a cache: the pages at its end, at a byte offset past 2^32
+    Hkv, D, page, n_pages = 8, 128, 64, 82000
+    small = list(cached(gen(45), [300, 1, 129], 16, Hkv, D, page))
+    far = list(small)
+    have = small[1].shape[0]
+    far[1], far[2] = (torch.zeros(n_pages * page, Hkv, D, dtype=torch.uint8, device=DEV) for _ in range(2))
+    far[1][-have:], far[2][-have:] = small[1], small[2]
+    far[5] = small[5] + (n_pages - have // page)
+    assert far[1].numel() > 2 ** 32
+    near = pkg.fp8_attention_decode(*small, page)
+    got = pkg.fp8_attention_decode(*far, page)
+    settled()
+    assert torch.equal(near, got)
+    # the same through the shared-prefix kernel
+    small = list(cached(gen(46), [2001 + i for i in range(70)], 32, Hkv, D, page, 1984))
+    have = small[1].shape[0]
+    far[1].zero_()
+    far[2].zero_()
+    far[1][-have:], far[2][-have:] = small[1], small[2]
+    far = [small[0], far[1], far[2], small[3], small[4], small[5] + (n_pages - have // page), small[6]]
+    near = pkg.fp8_attention_decode(*small, page, prefix_len=1984)
+    got = pkg.fp8_attention_decode(*far, page, prefix_len=1984)
+    settled()
+    assert torch.equal(near, got)
+    # and the cache write on the way of the rotation
+    q, k, v = (normal(gen(47), 3, h, D) for h in (2, Hkv, Hkv))
+    slot = torch.tensor([n_pages * page - 1, 5, n_pages * page - 1 - 4 * 10 ** 6], device=DEV)
+    one = torch.ones(1, device=DEV)
+    pkg.fp8_qk_norm_rope(q, k, int32([1, 2, 3]), pkg.fp8_rope_turns(rot_dim=D), v=v, k_scale=one, v_scale=one,
+                         slot_mapping=slot, k_cache=far[1], v_cache=far[2])
+    settled()
+    assert torch.equal(far[2][slot].view(torch.float8_e4m3fn).float(), v.to(torch.float8_e4m3fn).float())
+
+
+def test_prompt_beyond_32_bits():
+    # tokens whose queries and outputs lie past 2^32 bytes
+    g = gen(48)
+    T, Hq, Hkv, D = 270000, 64, 8, 128
+    qkv = torch.zeros(T, (Hq + 2 * Hkv) * D, dtype=torch.bfloat16, device=DEV)
+    qkv[-400:] = normal(g, 400, qkv.shape[1])
+    q, k, v = (t.unflatten(1, (-1, D)) for t in qkv.split([Hq * D, Hkv * D, Hkv * D], 1))
+    far = pkg.fp8_attention_prompt(q, k, v, int32([T - 400, T - 100, T]))
+    near = pkg.fp8_attention_prompt(q[-400:].contiguous(), k[-400:].contiguous(), v[-400:].contiguous(),
+                                    int32([0, 300, 400]))
+    settled()
+    assert far.numel() * 2 > 2 ** 32 and torch.equal(far[-400:], near)
+
+
 def test_decode_single_scale_strides_large_queries_and_scales():
     args = list(cached(gen(15), [333, 40], 8, 4, 64, 16))
     args[3], args[4] = args[3][:1], args[4][:1]
