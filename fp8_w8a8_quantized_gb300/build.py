@@ -99,7 +99,7 @@ def _link_module(obj: str) -> None:
     tmp = MODULE_PATH + f".{os.getpid()}.tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN",
            "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
-           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding module failed:\n{r.stdout}\n{r.stderr}")

@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/Exception.h>
@@ -148,8 +148,9 @@ void same_device(const Tensor& first, std::initializer_list<const Tensor*> other
                           t->device().str());
 }
 
+// (straight from the caching allocator: at::empty's dispatch costs as much again)
 Tensor make(at::IntArrayRef shape, at::ScalarType dtype, const Tensor& like) {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(like.device()));
+    return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
 }
 
 PyObject* status(fp8_status_t s) { return PyLong_FromLong(s); }

@@ -13,8 +13,9 @@
 // sincospif takes them from there.
 //
 // Bound by memory: every element is read once and written once.  A lane holds
-// eight consecutive elements of a head (one 16-byte access), D / 8 lanes
-// (rounded up to a power of two) a head, so norm and rotation need only
+// eight elements of a head, the four pairs that it turns: two runs of four, at
+// i and i + rot / 2 (eight consecutive ones where the pairs are neighbours),
+// D / 8 lanes (rounded up to a power of two) a head; only the norm needs
 // shuffles.  A warp stays with one token for many heads, because its lanes'
 // factors are the same in all of them:
 //   out_i = (x_i A_i + x_partner B_i) / norm,   A_i = gamma_i cos t,
@@ -46,17 +47,27 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
 
 constexpr int kBatch = 2;  // heads' loads of a lane on their way (four CTAs an SM; four heads, three CTAs: 4% slower)
 
-__device__ __forceinline__ void gamma8(const uint16_t* gamma, int chunk, bool live, float (&g)[8]) {
-    if (gamma && live) {
-        widen8(__ldg(reinterpret_cast<const uint4*>(gamma + chunk * 8)), g);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = 1.0f;
+// A lane's eight elements: four at `first`, four at `second` (elements).
+struct Runs {
+    int first, second;
+    __device__ uint4 load(const uint16_t* head) const {
+        const uint2 a = *reinterpret_cast<const uint2*>(head + first);
+        const uint2 b = *reinterpret_cast<const uint2*>(head + second);
+        return make_uint4(a.x, a.y, b.x, b.y);
     }
-}
+    __device__ void store(uint16_t* head, const uint4& v) const {
+        *reinterpret_cast<uint2*>(head + first) = make_uint2(v.x, v.y);
+        *reinterpret_cast<uint2*>(head + second) = make_uint2(v.z, v.w);
+    }
+    __device__ void store_codes(uint8_t* head, const uint2& v) const {
+        *reinterpret_cast<uint32_t*>(head + first) = v.x;
+        *reinterpret_cast<uint32_t*>(head + second) = v.y;
+    }
+};
 
-// kLanes: lanes of a head (a power of two, kLanes * 8 >= D).
-template <int kLanes, bool kNorm, bool kPairs>
+// kLanes: lanes of a head (a power of two, kLanes * 8 >= D).  kPairs: pairs
+// (2 i, 2 i + 1).  kWhole: all of a head is turned.
+template <int kLanes, bool kNorm, bool kPairs, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs a, int slices) {
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -68,33 +79,28 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
     if (t >= a.T) return;
     const int slice = static_cast<int>(w - t * slices);
     const bool live = chunk < a.D >> 3;
-    const int half = a.rot >> 4;  // chunks of half the rotated part (pairs d, d + rot / 2)
-    const bool turned = chunk < 2 * half;
-    const int partner = kPairs || !turned ? chunk : chunk < half ? chunk + half : chunk - half;
-    const int from = (lane & ~(kLanes - 1)) + partner;
+    const bool turned = kWhole || chunk < a.rot >> 3;
+    Runs at;
+    if (kPairs) {
+        at.first = 8 * chunk;
+        at.second = 8 * chunk + 4;
+    } else {  // (what is not turned: two runs as well, of the rest's halves)
+        const int from = turned ? 0 : a.rot, size = turned ? a.rot : a.D - a.rot;
+        at.first = from + 4 * (chunk - (from >> 3));
+        at.second = at.first + (size >> 1);
+    }
 
-    // this lane's sines and cosines: eight pairs, or the four within its chunk
-    float co[8], si[8];
-    // (what is not turned: x A + 0 (-0) keeps even a zero's sign)
+    // this lane's sines and cosines, of its four pairs
+    float co[4], si[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) co[i] = 1.0f, si[i] = -0.0f;
-    if (turned) {
+    for (int i = 0; i < 4; ++i) co[i] = 1.0f, si[i] = 0.0f;
+    if (turned && live) {
         const uint64_t position = static_cast<uint64_t>(static_cast<int64_t>(a.positions[t]));
-        const int base = kPairs ? chunk * 4 : (chunk < half ? chunk : chunk - half) * 8;
 #pragma unroll
-        for (int i = 0; i < (kPairs ? 4 : 8); ++i) {
-            const uint64_t turns = position * a.turns[base + i];
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t turns = position * a.turns[4 * chunk + i];
             const float x = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;
-            float s, c;
-            sincospif(x, &s, &c);
-            if (kPairs) {
-                co[2 * i] = co[2 * i + 1] = c;
-                si[2 * i] = -s;
-                si[2 * i + 1] = s;
-            } else {
-                co[i] = c;
-                si[i] = chunk < half ? -s : s;
-            }
+            sincospif(x, &si[i], &co[i]);
         }
     }
     const int64_t slot = a.k_cache ? (a.slot ? a.slot[t] : t) : -1;
@@ -113,26 +119,27 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
         const int lo = max(begin, off) - off, hi = min(end, off + (kind ? steps_k : steps_q)) - off;
         if (lo >= hi) continue;
         const int heads = kind ? a.Hkv : a.Hq;
-        const uint16_t* src = (kind ? a.k + t * a.ldk : a.q + t * a.ldq) + chunk * 8;
-        uint16_t* dst = kind ? (a.k_out ? a.k_out + t * a.ldko + chunk * 8 : nullptr)
-                             : a.q_out + t * a.ldqo + chunk * 8;
+        const uint16_t* src = kind ? a.k + t * a.ldk : a.q + t * a.ldq;
+        uint16_t* dst = kind ? (a.k_out ? a.k_out + t * a.ldko : nullptr) : a.q_out + t * a.ldqo;
         const uint16_t* gamma = kind ? a.gamma_k : a.gamma_q;
         const bool normed = kNorm && gamma;
-        float A[8], B[8];
-        gamma8(kNorm ? gamma : nullptr, chunk, live, A);
-        gamma8(kNorm ? gamma : nullptr, partner, live, B);
+        float A[8], B[8];  // of elements 0-3 and 4-7
+        {
+            float g[8];
+            if (normed && live) {
+                widen8(at.load(gamma), g);
+            } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) A[i] *= co[i];
-        if (kPairs) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float other = B[i];
-                B[i] = turned ? B[i + 1] * si[i] : si[i];
-                B[i + 1] = turned ? other * si[i + 1] : si[i + 1];
+                for (int i = 0; i < 8; ++i) g[i] = 1.0f;
             }
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) B[i] = turned ? B[i] * si[i] : si[i];
+            for (int i = 0; i < 8; ++i) {
+                // (what is not turned: x A + 0 (-0) keeps even a zero's sign)
+                const int pair = kPairs ? i >> 1 : i & 3, other = kPairs ? i ^ 1 : i ^ 4;
+                const bool low = kPairs ? !(i & 1) : i < 4;
+                A[i] = g[i] * co[pair];
+                B[i] = !turned ? -0.0f : low ? -g[other] * si[pair] : g[other] * si[pair];
+            }
         }
         for (int step = lo; step < hi; step += kBatch) {
             uint4 u[kBatch];
@@ -140,26 +147,14 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
             for (int j = 0; j < kBatch; ++j) {
                 const int head = (step + j) * kHeads + sub;
                 u[j] = make_uint4(0, 0, 0, 0);
-                if (live && step + j < hi && head < heads)
-                    u[j] = *reinterpret_cast<const uint4*>(src + head * a.D);
+                if (live && step + j < hi && head < heads) u[j] = at.load(src + head * a.D);
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 if (step + j >= hi) break;  // (the whole warp)
                 const int head = (step + j) * kHeads + sub;
-                float x[8], z[8];
+                float x[8];
                 widen8(u[j], x);
-                if (kPairs) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) z[i] = turned ? x[i ^ 1] : 0.0f;
-                } else {
-                    uint4 v = make_uint4(__shfl_sync(0xFFFFFFFFu, u[j].x, from),
-                                         __shfl_sync(0xFFFFFFFFu, u[j].y, from),
-                                         __shfl_sync(0xFFFFFFFFu, u[j].z, from),
-                                         __shfl_sync(0xFFFFFFFFu, u[j].w, from));
-                    if (!turned) v = make_uint4(0, 0, 0, 0);
-                    widen8(v, z);
-                }
                 float inv = 1.0f;
                 if (kNorm) {
                     float s0 = 0.0f, s1 = 0.0f;
@@ -173,18 +168,19 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
+                    const int p = kPairs ? i + 1 : i ^ 4, q = kPairs ? i : (i ^ 4) + 1;
+                    const float z0 = turned ? x[p] : 0.0f, z1 = turned ? x[q] : 0.0f;
                     mul2(y[i], y[i + 1], x[i], x[i + 1], A[i], A[i + 1]);
-                    fma2(y[i], y[i + 1], z[i], z[i + 1], B[i], B[i + 1]);
+                    fma2(y[i], y[i + 1], z0, z1, B[i], B[i + 1]);
                     if (kNorm) mul2(y[i], y[i + 1], y[i], y[i + 1], inv, inv);
                 }
                 const uint4 o = make_uint4(narrow2(y[0], y[1]), narrow2(y[2], y[3]), narrow2(y[4], y[5]),
                                            narrow2(y[6], y[7]));
                 if (!live || head >= heads) continue;
-                if (dst) *reinterpret_cast<uint4*>(dst + head * a.D) = o;
+                if (dst) at.store(dst + head * a.D, o);
                 if (kind && store) {
                     const float s = __ldg(a.k_scale + head * a.scale_stride);
-                    *reinterpret_cast<uint2*>(a.k_cache + (slot * a.Hkv + head) * a.D + chunk * 8) =
-                        quant8<false>(o, divisor_of(s));
+                    at.store_codes(a.k_cache + (slot * a.Hkv + head) * a.D, quant8<false>(o, divisor_of(s)));
                 }
             }
         }
@@ -211,6 +207,12 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
     }
 }
 
+template <int kLanes, bool kWhole>
+auto kernel_of(bool norm, bool pairs) {
+    return norm ? (pairs ? qk_norm_rope<kLanes, true, true, kWhole> : qk_norm_rope<kLanes, true, false, kWhole>)
+                : (pairs ? qk_norm_rope<kLanes, false, true, kWhole> : qk_norm_rope<kLanes, false, false, kWhole>);
+}
+
 template <int kLanes>
 cudaError_t launch_lanes(const QkNormRopeArgs& a, int num_sms, cudaStream_t st) {
     constexpr int kHeads = 32 / kLanes;
@@ -230,8 +232,9 @@ cudaError_t launch_lanes(const QkNormRopeArgs& a, int num_sms, cudaStream_t st) 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const bool norm = a.gamma_q || a.gamma_k;
-    auto kernel = norm ? (a.pairs ? qk_norm_rope<kLanes, true, true> : qk_norm_rope<kLanes, true, false>)
-                       : (a.pairs ? qk_norm_rope<kLanes, false, true> : qk_norm_rope<kLanes, false, false>);
+    // (a lane beyond D / 8 has nothing to turn either)
+    auto kernel = a.rot == a.D && a.D == 8 * kLanes ? kernel_of<kLanes, true>(norm, a.pairs)
+                                                    : kernel_of<kLanes, false>(norm, a.pairs);
     return cudaLaunchKernelEx(&cfg, kernel, a, slices);
 }
 
