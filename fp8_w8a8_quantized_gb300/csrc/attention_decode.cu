@@ -48,6 +48,7 @@ constexpr int kWarps = 8;            // warps of a CTA
 constexpr int kCtas = 152;           // CTAs at most (one per SM)
 constexpr int64_t kMaxPlan = 4096;   // requests up to which the work is cut by tokens
 constexpr int kBatch = 4;            // parts of a row that are loaded at a time
+constexpr int kWholeSteps = 4;       // steps of a request that one CTA does as a whole
 constexpr int kMinTokens = 64;       // tokens of a request that are worth a CTA
 
 // A request whose steps several CTAs share, for the kernel that joins them.
@@ -727,7 +728,11 @@ struct Launch {
     }
     static cudaError_t run(const DecodeArgs& a, cudaStream_t st) {
         const Shape s = shape_of<NT, W>(a.Hq, a.Hkv);
-        const bool planned = a.B <= kMaxPlan;
+        // Contexts of a few steps at most are not cut either: a second launch to
+        // join their parts takes longer than the steps do (7 requests of up to
+        // 301 tokens, 2 key heads: 6.2 us whole, 7.8 us cut and joined).
+        const int64_t steps = (a.width * a.page - a.skip + kTile * s.ways - 1) / (kTile * s.ways);
+        const bool planned = a.B <= kMaxPlan && steps > kWholeSteps;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         const int ctas = a.num_sms < kCtas ? a.num_sms : kCtas;
