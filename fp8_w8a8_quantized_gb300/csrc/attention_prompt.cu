@@ -306,18 +306,22 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
             }
             if (!ok) break;
             if (tiles > 0) {
+                // (what needs no O comes before the wait for it)
+                float inv[2];
+                uint16_t* dst[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float sum = rows.sum(e);
+                    inv[e] = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+                    dst[e] = a.out + (it.start + my_tok[e]) * a.ldo +
+                             static_cast<int64_t>(it.head * G + head_in[e]) * a.D + 8 * t;
+                }
                 if (!(ok = warp_ready(&bars->o_full[x], o_phase, abort_flag, status))) break;
                 o_phase ^= 1u;
                 tc_fence_after();
                 if (*reinterpret_cast<volatile int*>(&bars->dirty[item_no % kFlags]) != 0)
                     add_unfinite<DP>(tO, a.v + it.start * a.ldv + static_cast<int64_t>(it.head) * a.D, a.ldv, a.D,
                                      it.masked * kKeys, mine[0] ? my_tok[0] : -1, mine[1] ? my_tok[1] : -1);
-                float inv[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float sum = rows.sum(e);
-                    inv[e] = sum == 0.0f ? 0.0f : 1.0f / sum;
-                }
                 uint32_t o[DP / 32][16];
 #pragma unroll
                 for (int b = 0; b < DP / 32; ++b) tmem_ld_16x256b_x4(tO + 32 * b, o[b]);
@@ -328,20 +332,21 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
                     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[b][i]));  // (no use before the wait)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    uint16_t* dst = a.out + (it.start + my_tok[e]) * a.ldo +
-                                    static_cast<int64_t>(it.head * G + head_in[e]) * a.D + 8 * t;
 #pragma unroll
                     for (int b = 0; b < DP / 32; ++b) {
                         // w[i]: elements 8 i + 2 t, + 1; the quad's lanes exchange them so
                         // that lane t has elements 8 t .. 8 t + 7 for one 16-byte store
                         uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = pack_bf16(__uint_as_float(o[b][4 * i + 2 * e]) * inv[e],
-                                             __uint_as_float(o[b][4 * i + 2 * e + 1]) * inv[e]);
+                        for (int i = 0; i < 4; ++i) {
+                            float y0, y1;
+                            mul2(y0, y1, __uint_as_float(o[b][4 * i + 2 * e]),
+                                 __uint_as_float(o[b][4 * i + 2 * e + 1]), inv[e], inv[e]);
+                            w[i] = pack_bf16(y0, y1);
+                        }
                         transpose_quad(w, t);
                         if (mine[e] && 32 * b + 8 * t < a.D)
-                            *reinterpret_cast<uint4*>(dst + 32 * b) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4*>(dst[e] + 32 * b) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 __syncwarp();
