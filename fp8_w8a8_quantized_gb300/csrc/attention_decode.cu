@@ -168,17 +168,26 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
     // the line of work
     int64_t per = 0, lo, hi;
     if (planned) {
-        int64_t carry = 0;
-        for (int64_t b0 = 0; b0 < a.B; b0 += W * 32) {
-            const int64_t b = b0 + threadIdx.x;
-            // (a request without tokens has one step: someone has to write its zeros)
-            const int64_t n = b < a.B ? max(divide_up(length(b), step), int64_t(1)) : 0;
-            int64_t x = n;
+        // (a request without tokens has one step: someone has to write its zeros)
+        auto upto_lane = [&](int64_t b) {
+            int64_t x = b < a.B ? max(divide_up(length(b), step), int64_t(1)) : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
                 if (lane >= d) x += y;
             }
+            return x;
+        };
+        int64_t carry = 0;
+        if (a.B <= 32) {  // each warp for itself, all with the same values: nobody waits
+            const int64_t x = upto_lane(lane);
+            if (lane < a.B) upto[lane + 1] = x;
+            if (lane == 0) upto[0] = 0;
+            __syncwarp();
+        }
+        for (int64_t b0 = 0; a.B > 32 && b0 < a.B; b0 += W * 32) {
+            const int64_t b = b0 + threadIdx.x;
+            int64_t x = upto_lane(b);
             if (lane == 31) warp_sums[warp] = x;
             __syncthreads();
             int64_t before = carry;
@@ -190,8 +199,10 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
             if (b < a.B) upto[b + 1] = x;
             __syncthreads();
         }
-        if (threadIdx.x == 0) upto[0] = 0;
-        __syncthreads();
+        if (a.B > 32) {
+            if (threadIdx.x == 0) upto[0] = 0;
+            __syncthreads();
+        }
         const int64_t total = upto[a.B] * sh.groups;
         per = max(divide_up(total, gridDim.x), int64_t(max(kMinTokens / step, 1)));
         lo = min(per * blockIdx.x, total);
@@ -623,6 +634,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
 // row that has many are dealt to the CTA's warps, whose sums are then added in
 // the warps' order.
 constexpr int kJoinWarps = 16;
+constexpr int kJoinBatch = 8;  // parts on their way (a CTA a row of 128 parts: one round)
 template <int NT, int DP, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const DecodeArgs a) {
     constexpr int R = 8 * NT;
@@ -641,17 +653,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const D
     const int G = a.Hq / a.Hkv, lane = lane_id(), warp = threadIdx.x >> 5;
     const int r0 = cut.group % sh.blocks * R, h0 = cut.group / sh.blocks * sh.heads;
     const int rows = min(R, G - r0), items = rows * min(sh.heads, a.Hkv - h0);
-    const bool few = last - c0 < 4 * kBatch;
+    const bool few = last - c0 < 2 * kJoinBatch;
     const int step = few ? 1 : kJoinWarps, offset = few ? 0 : warp;
     for (int y = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y; y < items;
          y += few ? gridDim.y * kJoinWarps : gridDim.y) {
         const int head = y / rows, row = y - head * rows;
         float m = -INFINITY, l = 0.0f, o[V] = {};
-        for (int cta = c0 + offset; cta <= last; cta += kBatch * step) {
-            float2 ml[kBatch];
-            float part[kBatch][V];
+        for (int cta = c0 + offset; cta <= last; cta += kJoinBatch * step) {
+            float2 ml[kJoinBatch];
+            float part[kJoinBatch][V];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
+            for (int i = 0; i < kJoinBatch; ++i) {
                 const int from = cta + i * step;
                 ml[i] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
@@ -666,14 +678,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const D
             }
             float top = m;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+            for (int i = 0; i < kJoinBatch; ++i) top = fmaxf(top, ml[i].x);
             const float keep = m == -INFINITY ? 0.0f : ex2(m - top);
             m = top;
             l *= keep;
 #pragma unroll
             for (int e = 0; e < V; ++e) o[e] *= keep;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
+            for (int i = 0; i < kJoinBatch; ++i) {
                 const float take = ml[i].x == -INFINITY ? 0.0f : ex2(ml[i].x - top);
                 l += ml[i].y * take;
 #pragma unroll
