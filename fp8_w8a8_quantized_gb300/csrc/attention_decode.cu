@@ -49,6 +49,10 @@ constexpr int kCtas = 152;           // CTAs at most (one per SM)
 constexpr int64_t kMaxPlan = 4096;   // requests up to which the work is cut by tokens
 constexpr int kBatch = 4;            // parts of a row that are loaded at a time
 constexpr int kWholeSteps = 4;       // steps of a request that one CTA does as a whole
+// What a CTA could have read in the time that it takes to end one request and to
+// get into the next, some 2.5 us (64 requests of 257 to 16001 tokens: 90 us;
+// without it the CTAs with three requests end 8 us after those with one, 92 us).
+constexpr int kEntryBytes = 128 * 1024;
 constexpr int kMinTokens = 64;       // tokens of a request that are worth a CTA
 
 // A request whose steps several CTAs share, for the kernel that joins them.
@@ -159,6 +163,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
     const int G = a.Hq / a.Hkv;
     const int64_t room = a.width * a.page;
     const int step = kTile * sh.ways;
+    const int entry = a.B > 1 ? kEntryBytes / (2 * DP * kTile * W) : 0;
     // (tokens before `skip` are the prefix kernel's)
     auto length = [&](int64_t b) {
         const int64_t n = a.lens[b] < room ? a.lens[b] : room;
@@ -168,9 +173,10 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
     // the line of work
     int64_t per = 0, lo, hi;
     if (planned) {
-        // (a request without tokens has one step: someone has to write its zeros)
+        // (a request without tokens has one step: someone has to write its zeros;
+        // the first `entry` steps of each stand for the time that it takes to get into it)
         auto upto_lane = [&](int64_t b) {
-            int64_t x = b < a.B ? max(divide_up(length(b), step), int64_t(1)) : 0;
+            int64_t x = b < a.B ? max(divide_up(length(b), step), int64_t(1)) + entry : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
@@ -221,7 +227,8 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
     const int64_t begin = lo;
     while (lo < hi) {
         // the request that step `lo` lies in, and how far this CTA goes in it
-        int64_t b, first, end, u0, u1;  // its steps; this CTA's, counted from its first
+        int64_t b, first, end, inside;  // its steps on the line, and how many are before this CTA's
+        int u0, u1;                     // this CTA's steps of tokens
         int group = 0;
         if (planned) {
             int64_t at = lo;
@@ -237,10 +244,11 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
             b = x;
             first = lo - at + upto[b];
             end = lo - at + upto[b + 1];
-            u0 = lo - first;
-            u1 = min(end, hi) - first;
+            inside = lo - first;
+            u0 = static_cast<int>(max(inside - entry, int64_t(0)));
+            u1 = static_cast<int>(max(min(end, hi) - first - entry, int64_t(0)));
             // the CTA that begins a request, or that begins inside one, tells of the cut
-            if (threadIdx.x == 0 && (by_request ? u0 == 0 : u0 > 0 && u0 <= per)) {
+            if (threadIdx.x == 0 && (by_request ? inside == 0 : inside > 0 && inside <= per)) {
                 const bool cut = by_request ? hi < end : true;
                 parts.cuts[by_request ? group * a.B + b : blockIdx.x] =
                     Cut{first, end, cut ? per : 0, static_cast<int32_t>(b), group};
@@ -248,12 +256,12 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
         } else {
             group = static_cast<int>(lo / a.B);
             b = lo - group * a.B;
-            first = end = u0 = 0;
-            u1 = divide_up(length(b), step);
+            first = end = inside = u0 = 0;
+            u1 = static_cast<int>(divide_up(length(b), step));
         }
         const bool whole = !planned || (lo == first && hi >= end);
         const int slot = lo == begin ? 0 : 1;  // (only a CTA's first and last request can be cut)
-        lo = planned ? first + u1 : lo + gridDim.x;
+        lo = planned ? min(end, hi) : lo + gridDim.x;
 
         const int64_t len = length(b);
         const int hk = group / sh.blocks * sh.heads + my_head;
@@ -294,8 +302,8 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
             const int32_t* own_row = a.table + b * a.ld_table;
             const unsigned page = static_cast<unsigned>(a.page);
             // the slot of a lane's token of a step; -1 where there is none
-            auto slot_of = [&](int64_t u) {
-                const int64_t tok = a.skip + (u * sh.ways + way) * kTile + lane;
+            auto slot_of = [&](int u) {
+                const int64_t tok = a.skip + (static_cast<int64_t>(u) * sh.ways + way) * kTile + lane;
                 if (u >= u1 || tok - a.skip >= len) return -1;
                 const unsigned pg = static_cast<unsigned>(tok) / page;
                 const int id = (tok < a.prefix ? a.table : own_row)[pg];
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
                 copy_commit();
             }
             int next = ahead[ST - 1];
-            if (a.splits > 0 && u0 == 0 && way == 0) {
+            if (a.splits > 0 && inside == 0 && way == 0) {
                 // what the prefix kernel has of this request
                 const int64_t stride = static_cast<int64_t>(a.Hkv) * a.B * G;
                 const int64_t at0 = static_cast<int64_t>(hk) * a.B * G + b * G + r0;
@@ -413,7 +421,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
             }
 
             int stage = 0;
-            for (int64_t u = u0; u < u1; ++u) {
+            for (int u = u0; u < u1; ++u) {
                 copy_wait<ST - 2>();
                 __syncwarp();  // step u has landed for all lanes, and all are done with step u - 1
                 const unsigned there = there_of[warp][stage];
