@@ -56,7 +56,7 @@ def fp8_kv_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: tor
     from the front of free_pages (int32) into block_table (int32 [B, width],
     in place) and returns (slot_mapping int64 [max_tokens], positions int32
     [max_tokens], cu_seqlens int32 [B + 1], seq_lens int32 [B], pages_used
-    int32 [1])."""
+    int32 [1]); where none of them is given, the five share one allocation."""
     return _result((_module or _native()).kv_slots(
         ctx_lens, new_lens, free_pages, page_size, block_table, max_tokens, slot_mapping, positions,
         cu_seqlens, seq_lens, pages_used, _handle(stream)), "fp8_kv_slots")

@@ -153,6 +153,16 @@ Tensor make(at::IntArrayRef shape, at::ScalarType dtype, const Tensor& like) {
     return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
 }
 
+// A contiguous tensor in a block that make() gave, from byte `offset` on.
+Tensor carve(const Tensor& block, int64_t offset, at::IntArrayRef shape, at::ScalarType dtype) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(block.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+        c10::scalarTypeToTypeMeta(dtype));
+    t.unsafeGetTensorImpl()->set_storage_offset(offset / static_cast<int64_t>(c10::elementSize(dtype)));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    return t;
+}
+
 PyObject* status(fp8_status_t s) { return PyLong_FromLong(s); }
 
 #define NARGS(want)                                                          \
@@ -174,6 +184,18 @@ PyObject* kv_slots(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     expect(pages, "free_pages", at::kInt, {-1});
     const int64_t ld = table_stride(table, B);
     const Place place(ctx, a[11]);
+    if (!slot.defined() && !pos.defined() && !cu.defined() && !lens.defined() && !used.defined()) {
+        // one allocation for all five (with five the call takes the host 7.7 us instead of 5.2)
+        auto bytes = [](int64_t n) { return (n + 255) / 256 * 256; };
+        const int64_t at_pos = bytes(room * 8), at_cu = at_pos + bytes(room * 4),
+                      at_lens = at_cu + bytes((B + 1) * 4), at_used = at_lens + bytes(B * 4);
+        const Tensor block = make({at_used + 4}, at::kByte, ctx);
+        slot = carve(block, 0, {room}, at::kLong);
+        pos = carve(block, at_pos, {room}, at::kInt);
+        cu = carve(block, at_cu, {B + 1}, at::kInt);
+        lens = carve(block, at_lens, {B}, at::kInt);
+        used = carve(block, at_used, {1}, at::kInt);
+    }
     if (!slot.defined()) slot = make({room}, at::kLong, ctx);
     else expect(slot, "slot_mapping", at::kLong, {room});
     if (!pos.defined()) pos = make({room}, at::kInt, ctx);
