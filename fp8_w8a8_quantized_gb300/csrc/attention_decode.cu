@@ -641,14 +641,18 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
 // do the request of cut x.  A row of few parts is a warp's; the parts of a
 // row that has many are dealt to the CTA's warps, whose sums are then added in
 // the warps' order.
-constexpr int kJoinWarps = 16;
-constexpr int kJoinBatch = 8;  // parts on their way (a CTA a row of 128 parts: one round)
-template <int NT, int DP, int W>
-__global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const DecodeArgs a) {
+//
+// JW: warps of a CTA.  16 where a row is a CTA's (one request of 16383 tokens,
+// 128 parts a row, one round of loads: 13.9 us with the kernel before it; with 8
+// warps 16.4), 8 where it is a warp's (64 ragged requests 88.1 us instead of 88.9:
+// 16 warps of 90 registers have an SM to themselves, and half of them no row).
+constexpr int kJoinBatch = 8;  // parts on their way
+template <int NT, int DP, int W, int JW>
+__global__ void __launch_bounds__(JW * 32) attention_decode_join(const DecodeArgs a) {
     constexpr int R = 8 * NT;
     constexpr int V = DP / 32;
-    __shared__ float s_o[kJoinWarps][DP];
-    __shared__ float2 s_ml[kJoinWarps];
+    __shared__ float s_o[JW][DP];
+    __shared__ float2 s_ml[JW];
     pdl_launch_dependents();
     pdl_wait_primary();
     const Shape sh = shape_of<NT, W>(a.Hq, a.Hkv);
@@ -662,9 +666,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const D
     const int r0 = cut.group % sh.blocks * R, h0 = cut.group / sh.blocks * sh.heads;
     const int rows = min(R, G - r0), items = rows * min(sh.heads, a.Hkv - h0);
     const bool few = last - c0 < 2 * kJoinBatch;
-    const int step = few ? 1 : kJoinWarps, offset = few ? 0 : warp;
-    for (int y = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y; y < items;
-         y += few ? gridDim.y * kJoinWarps : gridDim.y) {
+    const int step = few ? 1 : JW, offset = few ? 0 : warp;
+    for (int y = few ? blockIdx.y * JW + warp : blockIdx.y; y < items;
+         y += few ? gridDim.y * JW : gridDim.y) {
         const int head = y / rows, row = y - head * rows;
         float m = -INFINITY, l = 0.0f, o[V] = {};
         for (int cta = c0 + offset; cta <= last; cta += kJoinBatch * step) {
@@ -718,9 +722,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_decode_join(const D
         __syncthreads();
         if (threadIdx.x < DP) {
             float top = -INFINITY;
-            for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_ml[w].x);
+            for (int w = 0; w < JW; ++w) top = fmaxf(top, s_ml[w].x);
             float sum = 0.0f, all = 0.0f;
-            for (int w = 0; w < kJoinWarps; ++w) {
+            for (int w = 0; w < JW; ++w) {
                 const float take = s_ml[w].x == -INFINITY ? 0.0f : ex2(s_ml[w].x - top);
                 sum += s_o[w][threadIdx.x] * take;
                 all += s_ml[w].y * take;
@@ -770,11 +774,15 @@ struct Launch {
         // few each, most of them, but one may still have almost all.
         const int64_t cuts = a.B * s.groups <= kCtas ? a.B * s.groups : ctas;
         const int64_t rows = s.heads * (a.Hq / a.Hkv < 8 * NT ? a.Hq / a.Hkv : 8 * NT);
-        const int64_t wide = cuts <= 16 ? rows : s.heads;
-        cfg.gridDim = dim3(static_cast<unsigned>(cuts), static_cast<unsigned>(wide));
-        cfg.blockDim = dim3(kJoinWarps * 32);
         cfg.dynamicSmemBytes = 0;
-        return cudaLaunchKernelEx(&cfg, attention_decode_join<NT, DP, W>, a);
+        if (cuts <= 16) {
+            cfg.gridDim = dim3(static_cast<unsigned>(cuts), static_cast<unsigned>(rows));
+            cfg.blockDim = dim3(16 * 32);
+            return cudaLaunchKernelEx(&cfg, attention_decode_join<NT, DP, W, 16>, a);
+        }
+        cfg.gridDim = dim3(static_cast<unsigned>(cuts), static_cast<unsigned>((rows + 7) / 8));
+        cfg.blockDim = dim3(8 * 32);
+        return cudaLaunchKernelEx(&cfg, attention_decode_join<NT, DP, W, 8>, a);
     }
 };
 
