@@ -28,6 +28,13 @@
 // holds of a request whose tokens it has alone goes to `out`, the rest as (m,
 // l, o) to the workspace, from where attention_decode_join adds it up, in the
 // order of the tokens.
+//
+// Measured, heads of 128: 64 requests of 257 to 16001 tokens, 64 / 8 heads, 510
+// MB in 87 us: 3 us to the first copy and 5 until it is there, some 70 at 7.1 to
+// 7.4 TB/s, 8 between the first CTA's end and the last's (more copies in flight
+// make that worse, not better: a ring that runs on into the next request 93 us,
+// one that is refilled a step earlier 96), 5 for the joining kernel.  One request
+// of 16383 tokens, 32 / 8 heads: 13.9 us, of which 5 are bytes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -50,8 +57,9 @@ constexpr int64_t kMaxPlan = 4096;   // requests up to which the work is cut by 
 constexpr int kBatch = 4;            // parts of a row that are loaded at a time
 constexpr int kWholeSteps = 4;       // steps of a request that one CTA does as a whole
 // What a CTA could have read in the time that it takes to end one request and to
-// get into the next, some 2.5 us (64 requests of 257 to 16001 tokens: 90 us;
-// without it the CTAs with three requests end 8 us after those with one, 92 us).
+// get into the next, some 2.5 us (64 requests of 257 to 16001 tokens: 88.8 us;
+// without it the CTAs with three requests end 8 us after those with one, 92.2).
+// Alone, a request has nothing to be balanced against.
 constexpr int kEntryBytes = 128 * 1024;
 constexpr int kMinTokens = 64;       // tokens of a request that are worth a CTA
 

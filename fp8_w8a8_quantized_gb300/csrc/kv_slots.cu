@@ -15,8 +15,12 @@
 // its request by bisection in shared memory.  A token on a page that this very
 // call takes looks the page up in `free`, not in the table, so no CTA reads
 // what another one writes.  (Loads go past L1: the lines that this grid's start
-// found there may be older than what the kernel before it wrote.)  Division by the page size is a multiplication
-// (64-bit divisions alone took 6 of 11 us for 256 requests).
+// found there may be older than what the kernel before it wrote.)  Division by
+// the page size is a multiplication (64-bit divisions alone took 6 of 11 us for
+// 256 requests).
+//
+// Measured: 256 requests with a token each 3.1 us, 96 prompts of up to 1365
+// tokens 4.8 us, back to back in a graph, where any launch takes 2.5 to 3.
 #include <cuda_runtime.h>
 
 #include <cstdint>

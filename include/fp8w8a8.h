@@ -362,7 +362,7 @@ FP8_API fp8_status_t fp8_linear_rmsnorm(const void* x_bf16, const void* gamma_bf
  * token are contiguous.  The cache is the one that fp8_kv_cache_quant_kv
  * writes, E4M3 [n_slots, Hkv, D] each for keys and values, cut into pages of
  * page_size consecutive slots; row b of a block table names the pages of
- * request b in order.  The pages have no counterpart for these operators.
+ * request b in order.
  * ---------------------------------------------------------------------------
  */
 
@@ -473,7 +473,10 @@ FP8_API fp8_status_t fp8_attention_prompt(const void* q, int64_t ldq, const void
  * Attention of one new token per request over the paged FP8 cache:
  *   out[b, h] = bf16_rn( v_scale[hk] sum_{j < len_b} w_j v_j / sum w_j ),
  *   w_j = exp(scale k_scale[hk] q . k_j - max_j),  hk = h / (Hq / Hkv),
- * where token j of request b lies in slot block_table[b, j / p] * p + j % p.
+ * with maximum and sums in fp32, w rounded to f16 for its product with v (the
+ * codes are exact in f16; q is, after a power of two of its own is taken out,
+ * to 2^-38 of its largest element).  Token j of request b lies in slot
+ * block_table[b, j / p] * p + j % p.
  * len_b is seq_lens[b], at least 0 and at most table_width * page_size; a
  * request without tokens gets zeros.  A table entry outside 0 ..
  * n_slots / page_size - 1 hides its page's tokens.
