@@ -12,7 +12,7 @@
 //                   lanes a row, writes P as bf16 over S, rescales O where
 //                   needed and finally writes the rows' output.  P has V's
 //                   type, as an MMA's operands must: each weight is off by up
-//                   to 2^-9 of itself, as the output is by its own rounding;
+//                   to 2^-8 of itself, as the output is by its own rounding;
 //                   their sum l is taken before that.  (Four warps a
 //                   tile, a lane a row, took 1450 clocks a tile, mostly
 //                   latency; the tensor core waits for S -> P of one tile

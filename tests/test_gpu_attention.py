@@ -405,6 +405,16 @@ def test_decode_more_requests_than_are_cut_by_tokens():
     check_decode(cached(gen(42), lens, 18, 1, 32, 16), 16)
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([160 + i % 41 for i in range(200)], 16, 8, 128),
+                                           ([161 + i % 7 for i in range(301)], 8, 8, 64),
+                                           ([0 if i % 3 else 170 for i in range(400)], 8, 8, 128),
+                                           ([1300 + i for i in range(90)], 4, 2, 128),
+                                           ([4000, 0, 1, 0], 32, 8, 128), ([150, 9000], 8, 8, 80)])
+def test_decode_cuts_everywhere_in_a_request(lens, Hq, Hkv, D):
+    # CTAs begin at every place of a request, before its first token too
+    check_decode(cached(gen(49 + D), lens, Hq, Hkv, D, 16), 16)
+
+
 def test_decode_one_long_request_among_many_short_ones():
     lens = [5 + i % 90 for i in range(200)]
     lens[77] = 6001
