@@ -637,9 +637,11 @@ cudaError_t prepare() {
 cudaError_t launch_attention_prompt(const PromptArgs& a, cudaStream_t st) {
     // Too few items for the SMs: smaller ones.  (32 heads on 8 of 128: one prompt
     // of 128 tokens 7.3 us with one tile a CTA, 9.3 with two; of 1024 tokens 23.6
-    // and 20.3, of 4096 tokens 143 and 119.)
-    const int64_t two_tiles = (a.T / (2 * (kRows / (a.Hq / a.Hkv))) + a.B) * a.Hkv;
-    const bool one = two_tiles <= a.num_sms / 2;
+    // and 20.3, of 4096 tokens 143 and 119.)  Prompts that as a rule leave the
+    // second tile empty: the same (128 of 32 tokens 29.0 and 34.3, 256 of 16 42 and
+    // 54, 64 of 64 27.2 and 27.2, 16 of 257 35.0 and 33.7).
+    const int64_t per = 2 * (kRows / (a.Hq / a.Hkv));  // tokens of two tiles
+    const bool one = (a.T / per + a.B) * a.Hkv <= a.num_sms / 2 || a.T <= a.B * per;
     if (a.D <= 64) return one ? launch_tiles<64, 1>(a, st) : launch_tiles<64, 2>(a, st);
     return one ? launch_tiles<128, 1>(a, st) : launch_tiles<128, 2>(a, st);
 }
