@@ -64,28 +64,6 @@ __device__ __forceinline__ float scaled(float x, int n) {
            __uint_as_float(static_cast<uint32_t>(127 + n - h) << 23);
 }
 
-// 16 bytes into shared memory: an asynchronous copy, or zeros at once where
-// there is nothing to copy (`src` is not touched then).
-__device__ __forceinline__ void copy_async16(uint32_t dst, const uint8_t* src, bool there) {
-    if (there)
-        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {  // all but the last N groups have landed
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
 // A query row goes to f16 with its largest element in [2^14, 2^15), which is
 // exact down to 2^-38 of that element; `top` is the row's largest bf16
 // magnitude (bits).  The power of two taken out: 14 - exponent.

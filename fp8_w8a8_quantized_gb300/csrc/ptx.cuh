@@ -150,6 +150,38 @@ __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity, unsi
 }
 
 // ---------------------------------------------------------------------------
+// Asynchronous copies of a thread's own
+// ---------------------------------------------------------------------------
+// 16 or 8 bytes into shared memory: an asynchronous copy, or zeros at once where
+// there is nothing to copy (`src` is not touched then).
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool there) {
+    if (there)
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void* src, bool there) {
+    if (there)
+        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst), "r"(0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the last N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// ---------------------------------------------------------------------------
 // TMA (tiled bulk tensor copies, global -> shared)
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {
