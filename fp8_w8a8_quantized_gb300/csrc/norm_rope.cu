@@ -87,14 +87,15 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
     const int64_t t = w / slices;
     if (t >= a.T) return;
     const int slice = static_cast<int>(w - t * slices);
-    const bool live = chunk < a.D >> 3;
-    const bool turned = kWhole || chunk < a.rot >> 3;
+    const int D = kWhole ? 8 * kLanes : a.D, rot = kWhole ? D : a.rot;
+    const bool live = kWhole || chunk < D >> 3;
+    const bool turned = kWhole || chunk < rot >> 3;
     Runs at;
     if (kPairs) {
         at.first = 8 * chunk;
         at.second = 8 * chunk + 4;
     } else {  // (what is not turned: two runs as well, of the rest's halves)
-        const int from = turned ? 0 : a.rot, size = turned ? a.rot : a.D - a.rot;
+        const int from = turned ? 0 : rot, size = turned ? rot : D - rot;
         at.first = from + 4 * (chunk - (from >> 3));
         at.second = at.first + (size >> 1);
     }
@@ -113,12 +114,12 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
         const uint32_t to = ring + (step - begin) % kDepth * 512;
         if (step < steps_q) {
             const int head = step * kHeads + sub;
-            at.copy(to, a.q + t * a.ldq + head * a.D, live && head < a.Hq);
+            at.copy(to, a.q + t * a.ldq + head * D, live && head < a.Hq);
         } else if (step < end) {
             const bool key = step < steps_q + steps_k;
             const int head = (step - steps_q - (key ? 0 : steps_k)) * kHeads + sub;
-            if (key) at.copy(to, a.k + t * a.ldk + head * a.D, live && head < a.Hkv);
-            else copy_async16(to, a.v + t * a.ldv + head * a.D + chunk * 8, live && head < a.Hkv);
+            if (key) at.copy(to, a.k + t * a.ldk + head * D, live && head < a.Hkv);
+            else copy_async16(to, a.v + t * a.ldv + head * D + chunk * 8, live && head < a.Hkv);
         }
         copy_commit();
     };
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
 
     const int64_t slot = a.k_cache ? (a.slot ? a.slot[t] : t) : -1;
     const bool store = slot >= 0 && slot < a.n_slots;
-    const float inv_d = 1.0f / static_cast<float>(a.D);
+    const float inv_d = 1.0f / static_cast<float>(D);
 
     // this lane's sines and cosines, of its four pairs
     float co[4], si[4];
@@ -207,10 +208,10 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
             const uint4 o = make_uint4(narrow2(y[0], y[1]), narrow2(y[2], y[3]), narrow2(y[4], y[5]),
                                        narrow2(y[6], y[7]));
             if (!live || head >= heads) continue;
-            if (dst) at.store(dst + head * a.D, o);
+            if (dst) at.store(dst + head * D, o);
             if (kind && store) {
                 const float s = a.k_scale[head * a.scale_stride];
-                at.store_codes(a.k_cache + (slot * a.Hkv + head) * a.D, quant8<false>(o, divisor_of(s)));
+                at.store_codes(a.k_cache + (slot * a.Hkv + head) * D, quant8<false>(o, divisor_of(s)));
             }
         }
     }
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
         const int head = step * kHeads + sub;
         if (!live || head >= a.Hkv) continue;
         const float s = a.v_scale[head * a.scale_stride];
-        *reinterpret_cast<uint2*>(a.v_cache + (slot * a.Hkv + head) * a.D + chunk * 8) =
+        *reinterpret_cast<uint2*>(a.v_cache + (slot * a.Hkv + head) * D + chunk * 8) =
             quant8<false>(u, divisor_of(s));
     }
 }
