@@ -20,12 +20,13 @@
 // factors are the same in all of them:
 //   out_i = (x_i A_i + x_partner B_i) / norm,   A_i = gamma_i cos t,
 //                                               B_i = -+ gamma_partner sin t,
-// and takes kBatch heads' loads at a time.
+// and the heads come through a ring of its own in shared memory, by asynchronous
+// copies (loads into registers, two steps at a time: 69 us instead of 64).
 //
 // Measured: 8192 tokens of 64 + 8 heads of 128 and 8 of values, with norms and
-// the cache write: 335 MB in 69 us, 4.8 TB/s, 73% of a plain copy's rate.  What
-// is left is latency: 64 registers a thread keep 41% of the warps' places
-// filled, and issue slots are 58% taken.  32 tokens: 2.7 us, the launch.
+// the cache write: 335 MB in 60 us, 5.6 TB/s, 83% of a plain copy's rate.  What
+// is left is instructions: three of four issue slots are taken while all warps
+// run, and the last tokens leave SMs idle.  32 tokens: 2.6 us, the launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
