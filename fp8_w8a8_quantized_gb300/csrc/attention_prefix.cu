@@ -339,8 +339,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
         // lane / kChunks and of the next row that another permutation meets
         constexpr int kStep = 32 / kChunks;           // rows between two chunks of a lane
         const int r0 = lane / kChunks;
-        const uint32_t at[2][2] = {{tile_chunk(r0, 2 * ch), tile_chunk(r0, 2 * ch + 1)},
-                                   {tile_chunk(r0 + kStep, 2 * ch), tile_chunk(r0 + kStep, 2 * ch + 1)}};
+        // (of eight lanes with one row, four store their second half first: with the
+        // first halves alone each bank would be met twice; 256 requests, 16384 tokens,
+        // 64 / 8 heads: 197 us instead of 202)
+        const bool swap = kChunks == 8 && ch >= 4;
+        const uint32_t c0 = 2 * ch + (swap ? 1 : 0), c1 = 2 * ch + (swap ? 0 : 1);
+        const uint32_t at[2][2] = {{tile_chunk(r0, c0), tile_chunk(r0, c1)},
+                                   {tile_chunk(r0 + kStep, c0), tile_chunk(r0 + kStep, c1)}};
         int job = warp - kMainWarps - 1;
         int now = slot_of(job), next = slot_of(job + kLoadWarps);
         if (job < jobs) {
@@ -365,8 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
                     // rows 8 apart have the same permutation
                     const int odd = kStep < 8 ? i & 1 : 0;
                     const uint32_t down = dst + 128 * kStep * (i - odd);
-                    st_shared16(down + at[odd][0], f16_lo(u.x), f16_hi(u.x), f16_lo(u.y), f16_hi(u.y));
-                    st_shared16(down + at[odd][1], f16_lo(u.z), f16_hi(u.z), f16_lo(u.w), f16_hi(u.w));
+                    const uint32_t w[4] = {swap ? u.z : u.x, swap ? u.w : u.y, swap ? u.x : u.z, swap ? u.y : u.w};
+                    st_shared16(down + at[odd][0], f16_lo(w[0]), f16_hi(w[0]), f16_lo(w[1]), f16_hi(w[1]));
+                    st_shared16(down + at[odd][1], f16_lo(w[2]), f16_hi(w[2]), f16_lo(w[3]), f16_hi(w[3]));
                 }
                 __syncwarp();  // the codes are read: the next ones may come
                 if (more) copy(job + kLoadWarps, next, h);
