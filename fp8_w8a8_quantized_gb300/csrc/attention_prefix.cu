@@ -23,10 +23,11 @@
 //     decode kernel spent 7 us a request on 16 of them.)
 //
 // Measured: 64 requests, 32 / 8 heads of 128, 8192 tokens shared and 1 to 777 of
-// their own: 37.7 us with the kernels after it; 121 without this one.  Its 20 us
+// their own: 38 us with the kernels after it; 121 without this one.  Its 20 us
 // are 2.3 until the first codes are asked for, 3 until S of the first key tile
-// is there, 2 a key tile (the load warps: copy and conversion of 32 tokens take a
-// warp 1.5), 1 for the last P V, 2.5 to have all parts of a cluster in shared
+// is there, 2 a key tile (two softmaxes in turn, each slowed to 2600 clocks by the
+// load warps beside them, which take 3000 for 32 tokens and wait for nothing), 1
+// for the last P V, 2.5 to have all parts of a cluster in shared
 // memory and 4.3 to add them up (128 KB a CTA, three quarters from other SMs; the
 // order and the number of loads on their way make no difference).
 #include <cuda_runtime.h>
