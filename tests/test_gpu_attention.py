@@ -262,6 +262,19 @@ def test_prompt_unseen_values_have_no_influence(bad):
             assert torch.isnan(got[t:{149: 150, 220: 240}[t], :2]).all()
 
 
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_prompt_bits_do_not_depend_on_its_company(D):
+    # alone, before many short ones (one query tile a CTA), four times over (two)
+    q, k, v, _ = packed(gen(23), [700] + [20] * 300, 32, 8, D)
+    parts = [t[:700].contiguous() for t in (q, k, v)]
+    alone = pkg.fp8_attention_prompt(*parts, int32([0, 700]))
+    among = pkg.fp8_attention_prompt(q, k, v, int32([0] + [700 + 20 * i for i in range(301)]))
+    four = pkg.fp8_attention_prompt(*(torch.cat([t] * 4) for t in parts), int32([0, 700, 1400, 2100, 2800]))
+    settled()
+    assert torch.equal(among[:700], alone)
+    assert all(torch.equal(four[700 * i: 700 * i + 700], alone) for i in range(4))
+
+
 def test_prompt_rows_outside_every_sequence_are_left():
     q, k, v, _ = packed(gen(3), [60], 4, 4, 64)
     out = torch.full((60, 4, 64), 9.0, dtype=torch.bfloat16, device=DEV)
