@@ -29,7 +29,7 @@ LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 SOURCES = ["api.cu", "quant.cu", "quant_variants.cu", "norm_quant.cu", "gemm_pair.cu", "gemm_decode.cu", "gemm_blockwise.cu", "noalloc.cu",
            "selftest.cu", "attention_api.cu", "kv_slots.cu", "norm_rope.cu", "attention_prompt.cu", "attention_decode.cu",
            "attention_prefix.cu"]
-HEADERS = ["ptx.cuh", "launch.h", "quant_math.cuh", "decode_common.cuh", "attention_tile.cuh"]
+HEADERS = ["ptx.cuh", "launch.h", "quant_math.cuh", "decode_common.cuh", "attention_plan.h", "attention_tile.cuh"]
 
 # The binding's extension module (host code only; links the library and torch).
 MODULE_SOURCE = "attention_binding.cpp"

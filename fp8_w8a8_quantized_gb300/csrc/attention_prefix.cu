@@ -34,6 +34,7 @@
 
 #include <cstdint>
 
+#include "attention_plan.h"
 #include "attention_tile.cuh"
 #include "launch.h"
 #include "ptx.cuh"
@@ -42,13 +43,11 @@
 namespace fp8k {
 namespace {
 
-constexpr int kStages = 4;
+constexpr int kStages = kPrefixStages;
 constexpr int kMainWarps = 16;                 // softmax: 8 a query tile
 constexpr int kLoadWarps = 7;
 constexpr int kMainRegs = 88, kSideRegs = 64;  // 512 x 88 + 256 x 64 = 768 x 80, the launch's
 constexpr int kThreads = 32 * (kMainWarps + 1 + kLoadWarps);
-constexpr int kMaxCluster = 4;  // (clusters of 8 found room for fewer CTAs: 71 us instead of 47)
-constexpr int kFillSms = 152;                  // CTAs that the parts should come to
 
 struct Bars {
     uint64_t full[kStages], empty[kStages];
@@ -57,7 +56,7 @@ struct Bars {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    uint32_t there[kStages][4];  // which tokens of a key tile exist
+    uint32_t there[kThereRows][4];  // which tokens of a key tile exist: there_row()
     float2 ml[2 * kRows];        // (m, l) of this CTA's part, m in log2 units
 };
 
@@ -191,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
                     hide_after(s, 0, limit[0] - 1 - key0);
                     hide_after(s, 1, limit[1] - 1 - key0);
                 }
-                const volatile uint32_t* there = bars->there[2 * j % kStages];
+                const volatile uint32_t* there = bars->there[there_row(j)];
                 const uint32_t word[4] = {there[0], there[1], there[2], there[3]};
                 if ((word[0] & word[1] & word[2] & word[3]) != 0xFFFFFFFFu) {
 #pragma unroll
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
         bool ok = n > 0 && ready(&bars->q_full, 0) && landed(0);
         for (int j = 0; ok && j <= n; ++j) {
             // P V of tile j - 1 and S of tile j; what they read is there
-            const uint32_t kk = 2 * j % kStages, vv = (2 * j + kStages - 1) % kStages;
+            const uint32_t kk = key_stage(j), vv = value_stage(j - 1);  // (j = 0: not used)
             const uint32_t kd = desc_kmajor(base_kv + uniform(kk) * kTile);
             const uint32_t vd = desc_nmajor(base_kv + uniform(vv) * kTile, kColBytes);
             tc_fence_after();
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             const bool more = job + kLoadWarps < jobs;
             if (!warp_ready(&bars->empty[stage], (n / kStages & 1u) ^ 1u, abort_flag, status)) break;
             const unsigned votes = __ballot_sync(0xFFFFFFFFu, now >= 0);
-            if (lane == 0 && !(n & 1)) *const_cast<volatile uint32_t*>(&bars->there[stage][job & 3]) = votes;
+            if (lane == 0 && !(n & 1)) *const_cast<volatile uint32_t*>(&bars->there[there_row(n >> 1)][job & 3]) = votes;
             const uint32_t dst = sKV + stage * kTile + (job & 3) * 32 * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -440,37 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
 }
 
 }  // namespace
-
-PrefixPlan prefix_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix) {
-    PrefixPlan p = {};
-    p.dim = D <= 64 ? 64 : 128;
-    p.all_rows = B * Hq;
-    if (B < 2 || prefix < kKeys) return p;
-    const int64_t tpt = kRows / (Hq / Hkv);
-    p.row_blocks = (B + 2 * tpt - 1) / (2 * tpt);
-    const int64_t tiles = (prefix + kKeys - 1) / kKeys, items = p.row_blocks * Hkv;
-    int64_t splits = items >= kFillSms ? 1 : kFillSms / items;
-    if (splits > tiles) splits = tiles;
-    p.cluster = splits >= kMaxCluster ? kMaxCluster : splits >= 2 ? 2 : 1;
-    splits = splits / p.cluster * p.cluster;
-    p.tiles = static_cast<int>((tiles + splits - 1) / splits);
-    // Worth it where it is faster than the decode kernel on the same tokens, by
-    // what both were measured to need (page size 16, 300 tokens beside the
-    // prefix): that one reads B times the prefix, out of L2 mostly, at 8.6
-    // bytes/ps with 8 heads of 128, 5 with heads of 64; this one costs 18 us
-    // and 2.4 us a key tile of a CTA.  At 32/8 heads of 128, own reading
-    // against this: B = 16, 8192 tokens 45 / 35 us, 2048 tokens 22 / 29; B = 64,
-    // 2048 tokens 43 / 31, 512 tokens 21 / 29; B = 4, 32768 tokens 44 / 59.
-    const double own_us = static_cast<double>(B) * prefix * 2 * Hkv * D / (D > 64 ? 8.6e6 : 5.0e6);
-    if (own_us < 18.0 + 2.4 * p.tiles) {
-        p.tiles = 0;
-        return p;
-    }
-    // whole clusters (the last parts may be empty), and no empty ones
-    const int64_t used = (tiles + p.tiles - 1) / p.tiles;
-    p.splits = static_cast<int>((used + p.cluster - 1) / p.cluster * p.cluster);
-    return p;
-}
 
 cudaError_t launch_attention_prefix(const DecodeArgs& a, const PrefixPlan& plan, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};

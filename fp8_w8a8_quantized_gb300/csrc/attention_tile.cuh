@@ -21,6 +21,7 @@
 
 #include <cstdint>
 
+#include "attention_plan.h"
 #include "ptx.cuh"
 #include "quant_math.cuh"
 
@@ -28,8 +29,6 @@ namespace fp8k {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // log2 of how far p may exceed 1 before m moves
-constexpr int kRows = 128;      // rows of a query tile
-constexpr int kKeys = 128;      // keys of a tile
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);

@@ -7,6 +7,7 @@
 
 #include <cstdint>
 
+#include "attention_plan.h"
 #include "fp8w8a8.h"
 
 namespace fp8k {
@@ -179,19 +180,8 @@ struct DecodeArgs {
 cudaError_t launch_attention_decode(const DecodeArgs& a, cudaStream_t st);
 size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix);
 
-// The tokens that all requests share, read once for all (attention_prefix.cu).
-struct PrefixPlan {
-    int splits;          // parts of the prefix (0: not worth it, the decode kernel reads it)
-    int cluster;         // CTAs of a cluster: parts that are added up before they are written
-    int tiles;           // key tiles of a part
-    int dim;             // D rounded up to 64 or 128
-    int64_t row_blocks;  // blocks of query rows
-    int64_t all_rows;    // B * Hq
-    int parts() const { return splits ? splits / cluster : 0; }
-    int64_t rows() const { return parts() * all_rows; }
-    size_t parts_bytes() const { return static_cast<size_t>(rows()) * (dim * 4 + 8); }
-};
-PrefixPlan prefix_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix);
+// The tokens that all requests share, read once for all (attention_prefix.cu;
+// the plan: attention_plan.h).
 cudaError_t launch_attention_prefix(const DecodeArgs& a, const PrefixPlan& plan, cudaStream_t st);
 
 // The current device's SM count and status word, after the same checks as

@@ -1,0 +1,97 @@
+"""GPU tests of decode attention's shared-prefix kernel where a CTA has three
+key tiles and more: its ring of keys and values goes round, running maxima move
+on past the second tile, and the prefix ends inside a tile or has pages that do
+not exist.  Checked against the 64-bit formula, and every case a hundred times
+for the same bits.
+
+Tolerances: bf16's rounding of the result (2^-8), f16's of each weight (2^-11 of
+its share of the weighted |v|), 2^-12 of the weighted |v| for fp32 products,
+sums and exponentials."""
+import pytest
+import torch
+
+import attention_ref as ref
+
+DEV = "cuda"
+
+# requests, query heads, key heads, dim, page, prefix
+CASES = [(24, 32, 8, 128, 16, 8200), (64, 8, 8, 64, 16, 12000), (128, 16, 8, 64, 16, 8016),
+         (100, 32, 8, 64, 20, 3001), (64, 64, 8, 128, 16, 4001), (33, 8, 8, 64, 7, 20001),
+         (24, 32, 32, 64, 1, 4200), (150, 64, 8, 128, 64, 1100), (300, 64, 32, 64, 16, 705),
+         (90, 28, 4, 80, 16, 5000)]
+
+
+def cached(seed, B, Hq, Hkv, D, page, prefix, own=40):
+    """Queries, a cache in shuffled pages, a table whose rows share the prefix's whole pages, lengths past it."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    lens = prefix + torch.randint(0, own, (B,), generator=g, device=DEV, dtype=torch.int32)
+    width, shared = -(-(prefix + own) // page), prefix // page
+    n_pages = shared + B * (width - shared) + 2
+    order = torch.randperm(n_pages, generator=g, device=DEV).to(torch.int32)
+    table = torch.cat([order[:shared].expand(B, shared),
+                       order[shared: shared + B * (width - shared)].view(B, width - shared)], 1).contiguous()
+    codes = [(torch.randn(n_pages * page, Hkv, D, generator=g, device=DEV) * 3).to(torch.float8_e4m3fn)
+             .view(torch.uint8) for _ in range(2)]
+    scales = [torch.rand(Hkv, generator=g, device=DEV) * 0.2 + 0.2 for _ in range(2)]
+    q = torch.randn(B, Hq, D, generator=g, device=DEV).to(torch.bfloat16)
+    return [q, codes[0], codes[1], scales[0], scales[1], table, lens]
+
+
+def formula(q, k_cache, v_cache, k_scale, v_scale, table, lens, page, prefix, scale=None):
+    """(out, weighted |v|) in 64 bits."""
+    values = ref.e4m3_values().to(DEV)
+    B, Hq, D = q.shape
+    Hkv = k_cache.shape[1]
+    n_pages = k_cache.shape[0] // page
+    out, size = (torch.zeros(B, Hq, D, dtype=torch.float64, device=DEV) for _ in range(2))
+    for b, n in enumerate(lens.tolist()):
+        j = torch.arange(max(0, min(n, table.shape[1] * page)), device=DEV)
+        pg = torch.where(j < prefix, table[0].long()[j // page], table[b].long()[j // page])
+        slots = (pg * page + j % page)[(pg >= 0) & (pg < n_pages)]
+        if not slots.numel():
+            continue
+        k = values[k_cache[slots].long()] * k_scale.double()[:, None]
+        v = values[v_cache[slots].long()] * v_scale.double()[:, None]
+        s = torch.einsum("hgd,nhd->hgn", q[b].double().view(Hkv, -1, D), k) * (D ** -0.5 if scale is None else scale)
+        w = torch.softmax(s, -1)
+        out[b] = torch.einsum("hgn,nhd->hgd", w, v).view(Hq, D)
+        size[b] = torch.einsum("hgn,nhd->hgd", w, v.abs()).view(Hq, D)
+    return out.cpu(), size.cpu()
+
+
+def settled():
+    import fp8_w8a8_quantized_gb300 as pkg
+    torch.cuda.synchronize()
+    assert pkg.fp8_device_status() == pkg.FP8_OK
+
+
+def decode(args, page, prefix, **more):
+    import fp8_w8a8_quantized_gb300 as pkg
+    return pkg.fp8_attention_decode(*args, page, prefix_len=prefix, **more)
+
+
+def check(args, page, prefix, what, times=100):
+    first = decode(args, page, prefix)
+    again = [decode(args, page, prefix) for _ in range(times)]
+    settled()
+    want, size = formula(*args, page, prefix)
+    ref.check(first, want, ref.U_BF16 * want.abs() + (ref.U_FP16 + ref.SUMS) * size, what)
+    assert all(torch.equal(first, x) for x in again), what
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_ring(case):
+    B, Hq, Hkv, D, page, prefix = case
+    args = cached(prefix + D, *case)
+    check(args, page, prefix, "whole")
+    # pages that do not exist: in the last key tile, in the one two before it, and further on
+    table = args[5]
+    for tile in {max(0, -(-prefix // 128) - 1 - i) for i in (0, 2, 5, 9, 13)}:
+        table[0, (128 * tile + 3) // page] = -1
+    check(args, page, prefix, "missing pages")
+    # requests that end inside the prefix
+    lens = args[6]
+    lens[1], lens[2], lens[B // 2], lens[B - 1] = 0, 1, prefix // 2, prefix - 129
+    check(args, page, prefix, "short requests")
