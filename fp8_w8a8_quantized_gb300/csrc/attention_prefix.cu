@@ -57,6 +57,7 @@ struct Bars {
     uint32_t tmem_base;
     int abort;
     uint32_t there[kThereRows][4];  // which tokens of a key tile exist: there_row()
+    int lost_from;               // first key tile of this CTA whose values lost NaN
     float2 ml[2 * kRows];        // (m, l) of this CTA's part, m in log2 units
 };
 
@@ -74,6 +75,57 @@ __device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
+}
+
+// NaN codes among the 16 E4M3 values at `addr` in shared memory become zeros;
+// whether there were any.
+__device__ __forceinline__ bool take_nan(uint32_t addr) {
+    const uint4 u = ld_shared16(addr);
+    uint32_t w[4] = {u.x, u.y, u.z, u.w}, found = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // (seven ones carry into the byte's top bit)
+        const uint32_t nan = ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+        found |= nan;
+        w[i] &= ~((nan >> 7) * 0xFFu);
+    }
+    if (found) st_shared16(addr, w[0], w[1], w[2], w[3]);
+    return found != 0;
+}
+
+// Gives O back the NaN of the values that a lane's rows see and that the load
+// warps took out (rare, and slow): of tokens `from` .. to - 1, values v.
+template <int DP>
+__device__ __noinline__ void add_nan(uint32_t tO, const uint8_t* v, int64_t row_bytes, int D, const int32_t* table,
+                                     unsigned page, int64_t n_pages, int from, int to0, int to1) {
+    const int t = lane_id() & 3;
+#pragma unroll 1
+    for (int b = 0; b < DP / 32; ++b) {
+        uint32_t o[16];
+        __syncwarp();
+        tmem_ld_16x256b_x4(tO + 32 * b, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[i]));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            for (int tok = from; tok < (e ? to1 : to0); ++tok) {
+                const unsigned pg = static_cast<unsigned>(tok) / page;
+                const int id = table[pg];
+                if (id < 0 || id >= n_pages) continue;
+                const uint8_t* at = v + (id * static_cast<int64_t>(page) + (tok - pg * page)) * row_bytes + 32 * b + 2 * t;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int d = 8 * (i >> 1) + (i & 1);
+                    if (32 * b + 2 * t + d < D && (at[d] & 0x7Fu) == 0x7Fu)
+                        o[4 * (i >> 1) + 2 * e + (i & 1)] = 0x7FFFFFFFu;
+                }
+            }
+        }
+        __syncwarp();
+        tmem_st_16x256b_x4(tO + 32 * b, o);
+    }
+    tmem_st_wait();
 }
 
 template <int DP>
@@ -103,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
         }
         mbar_init(&bars->drain, 1);
         bars->abort = 0;
+        bars->lost_from = INT32_MAX;
         fence_mbar_init();
     }
     if (warp == kMainWarps) {
@@ -206,6 +259,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             }
             if (ok && (ok = warp_ready(&bars->o_full[x], 0, abort_flag, status))) {
                 tc_fence_after();
+                const int lost = *reinterpret_cast<volatile int*>(&bars->lost_from);
+                if (lost < tiles) {
+                    const int end = (tile0 + tiles) * kKeys;
+                    add_nan<DP>(tO, a.v_cache + static_cast<int64_t>(hk) * a.D, static_cast<int64_t>(a.Hkv) * a.D, a.D,
+                                a.table, static_cast<unsigned>(a.page), a.n_pages, (tile0 + lost) * kKeys,
+                                real[0] ? min(limit[0], end) : 0, real[1] ? min(limit[1], end) : 0);
+                }
                 // Tile A's part goes where the queries were (S of both tiles is complete by
                 // now), B's where keys and values were (it is the last MMA that reads them).
                 float* part = reinterpret_cast<float*>(smem + (x == 0 ? 0 : 2 * kTile));
@@ -352,6 +412,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             copy(job, now, 0);
             copy(job, now, 1);
         }
+        // The tokens that every request of this CTA sees.  Beyond them a weight may be
+        // 0 beside a value that is NaN, and 0 NaN is NaN: there such values are set to 0,
+        // and the rows that see them get them back with their output.
+        int all_see = static_cast<int>(a.prefix);
+        for (int64_t b = b0 + lane; b < min(b0 + 2 * tpt, a.B); b += 32) all_see = min(all_see, max(a.lens[b], 0));
+        all_see = __reduce_min_sync(0xFFFFFFFFu, all_see);
         for (; job < jobs; job += kLoadWarps) {
             const int n = job >> 2, stage = n % kStages;  // tile 2 j: keys, 2 j + 1: values of key tile j
             const int later = slot_of(job + 2 * kLoadWarps);
@@ -360,10 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             const unsigned votes = __ballot_sync(0xFFFFFFFFu, now >= 0);
             if (lane == 0 && !(n & 1)) *const_cast<volatile uint32_t*>(&bars->there[there_row(n >> 1)][job & 3]) = votes;
             const uint32_t dst = sKV + stage * kTile + (job & 3) * 32 * 128;
+            const int tile = job >> 3;  // of this CTA
+            const bool guard = (job & 4) && min(static_cast<int64_t>(tile0 + tile + 1) * kKeys, a.prefix) > all_see;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 copy_wait<1>();
                 __syncwarp();
+                if (guard) {
+#pragma unroll 1
+                    for (int i = h * kChunks / 2; i < (h + 1) * kChunks / 2; ++i)
+                        if (take_nan(raw + 512 * i + 16 * lane)) atomicMin(&bars->lost_from, tile);
+                }
 #pragma unroll
                 for (int i = h * kChunks / 2; i < (h + 1) * kChunks / 2; ++i) {
                     const uint4 u = ld_shared16(raw + 512 * i + 16 * lane);

@@ -95,3 +95,54 @@ def test_ring(case):
     lens = args[6]
     lens[1], lens[2], lens[B // 2], lens[B - 1] = 0, 1, prefix // 2, prefix - 129
     check(args, page, prefix, "short requests")
+
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [CASES[0], CASES[2], CASES[3], CASES[8], CASES[9]], ids=lambda c: "-".join(map(str, c)))
+def test_nan_codes_reach_only_the_requests_that_see_them(case):
+    B, Hq, Hkv, D, page, prefix = case
+    args = cached(prefix + 7, *case)
+    lens, row = args[6], args[5][0].tolist()
+    g, head, channel = Hq // Hkv, Hkv - 1, D - 3
+    # requests that end at many places of the prefix; the others see all of it
+    for b in range(1, B, 3):
+        lens[b] = (b * 977 + 1) % prefix
+    clean = decode(args, page, prefix)
+    settled()
+    assert torch.isfinite(clean).all()
+    # a value that some requests see, in the first key tile, in the middle and at the end
+    for tok in (1, prefix // 2, prefix - 1):
+        slot = row[tok // page] * page + tok % page
+        bad = list(args)
+        bad[2] = args[2].clone()
+        bad[2][slot, head, channel] = 0xFF
+        got = decode(bad, page, prefix)
+        settled()
+        sees = (lens > tok).cpu()
+        assert sees.any() and (tok == 1 or not sees.all())
+        mine = torch.zeros(B, Hq, D, dtype=torch.bool)
+        mine[sees, head * g: (head + 1) * g, channel] = True
+        assert torch.isnan(got.cpu()[mine]).all(), tok
+        assert torch.equal(got.cpu()[~mine], clean.cpu()[~mine]), tok
+        # and a key: the heads that read it
+        bad = list(args)
+        bad[1] = args[1].clone()
+        bad[1][slot, 0, 5] = 0x7F
+        got = decode(bad, page, prefix)
+        settled()
+        mine = torch.zeros(B, Hq, D, dtype=torch.bool)
+        mine[sees, :g] = True
+        assert torch.isnan(got.cpu()[mine]).all(), tok
+        assert torch.equal(got.cpu()[~mine], clean.cpu()[~mine]), tok
+    # values that nobody sees
+    bad = list(args)
+    bad[2] = args[2].clone()
+    keep = int(lens.max())
+    lens.clamp_(max=prefix - 300)
+    clean = decode(args, page, prefix)
+    for tok in range(prefix - 300, prefix):
+        bad[2][row[tok // page] * page + tok % page] = 0x7F
+    got = decode(bad, page, prefix)
+    settled()
+    assert keep > prefix and torch.equal(got, clean) and torch.isfinite(got).all()
