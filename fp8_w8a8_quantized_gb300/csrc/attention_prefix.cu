@@ -214,7 +214,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             const int shift = query_shift(top);
+            // (never 0, which would make -inf of a masked score and the first maximum NaN;
+            // |s| < 2^31, so below 2^-126 all weights of the row are 1 anyhow)
             c[e] = scaled(unit, -shift);
+            if (fabsf(c[e]) < 0x1p-126f) c[e] = 0x1p-126f;
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) {
                 const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};

@@ -146,3 +146,24 @@ def test_nan_codes_reach_only_the_requests_that_see_them(case):
     got = decode(bad, page, prefix)
     settled()
     assert keep > prefix and torch.equal(got, clean) and torch.isfinite(got).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [CASES[0], CASES[2], CASES[7]], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("exponent", [-133, -126, -120])
+def test_queries_at_the_end_of_bf16(case, exponent):
+    # the largest element of a query is a power of two as small as bf16 has: all weights alike, and the
+    # factor that turns products into logarithms of weights has no digits left in fp32
+    B, Hq, Hkv, D, page, prefix = case
+    args = cached(prefix + 11, *case)
+    args[0] = (args[0].float().sign() * 2.0 ** exponent).to(torch.bfloat16)
+    assert args[0].any()
+    args[3] = torch.full_like(args[3], 2.0 ** -9)
+    args[6][1::4] = prefix - 200
+    got, alone = decode(args, page, prefix), decode(args, page, 0)
+    settled()
+    want, size = formula(*args, page, prefix)
+    tol = ref.U_BF16 * want.abs() + (ref.U_FP16 + ref.SUMS) * size
+    ref.check(got, want, tol, "shared")
+    if prefix % page == 0:
+        ref.check(alone, want, tol, "alone")
