@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
             for (int k = 0; k < kMaxCluster; ++k) top = k < ctas ? fmaxf(top, ml[k].x) : top;
 #pragma unroll
             for (int k = 0; k < kMaxCluster; ++k) {
-                if (k >= ctas || ml[k].x == -INFINITY) continue;  // (an empty part has written nothing)
+                // (an empty part has written nothing; a row whose scores are all NaN has no maximum, but a sum)
+                if (k >= ctas || ml[k].y == 0.0f) continue;
                 const float take = ex2(ml[k].x - top);
                 sum += ml[k].y * take;
                 o[0] += v[k].x * take, o[1] += v[k].y * take, o[2] += v[k].z * take, o[3] += v[k].w * take;

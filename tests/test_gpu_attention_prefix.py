@@ -167,3 +167,23 @@ def test_queries_at_the_end_of_bf16(case, exponent):
     ref.check(got, want, tol, "shared")
     if prefix % page == 0:
         ref.check(alone, want, tol, "alone")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [CASES[0], CASES[2]], ids=lambda c: "-".join(map(str, c)))
+def test_a_nan_query_stays_one(case):
+    B, Hq, Hkv, D, page, prefix = case
+    args = cached(prefix + 13, *case)
+    lens = args[6]
+    lens[3], lens[4], lens[5] = prefix, prefix + 5, prefix - 1000
+    clean = decode(args, page, prefix)
+    bad = list(args)
+    bad[0] = args[0].clone()
+    mine = torch.zeros(B, Hq, D, dtype=torch.bool)
+    for b in (3, 4, 5, B - 1):
+        bad[0][b, Hq - 2, 1] = float("nan")
+        mine[b, Hq - 2] = True
+    got = decode(bad, page, prefix)
+    settled()
+    assert torch.isnan(got.cpu()[mine]).all()
+    assert torch.equal(got.cpu()[~mine], clean.cpu()[~mine])
