@@ -1,6 +1,6 @@
 // Attention of one new token per request over the paged FP8 cache:
 //   out[b, h] = v_scale sum_j w_j v_j / sum_j w_j,
-//   w_j = 2^(y_j - m),  y_j = scale log2(e) k_scale q . k_j
+//   w_j = 2^(y_j - m + 7),  y_j = scale log2(e) k_scale q . k_j   (7: kLift)
 // in one pass over the cached tokens with the running maximum m, the running
 // sum l and the running output o of the softmax (as in attention_prompt.cu: m
 // follows the maximum in steps of at least 2^8).
@@ -500,8 +500,8 @@ __global__ void __launch_bounds__(W * 32, 1) attention_decode(const DecodeArgs a
                 uint32_t p[2][NT][2];
 #pragma unroll
                 for (int y = 0; y < NT; ++y) {
-                    const float b0 = m[y][0] == -INFINITY ? 0.0f : m[y][0];
-                    const float b1 = m[y][1] == -INFINITY ? 0.0f : m[y][1];
+                    const float b0 = m[y][0] == -INFINITY ? 0.0f : m[y][0] - kLift;
+                    const float b1 = m[y][1] == -INFINITY ? 0.0f : m[y][1] - kLift;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll

@@ -1,8 +1,8 @@
 // The shared-prefix part of decode attention: the queries of all requests
 // against tokens that all of them share, which are read once for all.
 //
-//   s = q . k,  p = 2^(c s - c m),  o = sum p v     (attention_tile.cuh; c = scale
-//                                                    log2(e) k_scale of the row)
+//   s = q . k,  p = 2^(c s - c m + 7),  o = sum p v   (attention_tile.cuh; c = scale
+//                                                      log2(e) k_scale of the row)
 //
 // With B requests this is a product of B G query rows a key head with the
 // prefix, bound by the tensor cores once B G is some 100 rows, where reading

@@ -29,6 +29,11 @@ namespace fp8k {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // log2 of how far p may exceed 1 before m moves
+// f16 holds 11 digits down to 2^-14 only, so where P is f16 all of p, in the sum l as
+// in P, is taken 2^7 times (it reaches 2^15 with the slack): weights keep their digits
+// down to 2^-21 of the largest one.  (One token with nearly all of the weight and a
+// value near 0 leaves the result to such weights: 2000 of 2^-20.6 were 4% off.)
+constexpr float kLift = 7.0f;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -147,8 +152,9 @@ template <bool kBf16, int DP, bool kAhead, typename Half>
 __device__ __forceinline__ void softmax_tile(uint32_t (&s)[4][16], uint32_t tS, uint32_t tO,
                                              SoftmaxRows& rows, const float (&c)[2],
                                              const bool (&real)[2], bool started, Half half) {
-    float base[2] = {rows.m[0] == -INFINITY ? 0.0f : -rows.m[0] * c[0],
-                     rows.m[1] == -INFINITY ? 0.0f : -rows.m[1] * c[1]};
+    constexpr float lift = kBf16 ? 0.0f : kLift;
+    float base[2] = {rows.m[0] == -INFINITY ? 0.0f : lift - rows.m[0] * c[0],
+                     rows.m[1] == -INFINITY ? 0.0f : lift - rows.m[1] * c[1]};
     uint32_t p[16];
     float sum[2][2] = {};
     if (kAhead) weights_of<kBf16>(s, 0, c, base, p, sum);
@@ -184,7 +190,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&s)[4][16], uint32_t tS, 
             rows.m[e] = raise[e] ? top[e] : rows.m[e];
             rows.l[e][0] *= keep[e];
             rows.l[e][1] *= keep[e];
-            base[e] = rows.m[e] == -INFINITY ? 0.0f : -rows.m[e] * c[e];
+            base[e] = rows.m[e] == -INFINITY ? 0.0f : lift - rows.m[e] * c[e];
             sum[e][0] = sum[e][1] = 0.0f;
         }
         if (started) {

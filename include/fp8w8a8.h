@@ -473,9 +473,9 @@ FP8_API fp8_status_t fp8_attention_prompt(const void* q, int64_t ldq, const void
  * Attention of one new token per request over the paged FP8 cache:
  *   out[b, h] = bf16_rn( v_scale[hk] sum_{j < len_b} w_j v_j / sum w_j ),
  *   w_j = exp(scale k_scale[hk] q . k_j - max_j),  hk = h / (Hq / Hkv),
- * with maximum and sums in fp32, w rounded to f16 for its product with v (the
- * codes are exact in f16; q is, after a power of two of its own is taken out,
- * to 2^-38 of its largest element).  Token j of request b lies in slot
+ * with maximum and sums in fp32, w rounded to f16 for its product with v (11
+ * digits down to 2^-21 of the largest w; the codes are exact in f16; q is, after
+ * a power of two of its own is taken out, to 2^-38 of its largest element).  Token j of request b lies in slot
  * block_table[b, j / p] * p + j % p.
  * len_b is seq_lens[b], at least 0 and at most table_width * page_size; a
  * request without tokens gets zeros.  A table entry outside 0 ..
