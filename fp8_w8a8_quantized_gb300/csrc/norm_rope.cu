@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(const QkNormRopeArgs
         *reinterpret_cast<uint2*>(a.v_cache + (slot * a.Hkv + head) * D + chunk * 8) =
             quant8<false>(u, divisor_of(s));
     }
+    copy_wait<0>();  // (values of a token without a slot were asked for all the same)
 }
 
 template <int kLanes, bool kWhole>
