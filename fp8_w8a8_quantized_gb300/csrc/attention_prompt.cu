@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kSideRegs));
       if (warp == kMainWarps) {
         // ------------------------------------------------ TMA loads
-        uint32_t loads = 0, issued = 0, q_loads = 0, q_issued[2] = {0, 0}, published = 0, asked = 0;
+        uint32_t loads = 0, issued = 0, q_loads = 0, q_issued[2] = {0, 0}, published = 0, asked = 0, answered = 0;
         bool ok = true;
         Item it;
         auto ask = [&]() {
@@ -376,11 +376,12 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
                 mbar_arrive_expect_tx(&bars->next_cta, 16);
                 cancel_next_cta(&bars->response, &bars->next_cta);
             }
+            ++asked;
             __syncwarp();
         };
         auto answer = [&](int64_t& n) {
-            if (!warp_ready(&bars->next_cta, asked & 1u, abort_flag, status)) return false;
-            ++asked;
+            if (!warp_ready(&bars->next_cta, answered & 1u, abort_flag, status)) return false;
+            ++answered;
             n = cancelled_cta(&bars->response);
             fence_proxy_async_smem();  // (read, before the next answer is written)
             __syncwarp();
@@ -453,6 +454,7 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
             }
             for (int x = 0; x < NQ; ++x)
                 if (q_issued[x]) wait_landed(&bars->q_full[x], (q_issued[x] - 1) & 1u, status);
+            if (asked != answered) wait_landed(&bars->next_cta, answered & 1u, status);
         }
         __syncwarp();
       } else if (warp == kMainWarps + 1 || (NQ == 2 && warp == kMainWarps + 3)) {
