@@ -162,10 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prefix(const DecodeArgs
         tmem_alloc(&bars->tmem_base, 512);
         tmem_relinquish();
     }
-    pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();  // (behind the allocation: see ptx.cuh)
     const uint32_t tmem = bars->tmem_base;
     volatile int* abort_flag = &bars->abort;
     pdl_wait_primary();

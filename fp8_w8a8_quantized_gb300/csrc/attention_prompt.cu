@@ -249,10 +249,10 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
         tmem_alloc(&bars->tmem_base, kTmem);
         tmem_relinquish();
     }
-    pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();  // (behind the allocation: see ptx.cuh)
     const uint32_t tmem = bars->tmem_base;
     volatile int* abort_flag = &bars->abort;
     pdl_wait_primary();

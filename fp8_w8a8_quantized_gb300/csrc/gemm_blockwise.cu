@@ -128,10 +128,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&bars->tmem_base, TMEM_COLS);
         tmem_relinquish();
     }
-    pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();  // (behind the allocation: see ptx.cuh)
     const uint32_t tmem_base = bars->tmem_base;
     volatile int* abort_flag = &bars->abort;
 
@@ -380,10 +380,10 @@ __global__ void __launch_bounds__(kThreads)
         tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
         tmem_relinquish();
     }
-    pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();  // (behind the allocation: see ptx.cuh)
     // Push: peers may send partials once every CTA's barriers are initialised.
     if constexpr (C::kPush) cluster_arrive();
     const uint32_t tmem_base = bars->tmem_base;

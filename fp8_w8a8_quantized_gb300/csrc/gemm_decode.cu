@@ -169,12 +169,12 @@ __global__ void __launch_bounds__(kThreads)
         tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
         tmem_relinquish();
     }
-    // the next kernel on the stream may start its prologue now (it waits for
-    // this grid's completion before touching memory)
-    pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // the next kernel on the stream may start its prologue now (it waits for
+    // this grid's completion before touching memory; behind the allocation: see ptx.cuh)
+    pdl_launch_dependents();
     // Push: peers may send partials once every CTA's barriers are
     // initialised (first half of a split cluster barrier; the wait comes
     // before sending).

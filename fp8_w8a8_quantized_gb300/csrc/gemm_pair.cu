@@ -122,9 +122,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc_pair(&bars->tmem_base, TMEM_COLS);
         tmem_relinquish_pair();
     }
-    pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
+    pdl_launch_dependents();  // (behind the allocation: see ptx.cuh)
     // both CTAs' barriers are initialised (and the TMEM allocated) before
     // either CTA signals the other's barriers
     cluster_sync_all();

@@ -736,6 +736,10 @@ __device__ __forceinline__ void pdl_wait_primary() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The next kernel on the stream may start once every CTA has called this or is
+// done.  A kernel with tensor memory calls it behind its allocation, which waits
+// without a limit: a successor could otherwise take the columns that this CTA
+// still waits for, and then wait for this kernel's end.
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
