@@ -177,7 +177,7 @@ PyObject* kv_slots(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     Tensor slot = tensor_of(a[6], "slot_mapping"), pos = tensor_of(a[7], "positions"),
            cu = tensor_of(a[8], "cu_seqlens"), lens = tensor_of(a[9], "seq_lens"),
            used = tensor_of(a[10], "pages_used");
-    TORCH_CHECK_VALUE(room >= 0, "max_tokens must not be negative");
+    TORCH_CHECK_VALUE(room >= 0 && room < int64_t(1) << 31, "max_tokens must be 0 .. 2^31 - 1");
     expect(ctx, "ctx_lens", at::kInt, {-1});
     const int64_t B = ctx.size(0);
     expect(fresh, "new_lens", at::kInt, {B});
