@@ -119,6 +119,15 @@ float float_of(PyObject* o, const char* name) {
     return static_cast<float>(v);
 }
 
+bool bool_of(PyObject* o, const char* name) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        TORCH_CHECK_VALUE(false, name, " must be true or false");
+    }
+    return v != 0;
+}
+
 void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 // Where a call runs: on the device of its first tensor, on the given stream
@@ -240,7 +249,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                  vc = tensor_of(a[15], "v_cache");
     Tensor qo = tensor_of(a[8], "q_out"), ko = tensor_of(a[9], "k_out");
     const float eps = float_of(a[6], "eps");
-    const bool pairs = PyObject_IsTrue(a[7]) == 1, cache_only = PyObject_IsTrue(a[16]) == 1;
+    const bool pairs = bool_of(a[7], "interleaved"), cache_only = bool_of(a[16], "cache_only");
     const int64_t ldq = tokens(q, "q");
     const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2);
     const int64_t ldk = tokens(k, "k", {T, -1, D}), Hkv = k.size(1);
