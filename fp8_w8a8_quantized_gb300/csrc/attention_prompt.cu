@@ -474,10 +474,6 @@ __global__ void __launch_bounds__(Config<DP, NQ>::kThreads, Config<DP, NQ>::kCta
             return warp_ready(bar, parity & 1u, abort_flag, status);
         };
         auto landed = [&](uint32_t k) { return ready(&bars->full[k % kStages], k / kStages); };
-        auto k_desc = [&](uint32_t stage) { return desc_kmajor(base_kv + uniform(stage) * kTile); };
-        auto v_desc = [&](uint32_t stage) {
-            return desc_nmajor(base_kv + uniform(stage) * kTile, kColBytes);
-        };
         Item it;
         while (ok && take_item(it, ok)) {
             const int tiles = uniform(max(it.tiles[0], it.tiles[1])), masked = uniform(it.masked);
