@@ -61,7 +61,7 @@
 namespace fp8k {
 namespace {
 
-constexpr int kClean = 4;  // (the ring holds two tiles of values at most)
+constexpr int kClean = 4;  // tiles of values with flags of their own
 constexpr int kFlags = 4;  // items whose "values were set to 0" flag is kept
 
 // A work item: the tokens of one sequence's block and one key head.
@@ -78,6 +78,8 @@ struct Item {
 template <int DP, int NQ>
 struct Config {
     static constexpr int kStages = NQ == 2 ? 5 : 2;
+    // (of stages in a row at most every other one and one more hold values)
+    static_assert(kClean >= (kStages + 1) / 2, "a tile's flags must not meet the next one's");
     static constexpr int kMainWarps = 8 * NQ;
     static constexpr int kThreads = 32 * (kMainWarps + 4);
     static constexpr int kCtas = 3 - NQ;  // an SM
