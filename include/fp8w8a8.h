@@ -412,9 +412,10 @@ FP8_API fp8_status_t fp8_kv_slots(const int32_t* ctx_lens, const int32_t* new_le
  *   for the rot_dim / 2 pairs i: (a, b) = (i, i + rot_dim / 2), or
  *   (2 i, 2 i + 1) with interleaved != 0, and w = 2 pi frac(position *
  *   turns[i] / 2^64); elements rot_dim .. D - 1 stay; then one rounding to
- *   bf16.  Frequencies are given as 64-bit fractions of a turn so that the
- *   angle of a far position is exact: turns[i] = round(2^64 f_i / (2 pi)) for
- *   a frequency of f_i radians per position.
+ *   bf16.  Frequencies are given as 64-bit fractions of a turn so that far
+ *   positions lose no digits: turns[i] = round(2^64 f_i / (2 pi)) for a
+ *   frequency of f_i radians per position.  The product with the position is
+ *   exact; sine and cosine take it to 2^-26 of a turn (10^-7 radians).
  *   With a cache, keys and values are then quantized exactly as
  *   fp8_kv_cache_quant_kv(k_out, v, ...) would.
  *
