@@ -10,8 +10,8 @@ residual stream, with this library's operators:
     fp8_linear             O projection
 
 One layer at the 8B shapes (32 query heads on 8 key heads of 128) by default:
-a system prompt is computed once, requests that share its pages bring their
-own prompts, and then every request gets a few new tokens.
+a system prompt is computed once, requests share its pages, and every request
+gets a few new tokens.
 
     python examples/attention_block.py [--requests N] [--system T] [--steps S]
 """
@@ -61,7 +61,7 @@ class AttentionBlock:
         """Pages and slots for new_lens[b] new tokens of each request."""
         slots, positions, cu, lens, used = fp8.fp8_kv_slots(
             self.ctx[rows], new_lens, self.free, self.page_size, self.table[rows], tokens)
-        taken = int(used)  # (a program with a pool of its own keeps this on the device)
+        taken = int(used)  # (pages come from the front of `free`: the host waits for their number)
         if taken > self.free.numel():
             raise RuntimeError(f"{taken} pages wanted, {self.free.numel()} free")
         self.free = self.free[taken:]

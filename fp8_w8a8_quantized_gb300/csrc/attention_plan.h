@@ -63,9 +63,9 @@ inline PrefixPlan prefix_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int
     // what both were measured to need (page size 16, 300 tokens beside the
     // prefix): that one reads B times the prefix, out of L2 mostly, at 8.6
     // bytes/ps with 8 heads of 128, 5 with heads of 64; this one costs 18 us
-    // and 2.4 us a key tile of a CTA.  At 32/8 heads of 128, own reading
-    // against this: B = 16, 8192 tokens 45 / 35 us, 2048 tokens 22 / 29; B = 64,
-    // 2048 tokens 43 / 31, 512 tokens 21 / 29; B = 4, 32768 tokens 44 / 59.
+    // and 2.4 us a key tile of a CTA.  The call at 32/8 heads of 128, own reading
+    // against this: B = 16, 8192 tokens 42 / 30 us, 2048 tokens 19 / 25; B = 64,
+    // 2048 tokens 44 / 32, 512 tokens 23 / 31; B = 4, 32768 tokens 39 / 50.
     const double own_us = static_cast<double>(B) * prefix * 2 * Hkv * D / (D > 64 ? 8.6e6 : 5.0e6);
     if (own_us < 18.0 + 2.4 * p.tiles) {
         p.tiles = 0;

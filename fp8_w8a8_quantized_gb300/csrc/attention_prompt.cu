@@ -36,12 +36,15 @@
 // (With one tile a CTA: softmax in warps 0-7, the others are warps 8-11.)
 //
 // Bound by the tensor cores where prompts are long.  Measured, heads of 128: one
-// prompt of 8192 tokens, 32 / 8 heads, 340 us at 1.9 GHz, 1.62 PFLOP/s, 85% of
-// what a large library product reaches (tensor pipe 70% busy: the rest is the
-// way S -> P -> O, 2600 to 3000 clocks for 2048 clocks of MMAs); nine prompts of
-// 129 to 2801, 64 / 8 heads, 202 us, 1.18 PFLOP/s (an item's start and end take
-// some 5000 clocks, and the masked halves of the last tiles are work too); 24
-// prompts of 1 to 257 tokens 17 us (items of two tiles: their latency).
+// prompt of 8192 tokens, 32 / 8 heads, 335 to 345 us on a cool GPU, 365 to 380 back
+// to back for seconds, 1.64 to 1.45 PFLOP/s, 86 to 76% of what a large library
+// product reaches in a burst (tensor pipe 70% busy: the rest is the way S -> P ->
+// O, 2600 to 3000 clocks for 2048 clocks of MMAs); nine prompts of 129 to 2801, 64 /
+// 8 heads, 202 us, 1.18 PFLOP/s (an item's start and end take some 5000 clocks, in
+// which the same warps write its output and take the next one's first softmax, and
+// the masked halves of the last tiles are work too); 24 prompts of 1 to 257 tokens
+// 17 us (items of two tiles: their latency).  Heads of 80, 96 and 112 run as heads
+// of 128, on zeros: 4096 tokens 95, 96, 97 us, of 128 98, of 64 87.
 //
 // A masked weight is 0, but 0 * inf is NaN: in tiles where some row masks some
 // key, warp 18 sets non-finite values to 0 in shared memory before the MMA
@@ -636,10 +639,10 @@ cudaError_t prepare() {
 
 cudaError_t launch_attention_prompt(const PromptArgs& a, cudaStream_t st) {
     // Too few items for the SMs: smaller ones.  (32 heads on 8 of 128: one prompt
-    // of 128 tokens 7.3 us with one tile a CTA, 9.3 with two; of 1024 tokens 23.6
-    // and 20.3, of 4096 tokens 143 and 119.)  Prompts that as a rule leave the
-    // second tile empty: the same (128 of 32 tokens 29.0 and 34.3, 256 of 16 42 and
-    // 54, 64 of 64 27.2 and 27.2, 16 of 257 35.0 and 33.7).
+    // of 128 tokens 6.9 us with one tile a CTA, 9.0 with two; of 1024 tokens 23.2
+    // and 18.7, of 4096 tokens 126 and 98.)  Prompts that as a rule leave the
+    // second tile empty: the same (128 of 32 tokens 28.8 and 34.6, 256 of 16 42 and
+    // 54, 64 of 64 27.1 and 27.4, 16 of 257 34.7 and 33.6).
     const int64_t per = 2 * (kRows / (a.Hq / a.Hkv));  // tokens of two tiles
     const bool one = (a.T / per + a.B) * a.Hkv <= a.num_sms / 2 || a.T <= a.B * per;
     if (a.D <= 64) return one ? launch_tiles<64, 1>(a, st) : launch_tiles<64, 2>(a, st);
