@@ -216,7 +216,7 @@ def _plain_grouped(s):
     if s["row_token"] is not None:
         x = x[s["row_token"].long()]
     amax = x.abs().amax(-1, keepdim=True)
-    s_x = torch.where(amax > 0, amax / E4M3_MAX, 1.0)
+    s_x = torch.where(amax > 0, amax / torch.full_like(amax, E4M3_MAX), 1.0)
     codes = (x / s_x).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn).float()
     # the rows of each expert side by side, as many places as the busiest one has rows
     offsets = s["offsets"].long()
@@ -248,7 +248,7 @@ def _plain_join(s):
     codes = scale = None
     if s["codes"]:
         amax = z.abs().amax(-1)
-        scale = torch.where(amax > 0, amax / E4M3_MAX, 1.0)
+        scale = torch.where(amax > 0, amax / torch.full_like(amax, E4M3_MAX), 1.0)
         codes = (z / scale[:, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
     return dict(h=h.to(torch.bfloat16), z=z.to(torch.bfloat16) if s["rows"] else None, codes=codes, scale=scale)
 
@@ -301,7 +301,8 @@ def _exact_grouped(case, s):
         return None
     x = s["x"] if s["row_token"] is None else s["x"][s["row_token"].long()]
     top = x.float().abs().max(1, keepdim=True).values
-    s_x = torch.where(top == 0, torch.ones_like(top), top / E4M3_MAX)  # the scale is an fp32 number by definition
+    # the scale is an fp32 number by definition: the quotient rounded once
+    s_x = torch.where(top == 0, torch.ones_like(top), (top.double() / E4M3_MAX).float())
     codes = _codes_of((x.float() / s_x).double().clamp(-E4M3_MAX, E4M3_MAX))
     out = torch.empty(x.shape[0], N // 2 if case["gated"] else N, dtype=torch.float64, device=DEVICE)
     bounds = s["offsets"].tolist()
