@@ -38,3 +38,11 @@ from ._attention import (  # noqa: F401,E402
     fp8_qk_norm_rope,
     fp8_rope_turns,
 )
+from ._experts import (  # noqa: F401,E402
+    fp8_grouped_gemm,
+    fp8_grouped_gemm_workspace_size,
+    fp8_grouped_linear,
+    fp8_grouped_linear_workspace_size,
+    fp8_moe_route,
+    fp8_residual_norm_quant,
+)

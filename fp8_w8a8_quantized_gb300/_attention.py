@@ -14,25 +14,33 @@ import torch
 
 from ._binding import _HERE, Fp8Error, _lock, lib
 
-MODULE_PATH = os.path.join(_HERE, "_build", "fp8_attention_binding"
-                           + importlib.machinery.EXTENSION_SUFFIXES[0])
 _module = None
+
+
+def _load(name: str):
+    """An extension module of the binding, from beside the library that it links to."""
+    lib()
+    path = os.path.join(_HERE, "_build", name + importlib.machinery.EXTENSION_SUFFIXES[0])
+    if not os.path.exists(path):
+        raise RuntimeError(f"binding module not built ({path}); run "
+                           "`python -m fp8_w8a8_quantized_gb300.build`")
+    with _lock:
+        if name not in _loaded:
+            spec = importlib.util.spec_from_file_location(name, path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _loaded[name] = module
+        return _loaded[name]
+
+
+_loaded: dict = {}
 
 
 def _native():
     """The loaded extension module."""
     global _module
     if _module is None:
-        lib()  # the library that the module links to
-        if not os.path.exists(MODULE_PATH):
-            raise RuntimeError(f"binding module not built ({MODULE_PATH}); run "
-                               "`python -m fp8_w8a8_quantized_gb300.build`")
-        with _lock:
-            if _module is None:
-                spec = importlib.util.spec_from_file_location("fp8_attention_binding", MODULE_PATH)
-                module = importlib.util.module_from_spec(spec)
-                spec.loader.exec_module(module)
-                _module = module
+        _module = _load("fp8_attention_binding")
     return _module
 
 

@@ -123,6 +123,26 @@ def lib() -> ctypes.CDLL:
                                            ctypes.c_float, _vp, _i64, _vp, _sz, _vp]
         L.fp8_attention_decode_workspace_size.restype = _sz
         L.fp8_attention_decode_workspace_size.argtypes = [_i64] * 7
+        _f, _i = ctypes.c_float, ctypes.c_int
+        L.fp8_moe_route.restype = _st
+        L.fp8_moe_route.argtypes = [_vp, _i, _i64, _i64, _i64, _i64, _i, _f, _vp, _vp, _vp, _vp,
+                                    _vp, _vp, _sz, _vp]
+        L.fp8_moe_route_workspace_size.restype = _sz
+        L.fp8_moe_route_workspace_size.argtypes = [_i64] * 3
+        L.fp8_grouped_gemm.restype = _st
+        L.fp8_grouped_gemm.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i, _vp,
+                                       _vp, _sz, _vp]
+        L.fp8_grouped_gemm_workspace_size.restype = _sz
+        L.fp8_grouped_gemm_workspace_size.argtypes = [_i64] * 4
+        L.fp8_grouped_linear.restype = _st
+        L.fp8_grouped_linear.argtypes = [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                         _i64, _i, _vp, _vp, _sz, _vp]
+        L.fp8_grouped_linear_workspace_size.restype = _sz
+        L.fp8_grouped_linear_workspace_size.argtypes = [_i64] * 4
+        L.fp8_residual_norm_quant.restype = _st
+        L.fp8_residual_norm_quant.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
+                                              _vp, _i64, _vp, _f, _f, _f, _i64, _i64, _vp, _i64,
+                                              _vp, _vp, _i64, _vp, _vp]
         L.fp8_selftest_wait_timeout.restype = _st
         L.fp8_selftest_wait_timeout.argtypes = [_i64, _vp, _vp]
         _lib = L

@@ -1,5 +1,6 @@
 """Build the CUDA library in-tree: fp8_w8a8_quantized_gb300/_build/libfp8w8a8.so,
-and the extension module of the attention block's binding beside it.
+and the extension modules of the attention block's and the expert block's
+binding beside it.
 
 Each .cu file is compiled for sm_103a only (``-gencode
 arch=compute_103a,code=sm_103a``), in parallel, then linked with the static
@@ -28,12 +29,12 @@ LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "quant.cu", "quant_variants.cu", "norm_quant.cu", "gemm_pair.cu", "gemm_decode.cu", "gemm_blockwise.cu", "noalloc.cu",
            "selftest.cu", "attention_api.cu", "kv_slots.cu", "norm_rope.cu", "attention_prompt.cu", "attention_decode.cu",
-           "attention_prefix.cu"]
+           "attention_prefix.cu", "experts_api.cu", "moe_route.cu", "gemm_grouped.cu", "residual_norm.cu"]
 HEADERS = ["ptx.cuh", "launch.h", "quant_math.cuh", "decode_common.cuh", "attention_plan.h", "attention_tile.cuh"]
 
-# The binding's extension module (host code only; links the library and torch).
-MODULE_SOURCE = "attention_binding.cpp"
-MODULE_PATH = os.path.join(OUT_DIR, "fp8_attention_binding" + importlib.machinery.EXTENSION_SUFFIXES[0])
+# The binding's extension modules (host code only; they link the library and torch).
+MODULES = ["attention_binding", "experts_binding"]
+MODULE_HEADERS = ["binding_args.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -73,11 +74,13 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _compile_module() -> str:
+def _compile_module(name: str) -> str:
     import torch
-    src = os.path.join(CSRC, MODULE_SOURCE)
-    obj = os.path.join(OUT_DIR, "attention_binding.o")
-    if not _stale(obj, [src, os.path.join(INCLUDE, "fp8w8a8.h"), __file__, torch.__file__]):
+    src = os.path.join(CSRC, name + ".cpp")
+    obj = os.path.join(OUT_DIR, name + ".o")
+    deps = [src] + [os.path.join(CSRC, h) for h in MODULE_HEADERS] + [
+        os.path.join(INCLUDE, "fp8w8a8.h"), __file__, torch.__file__]
+    if not _stale(obj, deps):
         return obj
     troot = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
@@ -88,30 +91,31 @@ def _compile_module() -> str:
            "-I", sysconfig.get_paths()["include"], "-I", cuda, "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {MODULE_SOURCE}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {name}.cpp:\n{r.stdout}\n{r.stderr}")
     return obj
 
 
-def _link_module(obj: str) -> None:
+def _link_module(name: str, obj: str) -> None:
     import torch
-    if not _stale(MODULE_PATH, [obj, LIB_PATH]):
+    path = os.path.join(OUT_DIR, "fp8_" + name + importlib.machinery.EXTENSION_SUFFIXES[0])
+    if not _stale(path, [obj, LIB_PATH]):
         return
-    tmp = MODULE_PATH + f".{os.getpid()}.tmp"
+    tmp = path + f".{os.getpid()}.tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN",
            "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding module failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MODULE_PATH)
+    os.replace(tmp, path)
 
 
 def build(verbose: bool = False) -> str:
-    """Compile (incrementally) and link the library and the binding's module;
+    """Compile (incrementally) and link the library and the binding's modules;
     returns the library's path."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        module = ex.submit(_compile_module)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + len(MODULES)) as ex:
+        modules = [ex.submit(_compile_module, m) for m in MODULES]
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     if _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".{os.getpid()}.tmp"
@@ -120,7 +124,8 @@ def build(verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB_PATH)
-    _link_module(module.result())
+    for name, obj in zip(MODULES, modules):
+        _link_module(name, obj.result())
     return LIB_PATH
 
 

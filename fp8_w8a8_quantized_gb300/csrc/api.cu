@@ -58,6 +58,7 @@ fp8_status_t current_device(DeviceState** out) {
                    fp8k::prepare_gemm_decode() != cudaSuccess ||
                    fp8k::prepare_gemm_blockwise() != cudaSuccess ||
                    fp8k::prepare_gemm_pair() != cudaSuccess ||
+                   fp8k::prepare_gemm_grouped() != cudaSuccess ||
                    fp8k::prepare_attention_prompt() != cudaSuccess ||
                    fp8k::prepare_attention_decode() != cudaSuccess ||
                    fp8k::prepare_attention_prefix() != cudaSuccess) {
@@ -184,12 +185,13 @@ fp8_status_t linear_checks(const void* x, const uint8_t* wq, const float* s_w, c
     return current_device(&d);
 }
 
-fp8_status_t device_info(int* num_sms, unsigned** status) {
+fp8_status_t device_info(int* num_sms, unsigned** status, int* pair_clusters) {
     DeviceState* d = nullptr;
     const fp8_status_t st = current_device(&d);
     if (st == FP8_OK) {
         *num_sms = d->num_sms;
         *status = d->status;
+        if (pair_clusters) *pair_clusters = d->pair_clusters;
     }
     return st;
 }

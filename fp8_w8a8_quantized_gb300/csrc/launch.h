@@ -184,9 +184,75 @@ size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
 // the plan: attention_plan.h).
 cudaError_t launch_attention_prefix(const DecodeArgs& a, const PrefixPlan& plan, cudaStream_t st);
 
-// The current device's SM count and status word, after the same checks as
+// Each token's best experts, their weights and the rows sorted by expert
+// (moe_route.cu).
+struct RouteArgs {
+    const void* logits;
+    bool fp32;
+    int64_t ld, T;
+    int E, k;
+    bool renorm;
+    float scale;
+    int32_t* ids;
+    float* weights;
+    int32_t *offsets, *row_token, *token_row;
+    int32_t* workspace;
+    int num_sms;
+};
+cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t st);
+size_t moe_route_workspace(int64_t T, int64_t E, int64_t k);
+
+// Rows of x gathered by row_token (null: row r is row r) and quantized
+// (quant.cu); a row without a token gets zeros with scale 1.  `zero` (optional)
+// is set to zeros, zero_words 32-bit words.
+cudaError_t launch_quant_gather(const void* x, int64_t T, int64_t R, int64_t K, int64_t ldx,
+                                const int32_t* row_token, uint8_t* q, float* s, uint32_t* zero,
+                                int64_t zero_words, cudaStream_t st);
+
+// Products of each expert's rows with its weights (gemm_grouped.cu).
+struct GroupedArgs {
+    const uint8_t* xq;
+    const float* s_tok;
+    const uint8_t* wq;
+    const float* s_w;
+    const int32_t* offsets;
+    int E, R, N, K;
+    bool swiglu;
+    void* y;
+    void* workspace;
+    bool zeroed;        // the first gemm_grouped_zero_words() words of it are zero
+    unsigned* status;
+    int num_sms;
+    int pair_clusters;  // co-resident clusters of the paired kernel (0: unknown)
+};
+cudaError_t launch_gemm_grouped(const GroupedArgs& a, cudaStream_t st);
+size_t gemm_grouped_workspace(int64_t E, int64_t R, int64_t N, int64_t K);
+int64_t gemm_grouped_zero_words();
+
+// The end of a block and the start of the next (residual_norm.cu).
+struct ResidualNormArgs {
+    const uint16_t *h, *y;
+    int64_t ldh, ldy, R;
+    const int32_t* token_row;
+    const float* weights;
+    int k;
+    const uint16_t *gamma_post, *gate, *gamma;
+    int64_t ldg;
+    float eps, residual_scale, branch_scale;
+    int64_t T, K;
+    uint16_t* h_out;
+    int64_t ldho;
+    uint16_t* z;
+    uint8_t* q;
+    int64_t ldq;
+    float* s;
+};
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, cudaStream_t st);
+
+// The current device's SM count, status word and (optional) co-resident clusters
+// of the paired-SM kernels, after the same checks as
 // every other entry point (api.cu).
-fp8_status_t device_info(int* num_sms, unsigned** status);
+fp8_status_t device_info(int* num_sms, unsigned** status, int* pair_clusters = nullptr);
 
 // Self-test of the bounded waits (selftest.cu): one CTA whose waits run out
 // after limit_ns; report[0..3] as fp8_selftest_wait_timeout documents.
@@ -203,6 +269,7 @@ fp8_status_t linear_checks(const void* x, const uint8_t* wq, const float* s_w, c
 cudaError_t prepare_gemm_decode();
 cudaError_t prepare_gemm_blockwise();
 cudaError_t prepare_gemm_pair();
+cudaError_t prepare_gemm_grouped();
 cudaError_t prepare_attention_prompt();
 cudaError_t prepare_attention_decode();
 cudaError_t prepare_attention_prefix();

@@ -53,6 +53,17 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
     return v;
 }
 
+// The same off the read-only path: for rows that the kernel before may have
+// written while this one was already resident.
+__device__ __forceinline__ uint4 ld_fresh(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // Max over the G threads of a row group.  `red` holds one float per warp.
 template <int G, int B>
 __device__ __forceinline__ float group_max(float m, float* red) {
@@ -76,11 +87,22 @@ __device__ __forceinline__ float group_max(float m, float* red) {
 // kGiven: the scale is *s_given for every row (a static, calibrated scale:
 // no maximum is taken, and quotients beyond 448 saturate); s (optional, may
 // be null) receives it per row.
-template <int G, int VPT, bool kGiven = false>
+//
+// kGather: row r is row source[r] of x (of T; zeros with scale 1 for any other
+// entry), so that the rows of an expert lie side by side behind the quantizer's
+// one launch; the launch also sets `zero` to zeros.
+struct Gather {
+    const int32_t* source;
+    int64_t T;
+    uint32_t* zero;
+    int64_t zero_words;
+};
+
+template <int G, int VPT, bool kGiven = false, bool kGather = false>
 __global__ void __launch_bounds__(G > kBlock ? G : kBlock)
     quant_rows_regs(const uint16_t* __restrict__ x, int64_t R, int64_t K, int64_t ldx,
                     uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s,
-                    const float* __restrict__ s_given = nullptr) {
+                    const float* __restrict__ s_given = nullptr, Gather g = {}) {
     constexpr int B = G > kBlock ? G : kBlock;
     constexpr int ROWS = B / G;
     __shared__ float red[B / 32];
@@ -96,15 +118,28 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock)
     const bool live = row < R;
     const int64_t C = K >> 4;  // 16-element chunks per row
 
-    const uint4* xr = reinterpret_cast<const uint4*>(x + (live ? row : 0) * ldx);
+    int64_t from = live ? row : 0;
+    bool there = live;
+    if constexpr (kGather) {
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * B + threadIdx.x; i < g.zero_words;
+             i += static_cast<int64_t>(gridDim.x) * B)
+            g.zero[i] = 0u;
+        if (g.source) {
+            from = live ? g.source[row] : -1;
+            there = from >= 0 && from < g.T;
+            if (!there) from = 0;
+        }
+    }
+    const uint4* xr = reinterpret_cast<const uint4*>(x + from * ldx);
     uint4 v[VPT][2];
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int64_t c = t + static_cast<int64_t>(i) * G;
-        if (live && c < C) {
-            v[i][0] = ld_stream(xr + 2 * c);
-            v[i][1] = ld_stream(xr + 2 * c + 1);
+        if constexpr (kGather) v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (there && c < C) {
+            v[i][0] = kGather ? ld_fresh(xr + 2 * c) : ld_stream(xr + 2 * c);
+            v[i][1] = kGather ? ld_fresh(xr + 2 * c + 1) : ld_stream(xr + 2 * c + 1);
             if constexpr (!kGiven) m = amax8(v[i][1], amax8(v[i][0], m));
         }
     }
@@ -132,18 +167,31 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock)
 
 // Rows longer than the register path holds: stream the row twice (the
 // second pass mostly hits L2).
+template <bool kGather>
 __global__ void __launch_bounds__(1024)
     quant_rows_stream(const uint16_t* __restrict__ x, int64_t R, int64_t K, int64_t ldx,
-                      uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s) {
+                      uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s, Gather g) {
     __shared__ float red[32];
     pdl_launch_dependents();
     pdl_wait_primary();
     const int64_t row = blockIdx.x;
     const int64_t C = K >> 4;
-    const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
+    int64_t from = row;
+    if constexpr (kGather) {
+        for (int64_t i = row * 1024 + threadIdx.x; i < g.zero_words; i += R * 1024) g.zero[i] = 0u;
+        if (g.source) from = g.source[row];
+        if (from < 0 || from >= g.T) {
+            for (int64_t c = threadIdx.x; c < C; c += 1024)
+                reinterpret_cast<uint4*>(q + row * ldq)[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (threadIdx.x == 0) s[row] = 1.0f;
+            return;
+        }
+    }
+    const uint4* xr = reinterpret_cast<const uint4*>(x + from * ldx);
     float m = 0.0f;
     for (int64_t c = threadIdx.x; c < C; c += 1024) {
-        const uint4 a = __ldg(xr + 2 * c), b = __ldg(xr + 2 * c + 1);
+        const uint4 a = kGather ? ld_fresh(xr + 2 * c) : __ldg(xr + 2 * c);
+        const uint4 b = kGather ? ld_fresh(xr + 2 * c + 1) : __ldg(xr + 2 * c + 1);
         m = amax8(b, amax8(a, m));
     }
     m = group_max<1024, 1024>(m, red);
@@ -151,8 +199,9 @@ __global__ void __launch_bounds__(1024)
     const Divisor dv = divisor_of(sc);
     uint4* qr = reinterpret_cast<uint4*>(q + row * ldq);
     for (int64_t c = threadIdx.x; c < C; c += 1024) {
-        const uint2 a = quant8<true>(ld_stream(xr + 2 * c), dv);
-        const uint2 b = quant8<true>(ld_stream(xr + 2 * c + 1), dv);
+        const uint2 a = quant8<true>(kGather ? ld_fresh(xr + 2 * c) : ld_stream(xr + 2 * c), dv);
+        const uint2 b =
+            quant8<true>(kGather ? ld_fresh(xr + 2 * c + 1) : ld_stream(xr + 2 * c + 1), dv);
         qr[c] = make_uint4(a.x, a.y, b.x, b.y);
     }
     if (threadIdx.x == 0) s[row] = sc;
@@ -187,43 +236,55 @@ cudaError_t launch_pdl(void (*kernel)(Params...), int64_t grid, int block, cudaS
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int G, int VPT, bool kGiven = false>
+template <int G, int VPT, bool kGiven = false, bool kGather = false>
 cudaError_t launch_regs(const uint16_t* x, int64_t R, int64_t K, int64_t ldx, uint8_t* q,
-                        int64_t ldq, float* s, cudaStream_t st, const float* s_given = nullptr) {
+                        int64_t ldq, float* s, cudaStream_t st, const float* s_given = nullptr,
+                        const Gather& g = {}) {
     constexpr int B = G > kBlock ? G : kBlock;
     constexpr int ROWS = B / G;
     const int64_t grid = (R + ROWS - 1) / ROWS;
-    return launch_pdl(quant_rows_regs<G, VPT, kGiven>, grid, B, st, x, R, K, ldx, q, ldq, s,
-                      s_given);
+    return launch_pdl(quant_rows_regs<G, VPT, kGiven, kGather>, grid, B, st, x, R, K, ldx, q, ldq,
+                      s, s_given, g);
 }
 
 // The launch for rows of K = 16 C values: small problems (decode batches)
 // one chunk per thread, large ones kVPT (four for rows longer than 32768).
 // Returns cudaErrorNotSupported for rows longer than the register path holds.
-template <bool kGiven>
+template <bool kGiven, bool kGather = false>
 cudaError_t dispatch_regs(const uint16_t* xb, int64_t R, int64_t K, int64_t ldx, uint8_t* q,
-                          int64_t ldq, float* s, const float* s_given, cudaStream_t st) {
+                          int64_t ldq, float* s, const float* s_given, cudaStream_t st,
+                          const Gather& g = {}) {
     const int64_t C = K / 16;
     if (R * C <= kLatencyChunks) {
-        if (C <= 32) return launch_regs<32, 1, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
-        if (C <= 64) return launch_regs<64, 1, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
-        if (C <= 128) return launch_regs<128, 1, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
-        if (C <= 256) return launch_regs<256, 1, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
-        if (C <= 512) return launch_regs<512, 1, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
-        if (C <= 1024) return launch_regs<1024, 1, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
-        if (C <= 2048) return launch_regs<1024, 2, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
+        if (C <= 32)
+            return launch_regs<32, 1, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
+        if (C <= 64)
+            return launch_regs<64, 1, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
+        if (C <= 128)
+            return launch_regs<128, 1, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
+        if (C <= 256)
+            return launch_regs<256, 1, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
+        if (C <= 512)
+            return launch_regs<512, 1, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
+        if (C <= 1024)
+            return launch_regs<1024, 1, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
+        if (C <= 2048)
+            return launch_regs<1024, 2, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
     }
-    if (C <= 32 * kVPT) return launch_regs<32, kVPT, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
-    if (C <= 64 * kVPT) return launch_regs<64, kVPT, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
+    if (C <= 32 * kVPT)
+        return launch_regs<32, kVPT, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
+    if (C <= 64 * kVPT)
+        return launch_regs<64, kVPT, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
     if (C <= 128 * kVPT)
-        return launch_regs<128, kVPT, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
+        return launch_regs<128, kVPT, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
     if (C <= 256 * kVPT)
-        return launch_regs<256, kVPT, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
+        return launch_regs<256, kVPT, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
     if (C <= 512 * kVPT)
-        return launch_regs<512, kVPT, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
+        return launch_regs<512, kVPT, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
     if (C <= 1024 * kVPT)
-        return launch_regs<1024, kVPT, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
-    if (C <= 1024 * 4) return launch_regs<1024, 4, kGiven>(xb, R, K, ldx, q, ldq, s, st, s_given);
+        return launch_regs<1024, kVPT, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
+    if (C <= 1024 * 4)
+        return launch_regs<1024, 4, kGiven, kGather>(xb, R, K, ldx, q, ldq, s, st, s_given, g);
     return cudaErrorNotSupported;
 }
 
@@ -248,7 +309,18 @@ cudaError_t launch_quant_rows(const void* x, int64_t R, int64_t K, int64_t ldx, 
     if (K == 0) return launch_pdl(fill_ones, (R + 255) / 256, 256, st, s, R);
     const cudaError_t e = dispatch_regs<false>(xb, R, K, ldx, q, ldq, s, nullptr, st);
     if (e != cudaErrorNotSupported) return e;
-    return launch_pdl(quant_rows_stream, R, 1024, st, xb, R, K, ldx, q, ldq, s);
+    return launch_pdl(quant_rows_stream<false>, R, 1024, st, xb, R, K, ldx, q, ldq, s, Gather{});
+}
+
+// Preconditions as above, and K > 0.
+cudaError_t launch_quant_gather(const void* x, int64_t T, int64_t R, int64_t K, int64_t ldx,
+                                const int32_t* row_token, uint8_t* q, float* s, uint32_t* zero,
+                                int64_t zero_words, cudaStream_t st) {
+    const uint16_t* xb = static_cast<const uint16_t*>(x);
+    const Gather g{row_token, T, zero, zero_words};
+    const cudaError_t e = dispatch_regs<false, true>(xb, R, K, ldx, q, K, s, nullptr, st, g);
+    if (e != cudaErrorNotSupported) return e;
+    return launch_pdl(quant_rows_stream<true>, R, 1024, st, xb, R, K, ldx, q, K, s, g);
 }
 
 }  // namespace fp8k

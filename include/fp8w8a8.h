@@ -517,6 +517,142 @@ FP8_API size_t fp8_attention_decode_workspace_size(int64_t B, int64_t Hq, int64_
                                                    int64_t table_width, int64_t page_size,
                                                    int64_t prefix_len);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The expert block: a feed-forward layer split into E experts of which each
+ * token takes the best top_k, between the attention block's residual stream
+ * and the next layer's FP8 input.  The pages have no counterpart; the products
+ * are the scaled GEMM of "FP8 Inference Explained, in depth", "Inside a
+ * quantized linear layer", for the rows of each expert with its weights.
+ * Which rows belong to which expert is known on the GPU alone: rows are sorted
+ * by expert, and expert e has rows offsets[e] .. offsets[e + 1] - 1.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Each token's best experts and the rows that they make.  For token t with
+ * logits l_0 .. l_{E-1}:
+ *   expert_ids[t, j] = the expert of the j-th largest logit (the lower number
+ *     first among equal ones), j < top_k;
+ *   weights[t, j] = scale exp(l_id - max l) / sum exp(l_i - max l), the sum over
+ *     all experts, or with renormalize != 0 over the token's top_k;
+ *   the pairs (t, j) sorted by expert, by token within one, are the rows:
+ *   row_token[r] = t of row r,  token_row[t, j] = r,
+ *   offsets[e] = rows of the experts below e.
+ * A logit of -infinity or NaN switches its expert off for the token.  Where
+ * fewer than top_k are left, the rest has expert -1, weight 0 and row -1 (a
+ * token of padding whose logits are all -infinity makes no rows); row_token is
+ * -1 from offsets[E] on.
+ *
+ *   logits     [device, in]   fp32 [T, E] (logits_fp32 != 0) or bf16, leading
+ *                             dimension ld (elements)
+ *   expert_ids [device, out]  int32 [T, top_k];  weights [device, out] fp32
+ *   offsets    [device, out]  int32 [E + 1]
+ *   row_token  [device, out]  int32 [T * top_k];  token_row [device, out]
+ *                             int32 [T, top_k]
+ *   workspace  [device]       fp8_moe_route_workspace_size() bytes, 16-byte
+ *                             aligned; need not start at zero; not in use by
+ *                             another call in flight
+ * Requirements: 1 <= top_k <= E <= 1024, top_k <= 32; T * top_k < 2^31; scale
+ * finite; pointers aligned to their elements.  With T == 0 only offsets is
+ * written.
+ */
+FP8_API fp8_status_t fp8_moe_route(const void* logits, int logits_fp32, int64_t ld, int64_t T,
+                                   int64_t E, int64_t top_k, int renormalize, float scale,
+                                   int32_t* expert_ids, float* weights, int32_t* offsets,
+                                   int32_t* row_token, int32_t* token_row, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/* Workspace bytes fp8_moe_route needs; 0 for invalid sizes. */
+FP8_API size_t fp8_moe_route_workspace_size(int64_t T, int64_t E, int64_t top_k);
+
+/*
+ * The products of each expert's rows with its weights, in one call:
+ *   a[r, n] = ((sum_k e4m3(xq[r, k]) e4m3(wq[e, n, k])) * s_tok[r]) * s_w[e, n],
+ *   e the expert of row r, products accumulated in fp32;
+ *   y[r, n] = bf16_rn(a[r, n]), n < N, or with swiglu != 0
+ *   y[r, n] = bf16_rn(a[r, n] / (1 + exp(-a[r, n])) * a[r, n + N / 2]), n < N / 2
+ *   (the first half of an expert's weight rows is the gate, the second the
+ *   values).  Rows before offsets[0] and from offsets[E] on stay as they are.
+ *
+ *   xq     [device, in]  E4M3 [R, K], contiguous;  s_tok [device, in] fp32 [R]
+ *   wq     [device, in]  E4M3 [E, N, K], contiguous;  s_w [device, in] fp32 [E, N]
+ *                        (fp8_quant_per_channel_weights of the [E * N, K] rows)
+ *   offsets [device, in] int32 [E + 1], non-decreasing, within 0 .. R
+ *   y      [device, out] bf16 [R, N], or [R, N / 2] with swiglu; contiguous
+ *   workspace [device]   fp8_grouped_gemm_workspace_size() bytes, 256-byte
+ *                        aligned; need not start at zero; not in use by
+ *                        another call in flight.  NULL if that is 0.
+ * Requirements: K % 16 == 0, K > 0; with swiglu N % 2 == 0; 1 <= E <= 1024;
+ * xq, wq and y 16-byte aligned; R, K, E * N < 2^31.  The order of each sum is
+ * fixed by the sizes and offsets: repeated calls give identical bits.
+ */
+FP8_API fp8_status_t fp8_grouped_gemm(const uint8_t* xq, const float* s_tok, const uint8_t* wq,
+                                      const float* s_w, const int32_t* offsets, int64_t E,
+                                      int64_t R, int64_t N, int64_t K, int swiglu, void* y_bf16,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes fp8_grouped_gemm needs; 0 for invalid sizes. */
+FP8_API size_t fp8_grouped_gemm_workspace_size(int64_t E, int64_t R, int64_t N, int64_t K);
+
+/*
+ * An expert layer: each row's token quantized by the rule of
+ * fp8_quant_per_token into the workspace, in the rows' order, then
+ * fp8_grouped_gemm.
+ *
+ *   x_bf16    [device, in]  bf16 [T, K], leading dimension ldx
+ *   row_token [device, in]  int32 [R]: row r is token row_token[r] (a row whose
+ *                           entry lies outside 0 .. T - 1 counts as zeros); or
+ *                           NULL: row r is row r of x, and T == R
+ *   workspace [device]      fp8_grouped_linear_workspace_size() bytes, 256-byte
+ *                           aligned; need not start at zero; not in use by
+ *                           another call in flight
+ * Requirements: as for fp8_grouped_gemm; x_bf16 16-byte aligned, ldx >= K and
+ * ldx % 8 == 0.
+ */
+FP8_API fp8_status_t fp8_grouped_linear(const void* x_bf16, int64_t T, int64_t ldx,
+                                        const int32_t* row_token, const uint8_t* wq,
+                                        const float* s_w, const int32_t* offsets, int64_t E,
+                                        int64_t R, int64_t N, int64_t K, int swiglu, void* y_bf16,
+                                        void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes fp8_grouped_linear needs; 0 for invalid sizes. */
+FP8_API size_t fp8_grouped_linear_workspace_size(int64_t E, int64_t R, int64_t N, int64_t K);
+
+/*
+ * The end of a block and the start of the next, in one pass over the tokens:
+ *   b = sum_j weights[t, j] y[token_row[t, j]]   (top_k > 0: an expert block's
+ *       rows; without weights each counts once; a row outside 0 .. R - 1 counts
+ *       as zeros), or b = y[t] (top_k == 0);
+ *   b = b / sqrt(mean b^2 + eps) * gamma_post    (with gamma_post)
+ *   b = b * gate                                 (with a gate)
+ *   h' = residual_scale h + branch_scale b;      h_out = bf16_rn(h')
+ *   z = h' / sqrt(mean h'^2 + eps) * gamma;      z_out = bf16_rn(z)
+ *   s = amax |z| / 448 (1 if z is zero),  xq = E4M3(z / s)
+ * All of it is in fp32, each result rounded once: the norm takes h' and the
+ * quantizer z before their rounding to bf16.
+ *
+ *   h      [device, in]   bf16 [T, K], ldh: the residual stream
+ *   y      [device, in]   bf16 [R, K], ldy (top_k == 0: R == T)
+ *   token_row [device, in] int32 [T, top_k];  weights [device, in] fp32
+ *                         [T, top_k] or NULL
+ *   gamma_post [device, in] bf16 [K] or NULL: no norm of the branch
+ *   gate   [device, in]   bf16 [T, K], ldg; ldg == 0: one row [K] for all
+ *                         tokens; NULL: no gate
+ *   gamma  [device, in]   bf16 [K]; may be NULL without z_out and xq
+ *   h_out  [device, out]  bf16 [T, K], ldho; may be h itself (ldho = ldh)
+ *   z_out  [device, out]  bf16 [T, K], contiguous, or NULL
+ *   xq     [device, out]  E4M3 [T, K], ldq, with s_tok fp32 [T]; or both NULL
+ * Requirements: K % 16 == 0, 0 < K <= 32768; top_k <= 32; leading dimensions >= K
+ * and % 8 == 0 (ldq % 16); bf16 tensors and xq 16-byte aligned, others 4; eps
+ * >= 0 finite; scales finite; T, R < 2^31.
+ */
+FP8_API fp8_status_t fp8_residual_norm_quant(
+    const void* h, int64_t ldh, const void* y, int64_t ldy, int64_t R, const int32_t* token_row,
+    const float* weights, int64_t top_k, const void* gamma_post, const void* gate, int64_t ldg,
+    const void* gamma, float eps, float residual_scale, float branch_scale, int64_t T, int64_t K,
+    void* h_out, int64_t ldho, void* z_out, uint8_t* xq, int64_t ldq, float* s_tok, void* stream);
+
 /* Workspace bytes fp8_linear needs for an [M, K] x [N, K]^T layer:
  * round_up(M*K, 256) + round_up(4*M, 256).  0 for invalid sizes. */
 FP8_API size_t fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K);
