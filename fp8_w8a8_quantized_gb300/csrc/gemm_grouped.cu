@@ -3,10 +3,34 @@
 //   a[r, n] = ((sum_k e4m3(xq[r, k]) e4m3(wq[e, n, k])) s_tok[r]) s_w[e, n]
 //   y = bf16(a), or bf16(silu(a[:, n]) a[:, n + N / 2])
 //
-// Simple form: a 32 x 32 tile of outputs a CTA, codes converted to fp32 in
-// shared memory, sums in fp32.
+// One persistent launch: each worker counts every expert's tiles from the bounds
+// and takes its share of the list.  A tile is 128 rows a CTA by 256 weight rows
+// (with the gated activation 128 of the gate and the 128 of the values that go
+// with them, so that both lie in the same lanes of tensor memory).  Rows are on
+// the MMA's M side even where an expert has few: the weights are then read as
+// fast as DRAM gives them with the tensor cores 40% busy, and the rows that an
+// expert does not have cost no loads (boxes of 32 rows are left out) and no
+// stores.  What MMAs read there is whatever the ring held; it reaches outputs of
+// those rows alone, which nothing reads.
+//   kPair = false: a worker is a CTA (cta_group::1, stages of 128 of K).  For
+//     few rows an expert: every SM streams weights of its own.
+//   kPair = true: a worker is two CTAs on two SMs (cta_group::2, 256 x 256 tiles,
+//     stages of 256 of K), as in gemm_pair.cu: half the loads into shared memory
+//     per product.
+//
+// The list: tile t of an expert's ceil(rows / tile rows) x ceil(N / 256), row
+// tiles next to one another, so that workers that run at the same time share
+// weights in L2.  Workers take whole tiles in turn; the tiles of the last,
+// unfull round are cut along K into equal shares for all workers.  A worker
+// that has part of a tile leaves its sums in the workspace, and the last of a
+// tile's workers to arrive (a counter for each 32 rows, zeroed by the kernel
+// before) adds the parts in the order of K: the order of every sum is fixed by
+// the sizes and bounds.  No worker waits for another.
+//
+// Per CTA 192 threads: warp 0 loads (TMA), warp 1 issues the MMAs (in a pair the
+// even CTA's), warps 2 to 5 scale, round and store.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -17,82 +41,618 @@
 namespace fp8k {
 namespace {
 
-constexpr int kTile = 32;
-constexpr int kDepth = 64;
-constexpr int kThreads = 256;
+constexpr int kThreads = 192;
+constexpr int kRows = 128;        // rows a CTA
+constexpr int BN = 256;           // accumulator columns
+constexpr int kHalf = 128;        // weight rows of a TMA box
+constexpr int kBoxRows = 32;      // rows of X of a TMA box
+constexpr int BKS = 128;          // bytes of K of a swizzled column
+constexpr int KSTEP = 32;         // K of one tcgen05.mma kind::f8f6f4
+constexpr int kAccBufs = 2;
+constexpr uint32_t TMEM_COLS = kAccBufs * BN;
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxCtas = 152;
+constexpr int kQuarters = 4;      // epilogue warps: 32 rows each
 
-__device__ __forceinline__ float value(uint8_t code) {
-    __nv_fp8_e4m3 v;
-    v.__x = code;
-    return static_cast<float>(v);
+template <bool kPair>
+struct Cfg {
+    static constexpr int CTAS = kPair ? 2 : 1;
+    static constexpr int BM = kRows * CTAS;
+    static constexpr int BK = kPair ? 256 : 128;  // K of a stage
+    static constexpr int COLUMNS = BK / BKS;
+    static constexpr int STAGES = kPair ? 3 : 4;
+    static constexpr int B_ROWS = BN / CTAS;      // weight rows in this CTA
+    static constexpr uint32_t A_COLUMN = kRows * BKS;
+    static constexpr uint32_t B_COLUMN = B_ROWS * BKS;
+    static constexpr uint32_t A_TILE = A_COLUMN * COLUMNS;
+    static constexpr uint32_t B_TILE = B_COLUMN * COLUMNS;
+    static constexpr uint32_t RING = STAGES * (A_TILE + B_TILE);
+};
+
+template <int kStages>
+struct Bars {
+    uint64_t full[kStages];    // pair: the even CTA's
+    uint64_t empty[kStages];
+    uint64_t acc_full[kAccBufs];
+    uint64_t acc_empty[kAccBufs];  // pair: the even CTA's
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    float s_w[kQuarters][BN];      // a tile's weight scales, each epilogue warp's own copy
+    int first[kMaxExperts + 1];    // tiles of the experts below
+};
+
+template <bool kPair>
+constexpr size_t smem_bytes() {
+    return 1024 + Cfg<kPair>::RING + sizeof(Bars<Cfg<kPair>::STAGES>);
 }
 
-__global__ void __launch_bounds__(kThreads)
-    grouped_simple(const uint8_t* xq, const float* s_tok, const uint8_t* wq,
-                   const float* s_w, const int32_t* offsets, int R, int N, int K, bool swiglu,
-                   __nv_bfloat16* y) {
-    __shared__ float xs[kTile][kDepth + 1], ws[2][kTile][kDepth + 1];
+struct Args {
+    const float* s_tok;
+    const float* s_w;
+    const int32_t* offsets;
+    __nv_bfloat16* y;
+    unsigned* count;   // [workers][CTAS][kQuarters]
+    float* parts;      // [workers][CTAS][2][slot]
+    int64_t slot;      // floats of a part: its quarters of 32 rows x BN
+    int E, R, N, K;
+    int min_saved;     // a round is cut where that saves so many stages
+    unsigned* status;
+};
+
+struct Bounds {
+    int begin, end;
+};
+__device__ __forceinline__ Bounds bounds_of(const Args& a, int e) {
+    Bounds b;
+    b.begin = min(max(a.offsets[e], 0), a.R);
+    b.end = min(max(a.offsets[e + 1], b.begin), a.R);
+    return b;
+}
+
+// A worker's pieces of the list in order: whole tiles, then its share of the
+// tiles that are cut.
+struct Walk {
+    int tiles, workers, nk;  // tiles of the list; workers of the cut ones
+    int whole;               // tiles of the list that are taken whole
+    int64_t units;           // stages of the others
+    int next;
+    int64_t u, u_end;
+    int tile, kb0, kb1;
+    __device__ __forceinline__ Walk(int all, int n, int me, int stages, int min_saved)
+        : tiles(all), workers(n), nk(stages), next(me) {
+        const int rest = all % n;
+        // (cut, the last round takes rest / n of a tile's time instead of all of it)
+        const bool cut = rest && static_cast<int64_t>(nk) * (n - rest) >= static_cast<int64_t>(min_saved) * n;
+        whole = cut ? all - rest : all;
+        units = cut ? static_cast<int64_t>(rest) * nk : 0;
+        if (units < workers) workers = static_cast<int>(units);  // (one stage at least for each)
+        u = me < workers ? units * me / workers : 0;
+        u_end = me < workers ? units * (me + 1) / workers : 0;
+        step = n;
+    }
+    __device__ __forceinline__ bool advance() {
+        if (next < whole) {
+            tile = next;
+            kb0 = 0, kb1 = nk;
+            next += step;
+            return true;
+        }
+        if (u >= u_end) return false;
+        const int64_t j = u / nk;
+        tile = whole + static_cast<int>(j);
+        kb0 = static_cast<int>(u - j * nk);
+        kb1 = static_cast<int>(min(static_cast<int64_t>(nk), kb0 + (u_end - u)));
+        u += kb1 - kb0;
+        return true;
+    }
+    // the worker that has unit x of the cut tiles
+    __device__ __forceinline__ int worker_of(int64_t x) const {
+        return static_cast<int>(((x + 1) * workers - 1) / units);
+    }
+
+   private:
+    int step;
+};
+
+// Where a tile lies.
+struct Place {
+    int e, row0, rows, n_blk;  // its first row, how many rows the expert has from there on
+};
+struct Finder {
+    int e = -1, begin = 0, end = 0, m_tiles = 1;
+    template <int BM>
+    __device__ __forceinline__ Place at(const Args& a, const int* first, int tile) {
+        if (e < 0 || tile < first[e] || tile >= first[e + 1]) {
+            int lo = 0, hi = a.E;  // first[lo] <= tile < first[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= tile) lo = mid;
+                else hi = mid;
+            }
+            e = lo;
+            const Bounds b = bounds_of(a, e);
+            begin = b.begin, end = b.end;
+            m_tiles = (end - begin + BM - 1) / BM;
+        }
+        const int local = tile - first[e];
+        const int n = local / m_tiles, m = local - n * m_tiles;
+        return {e, begin + m * BM, end - begin - m * BM, n};
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <bool kPair, bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Args a) {
+    using C = Cfg<kPair>;
+    using B = Bars<C::STAGES>;
+    constexpr int kOut = kGated ? BN / 2 : BN;  // outputs of a tile's row
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + C::STAGES * C::A_TILE;
+    B* bars = reinterpret_cast<B*>(smem + C::RING);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+    const bool leader = rank == 0;
+    const int worker = blockIdx.x / C::CTAS, workers = gridDim.x / C::CTAS;
+    const int F = kGated ? a.N / 2 : a.N;
+    const int nk = (a.K + C::BK - 1) / C::BK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int b = 0; b < kAccBufs; ++b) {
+            mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->acc_empty[b], kQuarters * C::CTAS);
+        }
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+    }
+    if (warp == 1) {
+        if constexpr (kPair) {
+            tmem_alloc_pair(&bars->tmem_base, TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&bars->tmem_base, TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    pdl_launch_dependents();  // (behind the allocation: see ptx.cuh)
+    if constexpr (kPair) cluster_sync_all();  // the peer's barriers and tensor memory are there
+    tc_fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+    volatile int* abort_flag = &bars->abort;
+
+    pdl_wait_primary();
+
+    // tiles of each expert, then of all below it
+    const int n_tiles = (F + kOut - 1) / kOut;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        const Bounds b = bounds_of(a, e);
+        bars->first[e + 1] = (b.end - b.begin + C::BM - 1) / C::BM * n_tiles;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int sum = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            int v = e0 + lane < a.E ? bars->first[e0 + lane + 1] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                if (lane >= d) v += u;
+            }
+            if (e0 + lane < a.E) bars->first[e0 + lane + 1] = sum + v;
+            sum += __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+        if (lane == 0) bars->first[0] = 0;
+    }
+    __syncthreads();
+    Walk walk(bars->first[a.E], workers, worker, nk, a.min_saved);
+    Finder find;
+
+    if (warp == 0) {
+        // ---- loads: this CTA's rows of X, its part of the weight rows ----
+        uint32_t stage = 0, phase = 0, issued = 0;
+        bool ok = true;
+        while (ok && walk.advance()) {
+            const Place p = find.at<C::BM>(a, bars->first, walk.tile);
+            const int mine = min(max(p.rows - rank * kRows, 0), kRows);
+            const int boxes = (mine + kBoxRows - 1) / kBoxRows;
+            // weight rows: with a gate the gate's and the values', else two halves of
+            // which the second may not be there
+            const int n0 = p.n_blk * kOut;
+            const int w0 = p.e * a.N + n0, w1 = kGated ? w0 + F : w0 + kHalf;
+            const bool two = kGated || n0 + kHalf < a.N;
+            uint32_t bytes;  // that the stage's barrier waits for
+            if constexpr (kPair) {
+                const int all = min(p.rows, kRows) + kBoxRows - 1, other = max(min(p.rows - kRows, kRows), 0) + kBoxRows - 1;
+                bytes = (all / kBoxRows + other / kBoxRows) * kBoxRows * C::BK + (two ? 2 : 1) * kHalf * C::BK;
+            } else {
+                bytes = boxes * kBoxRows * C::BK + (two ? 2 : 1) * kHalf * C::BK;
+            }
+            for (int kb = walk.kb0; kb < walk.kb1; ++kb) {
+                if (!(ok = warp_wait(&bars->empty[stage], phase ^ 1u, abort_flag, a.status))) break;
+                if (lane == 0) {
+                    uint8_t* xa = sA + stage * C::A_TILE;
+                    uint8_t* wb = sB + stage * C::B_TILE;
+                    const int row = p.row0 + rank * kRows;
+                    if (leader) mbar_arrive_expect_tx(&bars->full[stage], bytes);
+                    if constexpr (kPair) {
+                        const uint32_t full0 = map_to_rank(smem_u32(&bars->full[stage]), 0);
+#pragma unroll
+                        for (int j = 0; j < C::COLUMNS; ++j) {
+                            const int k = kb * C::BK + j * BKS;
+                            if (rank == 0 || two)
+                                tma_load_2d_pair(wb + j * C::B_COLUMN, &tmW, full0, k, rank ? w1 : w0);
+                            for (int i = 0; i < boxes; ++i)
+                                tma_load_2d_pair(xa + j * C::A_COLUMN + i * kBoxRows * BKS, &tmX, full0, k,
+                                                 row + i * kBoxRows);
+                        }
+                    } else {
+                        const int k = kb * C::BK;
+                        tma_load_2d(wb, &tmW, &bars->full[stage], k, w0);
+                        if (two) tma_load_2d(wb + kHalf * BKS, &tmW, &bars->full[stage], k, w1);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(xa + i * kBoxRows * BKS, &tmX, &bars->full[stage], k, row + i * kBoxRows);
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok && leader && lane == 0) {  // copies in flight land before the shared memory goes away
+            for (uint32_t j = issued > C::STAGES ? issued - C::STAGES : 0; j < issued; ++j)
+                wait_landed(&bars->full[j % C::STAGES], (j / C::STAGES) & 1u, a.status);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader) {
+            // ---- MMAs ----
+            constexpr uint32_t idesc = idesc_e4m3_f32(C::BM, BN);
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            int local = 0;
+            while (ok && walk.advance()) {
+                const int buf = local % kAccBufs;
+                const uint32_t acc_phase = (local / kAccBufs) & 1;
+                ++local;
+                if (!(ok = warp_wait_cluster(&bars->acc_empty[buf], acc_phase ^ 1u, abort_flag, a.status))) break;
+                tc_fence_after();
+                const uint32_t d = uniform(tmem_base + buf * BN);
+                for (int kb = walk.kb0; kb < walk.kb1; ++kb) {
+                    if (!(ok = warp_wait(&bars->full[stage], phase, abort_flag, a.status))) break;
+                    tc_fence_after();
+                    const uint32_t xa = uniform(smem_u32(sA + stage * C::A_TILE));
+                    const uint32_t wb = uniform(smem_u32(sB + stage * C::B_TILE));
+                    const uint32_t more = uniform(kb != walk.kb0);
+                    if (elect_one()) {
+                        const uint64_t a0 = sdesc_kmajor_sw128(xa), b0 = sdesc_kmajor_sw128(wb);
+#pragma unroll
+                        for (int kk = 0; kk < C::BK / KSTEP; ++kk) {
+                            const int j = kk / (BKS / KSTEP), w = kk % (BKS / KSTEP);
+                            const uint64_t ad = a0 + ((j * C::A_COLUMN) >> 4) + 2 * w;
+                            const uint64_t bd = b0 + ((j * C::B_COLUMN) >> 4) + 2 * w;
+                            if constexpr (kPair) mma_f8_pair(d, ad, bd, idesc, kk ? 1u : more);
+                            else mma_f8(d, ad, bd, idesc, kk ? 1u : more);
+                        }
+                        if constexpr (kPair) mma_commit_pair(&bars->empty[stage], 0x3);
+                        else mma_commit(&bars->empty[stage]);
+                    }
+                    __syncwarp();
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok && elect_one()) {
+                    if constexpr (kPair) mma_commit_pair(&bars->acc_full[buf], 0x3);
+                    else mma_commit(&bars->acc_full[buf]);
+                }
+                __syncwarp();
+            }
+            // every MMA has finished before tensor memory is freed
+            if (elect_one()) {
+                if constexpr (kPair) mma_commit_pair(&bars->drain, 0x1);
+                else mma_commit(&bars->drain);
+                wait_drain(&bars->drain, a.status);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---- outputs: 32 of this CTA's 128 rows a warp ----
+        const int quarter = warp & 3;
+        float* sw = bars->s_w[quarter];
+        const bool wide = F % 8 == 0;  // rows of y at 16-byte boundaries
+        int local = 0;
+        while (walk.advance()) {
+            const Place p = find.at<C::BM>(a, bars->first, walk.tile);
+            const int buf = local % kAccBufs;
+            const uint32_t acc_phase = (local / kAccBufs) & 1;
+            ++local;
+            const int first_row = rank * kRows + quarter * 32;  // of the warp, within the tile
+            const bool any = first_row < p.rows;
+            const bool row_ok = first_row + lane < p.rows;
+            const int64_t row = p.row0 + first_row + lane;
+            const int n0 = p.n_blk * kOut;
+            float st = 0.0f;
+            if (any) {
+                if (row_ok) st = a.s_tok[row];
+#pragma unroll
+                for (int i = 0; i < BN / 32; ++i) {
+                    const int c = i * 32 + lane;
+                    const int n = kGated ? (c & (kOut - 1)) + n0 : c + n0;
+                    sw[c] = n < F ? a.s_w[static_cast<int64_t>(p.e) * a.N + n + (kGated && c >= kOut ? F : 0)] : 0.0f;
+                }
+                __syncwarp();
+            }
+            // 32 outputs of this lane's row from column n0 + 32 c on
+            auto emit = [&](const float (&v)[32], int c) {
+                uint32_t packed[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                const int n = n0 + 32 * c;
+                if (!row_ok || n >= F) return;
+                __nv_bfloat16* out = a.y + row * F + n;
+                if (wide && n + 32 <= F) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        reinterpret_cast<uint4*>(out)[j] =
+                            make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+                } else {
+                    // (unrolled with a guard a column, so that packed[] stays in registers)
+                    uint16_t* o = reinterpret_cast<uint16_t*>(out);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (n + j < F) o[j] = static_cast<uint16_t>(packed[j >> 1] >> ((j & 1) * 16));
+                }
+            };
+            auto scaled = [&](float acc, int c) { return (acc * st) * sw[c]; };
+            auto gated = [&](float g, float u) { return g / (1.0f + __expf(-g)) * u; };
+            auto release = [&] {  // the accumulator has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (kPair) mbar_arrive_cluster(map_to_rank(smem_u32(&bars->acc_empty[buf]), 0));
+                    else mbar_arrive(&bars->acc_empty[buf]);
+                }
+            };
+            if (!warp_wait(&bars->acc_full[buf], acc_phase, abort_flag, a.status)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN;
+            if (!any) {
+                release();
+                continue;
+            }
+            if (walk.kb0 == 0 && walk.kb1 == nk) {
+                if constexpr (kGated) {
+#pragma unroll
+                    for (int c = 0; c < kOut / 32; ++c) {
+                        uint32_t g[32], u[32];
+                        tmem_ld_32x32b_x32(acc + 32 * c, g);
+                        tmem_ld_32x32b_x32(acc + kOut + 32 * c, u);
+                        tmem_ld_wait_regs(g);
+                        tmem_ld_wait_regs(u);
+                        if (c == kOut / 32 - 1) release();
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = gated(scaled(__uint_as_float(g[j]), 32 * c + j),
+                                         scaled(__uint_as_float(u[j]), kOut + 32 * c + j));
+                        emit(v, c);
+                    }
+                } else {
+                    // (chunk c + 1 is on its way while chunk c is scaled and stored)
+                    uint32_t ra[32], rb[32];
+                    auto one = [&](const uint32_t (&r)[32], int c) {
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = scaled(__uint_as_float(r[j]), 32 * c + j);
+                        emit(v, c);
+                    };
+                    tmem_ld_32x32b_x32(acc, ra);
+                    tmem_ld_wait_regs(ra);
+#pragma unroll
+                    for (int c = 0; c < BN / 32; c += 2) {
+                        tmem_ld_32x32b_x32(acc + (c + 1) * 32, rb);
+                        one(ra, c);
+                        tmem_ld_wait_regs(rb);
+                        if (c + 2 < BN / 32) tmem_ld_32x32b_x32(acc + (c + 2) * 32, ra);
+                        else release();
+                        one(rb, c + 1);
+                        if (c + 2 < BN / 32) tmem_ld_wait_regs(ra);
+                    }
+                }
+                __syncwarp();
+                continue;
+            }
+            // Part of a tile: the sums go to the workspace, four columns of a row side by
+            // side, the warp's rows next to one another.
+            auto part = [&](int w, int slot) {
+                return reinterpret_cast<float4*>(a.parts + ((static_cast<int64_t>(w) * C::CTAS + rank) * 2 + slot) * a.slot +
+                                                 quarter * 32 * BN) + lane;
+            };
+            float4* mine = part(worker, walk.kb0 == 0 ? 1 : 0);
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(acc + 32 * c, r);
+                tmem_ld_wait_regs(r);
+                if (row_ok) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        __stcg(mine + (8 * c + j) * 32,
+                               make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                           __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+                }
+            }
+            release();
+            const int64_t unit = static_cast<int64_t>(walk.tile - walk.whole) * nk;
+            const int w_first = walk.worker_of(unit), w_last = walk.worker_of(unit + nk - 1);
+            __threadfence();
+            __syncwarp();
+            unsigned before = 0;
+            if (lane == 0)
+                before = atomicAdd(a.count + (static_cast<int64_t>(w_first) * C::CTAS + rank) * kQuarters + quarter, 1u);
+            before = __shfl_sync(0xFFFFFFFFu, before, 0);
+            if (before != static_cast<unsigned>(w_last - w_first)) continue;
+            __threadfence();
+            auto sum = [&](float (&v)[32], int c) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                if (!row_ok) return;
+                for (int w = w_first; w <= w_last; ++w) {
+                    const float4* from = part(w, w == w_first ? 1 : 0) + 8 * c * 32;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 f = __ldcg(from + j * 32);
+                        v[4 * j] += f.x, v[4 * j + 1] += f.y, v[4 * j + 2] += f.z, v[4 * j + 3] += f.w;
+                    }
+                }
+            };
+            for (int c = 0; c < kOut / 32; ++c) {
+                float v[32];
+                sum(v, c);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = scaled(v[j], 32 * c + j);
+                if constexpr (kGated) {
+                    float u[32];
+                    sum(u, c + kOut / 32);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = gated(v[j], scaled(u[j], kOut + 32 * c + j));
+                }
+                emit(v, c);
+            }
+            __syncwarp();
+        }
+    }
+
+    // Neither CTA of a pair may free tensor memory or exit while MMAs, the peer's
+    // copies or its arrivals can still touch it.
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (kPair) cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (kPair) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+__global__ void clear_counts(unsigned* count, int n) {
     pdl_launch_dependents();
     pdl_wait_primary();
-    const int e = blockIdx.y;
-    const int begin = min(max(offsets[e], 0), R), end = min(max(offsets[e + 1], begin), R);
-    const int F = swiglu ? N / 2 : N;
-    const int n0 = blockIdx.x * kTile;
-    const int c = threadIdx.x % kTile, r0 = threadIdx.x / kTile;
-    for (int m0 = begin; m0 < end; m0 += kTile) {
-        float acc[2][4] = {};
-        for (int k0 = 0; k0 < K; k0 += kDepth) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-                const int r = i / kDepth, k = i % kDepth;
-                const bool in = k0 + k < K;
-                xs[r][k] = in && m0 + r < end ? value(xq[static_cast<int64_t>(m0 + r) * K + k0 + k]) : 0.0f;
-                for (int h = 0; h < (swiglu ? 2 : 1); ++h)
-                    ws[h][r][k] = in && n0 + r < F
-                                      ? value(wq[(static_cast<int64_t>(e) * N + h * F + n0 + r) * K + k0 + k])
-                                      : 0.0f;
-            }
-            __syncthreads();
-            for (int k = 0; k < kDepth; ++k)
-                for (int h = 0; h < (swiglu ? 2 : 1); ++h)
-                    for (int i = 0; i < 4; ++i) acc[h][i] += xs[r0 + 8 * i][k] * ws[h][c][k];
-        }
-        const int n = n0 + c;
-        if (n < F)
-            for (int i = 0; i < 4; ++i) {
-                const int r = m0 + r0 + 8 * i;
-                if (r >= end) continue;
-                float v = acc[0][i] * s_tok[r] * s_w[static_cast<int64_t>(e) * N + n];
-                if (swiglu) v = v / (1.0f + expf(-v)) * (acc[1][i] * s_tok[r] * s_w[static_cast<int64_t>(e) * N + F + n]);
-                y[static_cast<int64_t>(r) * F + n] = __float2bfloat16_rn(v);
-            }
-    }
+    for (int i = threadIdx.x; i < n; i += blockDim.x) count[i] = 0;
+}
+
+constexpr int64_t kCounts = kMaxCtas * kQuarters;
+constexpr int64_t kCountBytes = (kCounts * 4 + 255) / 256 * 256;
+
+// Floats of a part: the quarters of 32 rows that a CTA can have.
+int64_t slot_floats(int64_t R) {
+    const int64_t quarters = (R + 31) / 32;
+    return (quarters < kQuarters ? quarters : kQuarters) * 32 * BN;
+}
+
+// Pairs where experts have many rows on average.
+bool pairs_of(int64_t E, int64_t R) { return R >= 96 * E; }
+
+template <bool kPair, bool kGated>
+cudaError_t launch(const GroupedArgs& g, const Args& a, cudaStream_t st) {
+    using C = Cfg<kPair>;
+    CUtensorMap tmX, tmW;
+    if (!encode_tmap_u8(&tmX, g.xq, g.R, g.K, g.K, BKS, kBoxRows)) return cudaErrorInvalidValue;
+    if (!encode_tmap_u8(&tmW, g.wq, static_cast<uint64_t>(g.E) * g.N, g.K, g.K, BKS, kHalf)) return cudaErrorInvalidValue;
+    int ctas = g.num_sms < kMaxCtas ? g.num_sms : kMaxCtas;
+    if (kPair && g.pair_clusters > 0 && 2 * g.pair_clusters < ctas) ctas = 2 * g.pair_clusters;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(ctas / C::CTAS * C::CTAS);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<kPair>();
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, gemm_grouped_kernel<kPair, kGated>, tmX, tmW, a);
 }
 
 }  // namespace
 
 size_t gemm_grouped_workspace(int64_t E, int64_t R, int64_t N, int64_t K) {
-    (void)E, (void)R, (void)N, (void)K;
-    return 0;
+    (void)E, (void)N, (void)K;
+    return static_cast<size_t>(kCountBytes + kMaxCtas * 2 * slot_floats(R) * 4);
 }
 
-int64_t gemm_grouped_zero_words() { return 0; }
+int64_t gemm_grouped_zero_words() { return kCounts; }
 
-cudaError_t prepare_gemm_grouped() { return cudaSuccess; }
+cudaError_t prepare_gemm_grouped() {
+    auto set = [](auto kernel, size_t bytes) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    };
+    cudaError_t e = set(gemm_grouped_kernel<false, false>, smem_bytes<false>());
+    if (e == cudaSuccess) e = set(gemm_grouped_kernel<false, true>, smem_bytes<false>());
+    if (e == cudaSuccess) e = set(gemm_grouped_kernel<true, false>, smem_bytes<true>());
+    if (e == cudaSuccess) e = set(gemm_grouped_kernel<true, true>, smem_bytes<true>());
+    return e;
+}
 
-cudaError_t launch_gemm_grouped(const GroupedArgs& a, cudaStream_t st) {
-    const int F = a.swiglu ? a.N / 2 : a.N;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((F + kTile - 1) / kTile, a.E);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, grouped_simple, a.xq, a.s_tok, a.wq, a.s_w, a.offsets, a.R, a.N, a.K, a.swiglu,
-                              static_cast<__nv_bfloat16*>(a.y));
+cudaError_t launch_gemm_grouped(const GroupedArgs& g, cudaStream_t st) {
+    Args a;
+    a.s_tok = g.s_tok, a.s_w = g.s_w;
+    a.offsets = g.offsets;
+    a.y = static_cast<__nv_bfloat16*>(g.y);
+    a.count = static_cast<unsigned*>(g.workspace);
+    a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(g.workspace) + kCountBytes);
+    a.slot = slot_floats(g.R);
+    a.E = g.E, a.R = g.R, a.N = g.N, a.K = g.K;
+    a.status = g.status;
+    if (!g.zeroed) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, clear_counts, a.count, static_cast<int>(kCounts));
+        if (e != cudaSuccess) return e;
+    }
+    if (pairs_of(g.E, g.R)) {
+        a.min_saved = 8;
+        return g.swiglu ? launch<true, true>(g, a, st) : launch<true, false>(g, a, st);
+    }
+    a.min_saved = 3;
+    return g.swiglu ? launch<false, true>(g, a, st) : launch<false, false>(g, a, st);
 }
 
 }  // namespace fp8k
