@@ -117,7 +117,6 @@ fp8_status_t fp8_moe_route(const void* logits, int logits_fp32, int64_t ld, int6
     a.weights = weights;
     a.offsets = offsets, a.row_token = row_token, a.token_row = token_row;
     a.workspace = static_cast<int32_t*>(workspace);
-    a.num_sms = num_sms;
     return said(fp8k::launch_moe_route(a, as_stream(stream)));
 }
 

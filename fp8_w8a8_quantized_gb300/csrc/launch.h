@@ -197,7 +197,6 @@ struct RouteArgs {
     float* weights;
     int32_t *offsets, *row_token, *token_row;
     int32_t* workspace;
-    int num_sms;
 };
 cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t st);
 size_t moe_route_workspace(int64_t T, int64_t E, int64_t k);

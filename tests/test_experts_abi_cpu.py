@@ -22,7 +22,7 @@ def call(f, defaults, **changed):
     return f(*{**defaults, **changed}.values())
 
 
-ROUTE = dict(logits=P, fp32=1, ld=64, T=32, E=64, k=8, renorm=1, scale=1.0, ids=P, weights=P, offsets=P, rows=P,
+ROUTE = dict(logits=P, fp32=1, ld=64, T=4096, E=64, k=8, renorm=1, scale=1.0, ids=P, weights=P, offsets=P, rows=P,
              back=P, ws=P, bytes=1 << 30, stream=None)
 GEMM = dict(xq=P, s_tok=P, wq=P, s_w=P, offsets=P, E=8, R=64, N=256, K=512, swiglu=0, y=P, ws=P, bytes=1 << 30,
             stream=None)
@@ -92,7 +92,8 @@ def test_workspaces(L):
         assert call(L.fp8_grouped_gemm, GEMM, bytes=need - 1) == WS
         assert call(L.fp8_grouped_gemm, GEMM, ws=None) == WS
         assert call(L.fp8_grouped_gemm, GEMM, ws=P + 128) == WS
-    need = L.fp8_moe_route_workspace_size(32, 64, 8)
+    need = L.fp8_moe_route_workspace_size(4096, 64, 8)
+    assert need > 0
     assert call(L.fp8_moe_route, ROUTE, bytes=need - 1) == WS
     for bad in ((0, 64, 256, 512), (8, -1, 256, 512), (8, 64, 256, 500), (8, 0, 256, 512), (8, 64, 0, 512),
                 (1025, 64, 256, 512), (8, 64, 1 << 29, 512)):
