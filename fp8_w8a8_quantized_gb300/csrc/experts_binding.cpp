@@ -183,6 +183,18 @@ PyObject* residual_norm_quant(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     TORCH_CHECK_VALUE(want_codes || (!xq.defined() && !s_tok.defined()), "xq and s_tok need codes=True");
     const Place place(h, a[16]);
     int64_t ldho = K, ldq = K;
+    if (!h_out.defined() && !z.defined() && !xq.defined() && !s_tok.defined()) {
+        // one allocation for all of them
+        auto bytes = [](int64_t n) { return (n + 255) / 256 * 256; };
+        const int64_t wide = bytes(2 * T * K), at_q = wide + (want_z ? wide : 0), at_s = at_q + bytes(T * K);
+        const Tensor block = make({want_codes ? at_s + 4 * T : at_q}, at::kByte, h);
+        h_out = carve(block, 0, {T, K}, at::kBFloat16);
+        if (want_z) z = carve(block, wide, {T, K}, at::kBFloat16);
+        if (want_codes) {
+            xq = carve(block, at_q, {T, K}, at::kByte);
+            s_tok = carve(block, at_s, {T}, at::kFloat);
+        }
+    }
     if (h_out.defined()) ldho = rows(h_out, "h_out", at::kBFloat16, {T, K});
     else h_out = make({T, K}, at::kBFloat16, h);
     if (want_z) result(z, "z", at::kBFloat16, {T, K}, h);

@@ -8,9 +8,12 @@
 //
 // A group of G threads owns a token and keeps its row in registers in fp32,
 // 8 elements (a 16-byte load) a chunk, so that every tensor is read once and
-// each result is rounded once.  Up to three reductions over the row follow one
-// another (sum of squares of b, of h', maximum of z); several CTAs an SM hide
-// them.
+// each result is rounded once.  Everything that a token needs is asked for at its
+// start or ahead of the reduction before it is used: up to three reductions over
+// the row follow one another (sum of squares of b, of h', maximum of z), and
+// several CTAs an SM hide them.  Bound by DRAM, with the instructions close
+// behind: arithmetic is on pairs (f32x2), and z is kept negated, which is what the
+// quantizer's division wants (quant_math.cuh).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -49,138 +52,173 @@ __device__ __forceinline__ float over_row(float v, float* red) {
 // (plain loads: what earlier kernels write may not come through the read-only path)
 __device__ __forceinline__ uint4 load(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
-__device__ __forceinline__ void widen(const uint4& u, float (&v)[8]) {
-    v[0] = bf16lo(u.x), v[1] = bf16hi(u.x), v[2] = bf16lo(u.y), v[3] = bf16hi(u.y);
-    v[4] = bf16lo(u.z), v[5] = bf16hi(u.z), v[6] = bf16lo(u.w), v[7] = bf16hi(u.w);
-}
+__device__ __forceinline__ uint32_t word(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 
+// Two fp32 values -> a bf16 pair, `lo` in the low half.
 __device__ __forceinline__ uint32_t pair(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint4 narrow(const float (&v)[8]) {
-    return make_uint4(pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7]));
+__device__ __forceinline__ uint4 narrow(const float (&v)[8], uint32_t flip = 0) {
+    return make_uint4(pair(v[0], v[1]) ^ flip, pair(v[2], v[3]) ^ flip, pair(v[4], v[5]) ^ flip, pair(v[6], v[7]) ^ flip);
 }
 
-__device__ __forceinline__ float quotient(float x, const Divisor& d) {
-    return d.ieee ? __fdiv_rn(x, d.s) : div_rn(x, d);
+// v += s * u, v *= u, v *= s, and the sum of squares of v into (s0, s1).
+__device__ __forceinline__ void add_scaled(float (&v)[8], float s, const uint4& u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fma2(v[2 * i], v[2 * i + 1], bf16lo(word(u, i)), bf16hi(word(u, i)), s, s);
+}
+__device__ __forceinline__ void times(float (&v)[8], const uint4& u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mul2(v[2 * i], v[2 * i + 1], v[2 * i], v[2 * i + 1], bf16lo(word(u, i)), bf16hi(word(u, i)));
+}
+__device__ __forceinline__ void times(float (&v)[8], float s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mul2(v[2 * i], v[2 * i + 1], v[2 * i], v[2 * i + 1], s, s);
+}
+__device__ __forceinline__ void squares(const float (&v)[8], float& s0, float& s1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fma2(s0, s1, v[2 * i], v[2 * i + 1], v[2 * i], v[2 * i + 1]);
 }
 
-template <int G, int VPT>
-__global__ void __launch_bounds__(G > kBlock ? G : kBlock) residual_norm(const ResidualNormArgs a) {
+// Codes of -v / s: the steps of quant2 (quant_math.cuh) on fp32 values, which |v| <= 448 s bounds.
+__device__ __forceinline__ uint2 codes_of_negated(const float (&v)[8], const Divisor& d) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float z0 = v[2 * i], z1 = v[2 * i + 1];
+        if (d.ieee) {
+            c[i] = cvt_e4m3x2(__fdiv_rn(-z0, d.s), __fdiv_rn(-z1, d.s));
+            continue;
+        }
+        float q0, q1;
+        mul2(q0, q1, z0, z1, d.nr, d.nr);
+        float e0 = z0, e1 = z1;
+        fma2(e0, e1, q0, q1, d.s, d.s);
+        float y0 = q0, y1 = q1;
+        fma2(y0, y1, e0, e1, d.nr, d.nr);
+        c[i] = cvt_e4m3x2(y0, y1);
+    }
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+// kTop: the branch is rows of y by weight, not row t of it.
+template <int G, int VPT, bool kTop>
+__global__ void __launch_bounds__(G > kBlock ? G : kBlock, 1024 / (G > kBlock ? G : kBlock)) residual_norm(const ResidualNormArgs a) {
     constexpr int B = G > kBlock ? G : kBlock;
     constexpr int ROWS = B / G;
+    constexpr uint32_t kNegate = 0x80008000u;
+    // (64 registers a thread do not hold two chunks of everything)
+    constexpr bool kEarly = G < 1024 || VPT == 1;
+    constexpr int kAhead = kEarly ? 2 : 1;  // rows of a token on their way at a time
     __shared__ float red[B / 32];
     pdl_launch_dependents();
     pdl_wait_primary();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / G;
     const int i0 = threadIdx.x % G;
-    const bool live = t < a.T;
     const int C = static_cast<int>(a.K >> 3);
+    const int mine = t < a.T ? (C - i0 + G - 1) / G : 0;  // chunks of this thread
     const float K = static_cast<float>(a.K);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
+    uint4 h[VPT], g[VPT];
+    auto load_stream = [&](int i) { h[i] = i < mine ? load(a.h + t * a.ldh + 8 * (i0 + i * G)) : zero; };
+    auto load_gate = [&](int i) {
+        if (a.gate) g[i] = i < mine ? load(a.gate + t * a.ldg + 8 * (i0 + i * G)) : zero;
+    };
     float b[VPT][8];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i) {
+        if constexpr (kEarly) {
+            load_stream(i);
+            load_gate(i);
+        }
+        const uint4 y = !kTop && i < mine ? load(a.y + t * a.ldy + 8 * (i0 + i * G)) : zero;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[i][j] = 0.0f;
-    if (live) {
-        for (int j = 0; j < max(a.k, 1); ++j) {
-            const int64_t row = a.k > 0 ? a.token_row[t * a.k + j] : t;
-            if (row < 0 || row >= a.R) continue;
-            const float w = a.k > 0 && a.weights ? a.weights[t * a.k + j] : 1.0f;
+        for (int j = 0; j < 4; ++j) b[i][2 * j] = bf16lo(word(y, j)), b[i][2 * j + 1] = bf16hi(word(y, j));
+    }
+    if constexpr (kTop) {
+        if (mine > 0) {
+            const int32_t* rows = a.token_row + t * a.k;
+            const float* weights = a.weights ? a.weights + t * a.k : nullptr;
+            for (int j = 0; j < a.k; j += kAhead) {
+                uint4 y[kAhead][VPT];
+                float w[kAhead];
+                bool in[kAhead];
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int c = i0 + i * G;
-                if (c < C) {
-                    float v[8];
-                    widen(load(a.y + row * a.ldy + 8 * c), v);
+                for (int l = 0; l < kAhead; ++l) {
+                    const int64_t r = j + l < a.k ? rows[j + l] : -1;
+                    in[l] = r >= 0 && r < a.R;
+                    w[l] = in[l] && weights ? weights[j + l] : 1.0f;
 #pragma unroll
-                    for (int l = 0; l < 8; ++l) b[i][l] = fmaf(w, v[l], b[i][l]);
+                    for (int i = 0; i < VPT; ++i)
+                        if (in[l] && i < mine) y[l][i] = load(a.y + r * a.ldy + 8 * (i0 + i * G));
                 }
+#pragma unroll
+                for (int l = 0; l < kAhead; ++l)
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i)
+                        if (in[l] && i < mine) add_scaled(b[i], w[l], y[l][i]);
             }
         }
     }
     if (a.gamma_post) {
-        float ss = 0.0f;
+        uint4 p[VPT];
+        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(b[i][j], b[i][j], ss);
-        ss = over_row<G, false>(ss, red);
+        for (int i = 0; i < VPT; ++i) {
+            p[i] = i < mine ? load(a.gamma_post + 8 * (i0 + i * G)) : zero;
+            squares(b[i], s0, s1);
+        }
+        const float ss = over_row<G, false>(s0 + s1, red);
         const float inv = 1.0f / sqrtf(ss / K + a.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = i0 + i * G;
-            if (live && c < C) {
-                float g[8];
-                widen(load(a.gamma_post + 8 * c), g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) b[i][j] = b[i][j] * inv * g[j];
-            }
+            times(b[i], inv);
+            times(b[i], p[i]);
         }
     }
-    float ss = 0.0f;
+    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = i0 + i * G;
-        if (live && c < C) {
-            if (a.gate) {
-                float g[8];
-                widen(load(a.gate + t * a.ldg + 8 * c), g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) b[i][j] *= g[j];
-            }
-            float h[8];
-            widen(load(a.h + t * a.ldh + 8 * c), h);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                b[i][j] = fmaf(a.residual_scale, h[j], a.branch_scale * b[i][j]);
-                ss = fmaf(b[i][j], b[i][j], ss);
-            }
-            *reinterpret_cast<uint4*>(a.h_out + t * a.ldho + 8 * c) = narrow(b[i]);
+        if constexpr (!kEarly) {
+            load_stream(i);
+            load_gate(i);
         }
+        if (a.gate) times(b[i], g[i]);
+        times(b[i], a.branch_scale);
+        add_scaled(b[i], a.residual_scale, h[i]);
+        squares(b[i], s0, s1);
+        if (i < mine) *reinterpret_cast<uint4*>(a.h_out + t * a.ldho + 8 * (i0 + i * G)) = narrow(b[i]);
     }
     if (!a.z && !a.q) return;
-    ss = over_row<G, false>(ss, red);
-    const float inv = 1.0f / sqrtf(ss / K + a.eps);
+    uint4 p[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) p[i] = i < mine ? load(a.gamma + 8 * (i0 + i * G)) : zero;
+    const float ss = over_row<G, false>(s0 + s1, red);
+    const float inv = -1.0f / sqrtf(ss / K + a.eps);  // (z is negated from here on)
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = i0 + i * G;
-        if (live && c < C) {
-            float g[8];
-            widen(load(a.gamma + 8 * c), g);
+        times(b[i], inv);
+        times(b[i], p[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                b[i][j] = b[i][j] * inv * g[j];
-                m = fmaxf(m, fabsf(b[i][j]));
-            }
-            if (a.z) *reinterpret_cast<uint4*>(a.z + t * a.K + 8 * c) = narrow(b[i]);
-        }
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(b[i][j]));
+        if (a.z && i < mine) *reinterpret_cast<uint4*>(a.z + t * a.K + 8 * (i0 + i * G)) = narrow(b[i], kNegate);
     }
     if (!a.q) return;
     m = over_row<G, true>(m, red);
-    if (!live) return;
     const float sc = scale_of(m);
     const Divisor d = divisor_of(sc);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = i0 + i * G;
-        if (c < C) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = cvt_e4m3x2(quotient(b[i][2 * j], d), quotient(b[i][2 * j + 1], d));
-            *reinterpret_cast<uint2*>(a.q + t * a.ldq + 8 * c) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-        }
-    }
-    if (i0 == 0) a.s[t] = sc;
+    for (int i = 0; i < VPT; ++i)
+        if (i < mine) *reinterpret_cast<uint2*>(a.q + t * a.ldq + 8 * (i0 + i * G)) = codes_of_negated(b[i], d);
+    if (i0 == 0 && t < a.T) a.s[t] = sc;
 }
 
-template <int G, int VPT>
-cudaError_t launch(const ResidualNormArgs& a, cudaStream_t st) {
+template <int G, int VPT, bool kTop>
+cudaError_t launch_as(const ResidualNormArgs& a, cudaStream_t st) {
     constexpr int B = G > kBlock ? G : kBlock;
     constexpr int ROWS = B / G;
     cudaLaunchConfig_t cfg = {};
@@ -192,17 +230,33 @@ cudaError_t launch(const ResidualNormArgs& a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, residual_norm<G, VPT>, a);
+    return cudaLaunchKernelEx(&cfg, residual_norm<G, VPT, kTop>, a);
 }
+
+template <int G, int VPT>
+cudaError_t launch(const ResidualNormArgs& a, cudaStream_t st) {
+    return a.k > 0 ? launch_as<G, VPT, true>(a, st) : launch_as<G, VPT, false>(a, st);
+}
+
+// Chunks of all tokens up to which a thread has one (its serial work is the
+// call's latency); beyond, two.
+constexpr int64_t kFewChunks = 152 * 1024;
 
 }  // namespace
 
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, cudaStream_t st) {
     const int64_t C = a.K / 8;
-    if (C <= 32) return launch<32, 1>(a, st);
-    if (C <= 64) return launch<64, 1>(a, st);
-    if (C <= 128) return launch<128, 1>(a, st);
-    if (C <= 256) return launch<256, 1>(a, st);
+    if (a.T * C <= kFewChunks) {
+        if (C <= 32) return launch<32, 1>(a, st);
+        if (C <= 64) return launch<64, 1>(a, st);
+        if (C <= 128) return launch<128, 1>(a, st);
+        if (C <= 256) return launch<256, 1>(a, st);
+        if (C <= 512) return launch<512, 1>(a, st);
+        if (C <= 1024) return launch<1024, 1>(a, st);
+    }
+    if (C <= 64) return launch<32, 2>(a, st);
+    if (C <= 128) return launch<64, 2>(a, st);
+    if (C <= 256) return launch<128, 2>(a, st);
     if (C <= 512) return launch<256, 2>(a, st);
     if (C <= 1024) return launch<512, 2>(a, st);
     if (C <= 2048) return launch<1024, 2>(a, st);
