@@ -43,8 +43,8 @@ namespace {
 constexpr int kThreads = 192;
 constexpr int kTileRows = 128;        // rows a CTA
 constexpr int BN = 256;           // accumulator columns
-constexpr int kHalf = 128;        // weight rows of a TMA box
-constexpr int kBoxRows = 32;      // rows of X of a TMA box
+constexpr int kHalf = 128;        // weight rows of a TMA box (of a small tile's: kHalf / 2)
+constexpr int kBoxRows = 32;      // rows of X of a TMA box, where there are fewer than a CTA's tile has
 constexpr int BKS = 128;          // bytes of K of a swizzled column
 constexpr int KSTEP = 32;         // K of one tcgen05.mma kind::f8f6f4
 constexpr int kAccBufs = 2;
@@ -164,6 +164,11 @@ struct Args {
     unsigned* status;
 };
 
+// X in boxes of a CTA's rows and of kBoxRows, W in boxes of kHalf and kHalf / 2 rows.
+struct Maps {
+    CUtensorMap x, x_few, w, w_small;
+};
+
 struct Bounds {
     int begin, end;
 };
@@ -208,7 +213,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 template <bool kPair, bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
-    gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Args a) {
+    gemm_grouped_kernel(const __grid_constant__ Maps maps, const Args a) {
     using C = Cfg<kPair>;
     using B = Bars<C::STAGES>;
     constexpr int kOut = kGated ? BN / 2 : BN;  // outputs of a tile's row
@@ -243,8 +248,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tmX);
-        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&maps.x);
+        tma_prefetch_desc(&maps.x_few);
+        tma_prefetch_desc(&maps.w);
+        if constexpr (kPair) tma_prefetch_desc(&maps.w_small);
     }
     if (warp == 1) {
         if constexpr (kPair) {
@@ -296,44 +303,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && walk.advance()) {
             const Place p = find.at<C::BM>(a, bars->first, walk.tile);
-            const int mine = min(max(p.rows - rank * kTileRows, 0), kTileRows);
-            const int boxes = (mine + kBoxRows - 1) / kBoxRows;
-            // weight rows: with a gate the gate's and the values', else two halves of
-            // which the second may not be there
-            const int n0 = p.n_blk * kOut;
-            const int w0 = p.e * a.N + n0, w1 = kGated ? w0 + F : w0 + kHalf;
-            const bool two = kGated || n0 + kHalf < a.N;
-            uint32_t bytes;  // that the stage's barrier waits for
-            if constexpr (kPair) {
-                const int all = min(p.rows, kTileRows) + kBoxRows - 1, other = max(min(p.rows - kTileRows, kTileRows), 0) + kBoxRows - 1;
-                bytes = (all / kBoxRows + other / kBoxRows) * kBoxRows * C::BK + (two ? 2 : 1) * kHalf * C::BK;
+            const bool small = kPair && p.rows <= kTileRows;
+            const int cta_rows = small ? kTileRows / 2 : kTileRows;
+            // rows of X in boxes of 32, or all 128 in one
+            auto boxes_of = [&](int cta) {
+                return (min(max(p.rows - cta * cta_rows, 0), cta_rows) + kBoxRows - 1) / kBoxRows;
+            };
+            const int boxes = boxes_of(rank);
+            const bool one_box = boxes == kTileRows / kBoxRows;
+            const int row = p.row0 + rank * cta_rows;
+            // weight rows, halves of the tile's columns: with a gate the gate's and the values', or
+            // 128 and 128; in a small tile both CTAs have 64 of each half.  A half or a quarter that
+            // is beyond the expert's rows is left out.
+            const int n0 = p.n_blk * kOut, left = F - n0;
+            const int w_first = p.e * a.N + n0, w_second = w_first + (kGated ? F : kHalf);
+            const bool second = kGated || left > kHalf;
+            constexpr int kQuarter = kHalf / 2;
+            // (a small tile's CTA: with a gate 64 of the gate and the 64 values that go with them, else
+            // the two quarters of a half)
+            const bool far = kGated ? left > kQuarter : second;  // the odd CTA has weight rows
+            const int s0 = kGated ? w_first + rank * kQuarter : rank ? w_second : w_first;
+            const int s1 = kGated ? w_second + rank * kQuarter : s0 + kQuarter;
+            const bool s1_there = kGated || left > rank * kHalf + kQuarter;
+            uint32_t bytes;  // of K, that the stage's barrier waits for
+            if (small) {
+                const int near_boxes = kGated || left > kQuarter ? 2 : 1;
+                const int far_boxes = !far ? 0 : kGated || left > kHalf + kQuarter ? 2 : 1;
+                bytes = (boxes_of(0) + boxes_of(1)) * kBoxRows + (near_boxes + far_boxes) * kQuarter;
             } else {
-                bytes = boxes * kBoxRows * C::BK + (two ? 2 : 1) * kHalf * C::BK;
+                bytes = (kPair ? boxes_of(0) + boxes_of(1) : boxes) * kBoxRows + (second ? 2 : 1) * kHalf;
             }
             for (int kb = walk.kb0; kb < walk.kb1; ++kb) {
                 if (!(ok = warp_wait(&bars->empty[stage], phase ^ 1u, abort_flag, a.status))) break;
                 if (lane == 0) {
                     uint8_t* xa = sA + stage * C::A_TILE;
                     uint8_t* wb = sB + stage * C::B_TILE;
-                    const int row = p.row0 + rank * kTileRows;
-                    if (leader) mbar_arrive_expect_tx(&bars->full[stage], bytes);
-                    if constexpr (kPair) {
-                        const uint32_t full0 = map_to_rank(smem_u32(&bars->full[stage]), 0);
+                    const int columns = min(C::COLUMNS, (a.K - kb * C::BK + BKS - 1) / BKS);
+                    if (leader) mbar_arrive_expect_tx(&bars->full[stage], bytes * BKS * columns);
+                    const uint32_t full0 = kPair ? map_to_rank(smem_u32(&bars->full[stage]), 0) : 0u;
+                    auto load = [&](uint8_t* to, const CUtensorMap* map, int k, int r) {
+                        if constexpr (kPair) tma_load_2d_pair(to, map, full0, k, r);
+                        else tma_load_2d(to, map, &bars->full[stage], k, r);
+                    };
 #pragma unroll
-                        for (int j = 0; j < C::COLUMNS; ++j) {
-                            const int k = kb * C::BK + j * BKS;
-                            if (rank == 0 || two)
-                                tma_load_2d_pair(wb + j * C::B_COLUMN, &tmW, full0, k, rank ? w1 : w0);
-                            for (int i = 0; i < boxes; ++i)
-                                tma_load_2d_pair(xa + j * C::A_COLUMN + i * kBoxRows * BKS, &tmX, full0, k,
-                                                 row + i * kBoxRows);
+                    for (int c = 0; c < C::COLUMNS; ++c) {
+                        if (c >= columns) break;
+                        const int k = kb * C::BK + c * BKS;
+                        uint8_t* w = wb + c * C::B_COLUMN;
+                        uint8_t* x = xa + c * C::A_COLUMN;
+                        if (small) {
+                            if (rank == 0 || far) {
+                                load(w, &maps.w_small, k, s0);
+                                if (s1_there) load(w + kQuarter * BKS, &maps.w_small, k, s1);
+                            }
+                        } else if (kPair) {
+                            if (rank == 0 || second) load(w, &maps.w, k, rank ? w_second : w_first);
+                        } else {
+                            load(w, &maps.w, k, w_first);
+                            if (second) load(w + kHalf * BKS, &maps.w, k, w_second);
                         }
-                    } else {
-                        const int k = kb * C::BK;
-                        tma_load_2d(wb, &tmW, &bars->full[stage], k, w0);
-                        if (two) tma_load_2d(wb + kHalf * BKS, &tmW, &bars->full[stage], k, w1);
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(xa + i * kBoxRows * BKS, &tmX, &bars->full[stage], k, row + i * kBoxRows);
+                        if (one_box) load(x, &maps.x, k, row);
+                        else
+                            for (int i = 0; i < boxes; ++i) load(x + i * kBoxRows * BKS, &maps.x_few, k, row + i * kBoxRows);
                     }
                 }
                 __syncwarp();
@@ -352,11 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (leader) {
             // ---- MMAs ----
-            constexpr uint32_t idesc = idesc_e4m3_f32(C::BM, BN);
             uint32_t stage = 0, phase = 0;
             bool ok = true;
             int local = 0;
             while (ok && walk.advance()) {
+                const bool small = kPair && find.at<C::BM>(a, bars->first, walk.tile).rows <= kTileRows;
+                const uint32_t idesc =
+                    uniform(small ? idesc_e4m3_f32(kTileRows, BN) : idesc_e4m3_f32(C::BM, BN));
                 const int buf = local % kAccBufs;
                 const uint32_t acc_phase = (local / kAccBufs) & 1;
                 ++local;
@@ -369,15 +402,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t xa = uniform(smem_u32(sA + stage * C::A_TILE));
                     const uint32_t wb = uniform(smem_u32(sB + stage * C::B_TILE));
                     const uint32_t more = uniform(kb != walk.kb0);
+                    const int steps = (a.K - kb * C::BK + KSTEP - 1) / KSTEP;  // (the last stage may have fewer)
                     if (elect_one()) {
                         const uint64_t a0 = sdesc_kmajor_sw128(xa), b0 = sdesc_kmajor_sw128(wb);
-#pragma unroll
-                        for (int kk = 0; kk < C::BK / KSTEP; ++kk) {
+                        auto mma = [&](int kk) {
                             const int j = kk / (BKS / KSTEP), w = kk % (BKS / KSTEP);
                             const uint64_t ad = a0 + ((j * C::A_COLUMN) >> 4) + 2 * w;
                             const uint64_t bd = b0 + ((j * C::B_COLUMN) >> 4) + 2 * w;
                             if constexpr (kPair) mma_f8_pair(d, ad, bd, idesc, kk ? 1u : more);
                             else mma_f8(d, ad, bd, idesc, kk ? 1u : more);
+                        };
+                        if (steps >= C::BK / KSTEP) {
+#pragma unroll
+                            for (int kk = 0; kk < C::BK / KSTEP; ++kk) mma(kk);
+                        } else {
+                            for (int kk = 0; kk < steps; ++kk) mma(kk);
                         }
                         if constexpr (kPair) mma_commit_pair(&bars->empty[stage], 0x3);
                         else mma_commit(&bars->empty[stage]);
@@ -414,8 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int buf = local % kAccBufs;
             const uint32_t acc_phase = (local / kAccBufs) & 1;
             ++local;
-            const int first_row = rank * kTileRows + quarter * 32;  // of the warp, within the tile
-            const int cta_rows = min(p.rows - rank * kTileRows, kTileRows);
+            // A small tile (M = 128 over the pair): 64 rows a CTA, lanes 0 .. 63 with the first half
+            // of the columns, lanes 64 .. 127 with the second.
+            const bool small = kPair && p.rows <= kTileRows;
+            const int cta_row0 = rank * (small ? kTileRows / 2 : kTileRows);
+            const int first_row = cta_row0 + (small ? quarter & 1 : quarter) * 32;  // of the warp, within the tile
+            const int cta_rows = min(p.rows - cta_row0, small ? kTileRows / 2 : kTileRows);
+            const int column0 = small ? (quarter >> 1) * (kOut / 2) : 0;  // of the warp's outputs
+            const int chunks = (small ? kOut / 2 : kOut) / 32;
+            const int up = small ? kOut / 2 : kOut;  // columns from a gate to its value in tensor memory
             const bool any = first_row < p.rows, whole = walk.kb0 == 0 && walk.kb1 == nk;
             const bool row_ok = first_row + lane < p.rows;
             const int64_t row = static_cast<int64_t>(p.row0) + first_row + lane;
@@ -455,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t packed[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-                const int n = n0 + 32 * c;
+                const int n = n0 + column0 + 32 * c;
                 if (wide) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -473,7 +519,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 32; ++j)
                     if (n + j < F) o[j] = static_cast<uint16_t>(packed[j >> 1] >> ((j & 1) * 16));
             };
-            auto scaled = [&](float acc, int c) { return (acc * st) * sw[c]; };
             // (a quotient that is rounded to 2^-22 and takes the same time for every value: rows that
             // are not there hold anything, and a true division of NaN takes 50 times as long)
             auto gated = [&](float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; };
@@ -493,20 +538,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             if (whole) {
+                const float* sg = sw + column0;
                 if constexpr (kGated) {
+                    const float* su = sg + kOut;
 #pragma unroll
                     for (int c = 0; c < kOut / 32; ++c) {
+                        if (c >= chunks) break;
                         uint32_t g[32], u[32];
                         tmem_ld_32x32b_x32(acc + 32 * c, g);
-                        tmem_ld_32x32b_x32(acc + kOut + 32 * c, u);
+                        tmem_ld_32x32b_x32(acc + up + 32 * c, u);
                         tmem_ld_wait_regs(g);
                         tmem_ld_wait_regs(u);
-                        if (c == kOut / 32 - 1) release();
+                        if (c == chunks - 1) release();
                         float v[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            v[j] = gated(scaled(__uint_as_float(g[j]), 32 * c + j),
-                                         scaled(__uint_as_float(u[j]), kOut + 32 * c + j));
+                            v[j] = gated((__uint_as_float(g[j]) * st) * sg[32 * c + j],
+                                         (__uint_as_float(u[j]) * st) * su[32 * c + j]);
                         emit(v, c);
                     }
                 } else {
@@ -515,20 +563,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     auto one = [&](const uint32_t (&r)[32], int c) {
                         float v[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = scaled(__uint_as_float(r[j]), 32 * c + j);
+                        for (int j = 0; j < 32; ++j) v[j] = (__uint_as_float(r[j]) * st) * sg[32 * c + j];
                         emit(v, c);
                     };
                     tmem_ld_32x32b_x32(acc, ra);
                     tmem_ld_wait_regs(ra);
 #pragma unroll
                     for (int c = 0; c < BN / 32; c += 2) {
+                        if (c >= chunks) break;
                         tmem_ld_32x32b_x32(acc + (c + 1) * 32, rb);
                         one(ra, c);
                         tmem_ld_wait_regs(rb);
-                        if (c + 2 < BN / 32) tmem_ld_32x32b_x32(acc + (c + 2) * 32, ra);
+                        if (c + 2 < chunks) tmem_ld_32x32b_x32(acc + (c + 2) * 32, ra);
                         else release();
                         one(rb, c + 1);
-                        if (c + 2 < BN / 32) tmem_ld_wait_regs(ra);
+                        if (c + 2 < chunks) tmem_ld_wait_regs(ra);
                     }
                 }
                 __syncwarp();
@@ -539,15 +588,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return a.parts + ((static_cast<int64_t>(w) * C::CTAS + rank) * 2 + slot) * a.slot;
             };
             if (any) {
-                float* mine = part(worker, walk.kb0 == 0 ? 1 : 0) + quarter * 32 * BN;
+                float* mine = part(worker, walk.kb0 == 0 ? 1 : 0) + (first_row - cta_row0) * BN;
 #pragma unroll
                 for (int c = 0; c < BN / 32; ++c) {
+                    if (small && c >= BN / 64) break;
+                    // (columns as in a tile of all rows: the gate's, then the values')
+                    const int column = !small ? 32 * c
+                                       : kGated ? column0 + 32 * (c & 1) + (c >> 1) * kOut
+                                                : column0 + 32 * c;
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(acc + 32 * c, r);
                     tmem_ld_wait_regs(r);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) piece(j) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                    flush(mine + 32 * c, BN * 4, 128);
+                    flush(mine + column, BN * 4, 128);
                 }
             }
             release();
@@ -576,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float4 sl = reinterpret_cast<const float4*>(sw)[lane], sh = reinterpret_cast<const float4*>(sw)[32 + lane];
             const int64_t step = a.slot * 2 * C::CTAS;
             auto put = [&](const float (&q)[4], int r, int n) {
-                __nv_bfloat16* out = a.y + (static_cast<int64_t>(p.row0) + rank * kTileRows + r) * F + n;
+                __nv_bfloat16* out = a.y + (static_cast<int64_t>(p.row0) + cta_row0 + r) * F + n;
                 if (wide) {
                     if (n < F)
                         *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(q[0], q[1]), pack_bf16x2(q[2], q[3]));
@@ -610,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     if (r0 + i >= cta_rows) break;
-                    const float t = a.s_tok[p.row0 + rank * kTileRows + r0 + i];
+                    const float t = a.s_tok[p.row0 + cta_row0 + r0 + i];
                     float v[4] = {(lo[i].x * t) * sl.x, (lo[i].y * t) * sl.y, (lo[i].z * t) * sl.z, (lo[i].w * t) * sl.w};
                     float u[4] = {(hi[i].x * t) * sh.x, (hi[i].y * t) * sh.y, (hi[i].z * t) * sh.z, (hi[i].w * t) * sh.w};
                     if constexpr (kGated) {
@@ -660,9 +714,13 @@ bool pairs_of(int64_t E, int64_t R) { return R > kTileRows * E; }
 template <bool kPair, bool kGated>
 cudaError_t launch(const GroupedArgs& g, const Args& a, cudaStream_t st) {
     using C = Cfg<kPair>;
-    CUtensorMap tmX, tmW;
-    if (!encode_tmap_u8(&tmX, g.xq, g.R, g.K, g.K, BKS, kBoxRows)) return cudaErrorInvalidValue;
-    if (!encode_tmap_u8(&tmW, g.wq, static_cast<uint64_t>(g.E) * g.N, g.K, g.K, BKS, kHalf)) return cudaErrorInvalidValue;
+    Maps maps;
+    const uint64_t w_rows = static_cast<uint64_t>(g.E) * g.N;
+    if (!encode_tmap_u8(&maps.x, g.xq, g.R, g.K, g.K, BKS, kTileRows) ||
+        !encode_tmap_u8(&maps.x_few, g.xq, g.R, g.K, g.K, BKS, kBoxRows) ||
+        !encode_tmap_u8(&maps.w, g.wq, w_rows, g.K, g.K, BKS, kHalf) ||
+        !encode_tmap_u8(&maps.w_small, g.wq, w_rows, g.K, g.K, BKS, kHalf / 2))
+        return cudaErrorInvalidValue;
     int ctas = g.num_sms < kMaxCtas ? g.num_sms : kMaxCtas;
     if (kPair && g.pair_clusters > 0 && 2 * g.pair_clusters < ctas) ctas = 2 * g.pair_clusters;
     cudaLaunchConfig_t cfg = {};
@@ -679,7 +737,7 @@ cudaError_t launch(const GroupedArgs& g, const Args& a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kPair ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemm_grouped_kernel<kPair, kGated>, tmX, tmW, a);
+    return cudaLaunchKernelEx(&cfg, gemm_grouped_kernel<kPair, kGated>, maps, a);
 }
 
 }  // namespace
