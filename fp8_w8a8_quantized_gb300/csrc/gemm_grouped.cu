@@ -44,8 +44,8 @@ constexpr int kThreads = 192;
 constexpr int kTileRows = 128;        // rows a CTA
 constexpr int BN = 256;           // accumulator columns
 constexpr int kHalf = 128;        // weight rows of a TMA box (of a small tile's: kHalf / 2)
-constexpr int kBoxRows = 32;      // rows of X of a TMA box, where there are fewer than a CTA's tile has
-constexpr int BKS = 128;          // bytes of K of a swizzled column
+constexpr int kMinBox = 32;       // rows of X of the smallest of three TMA boxes (32, 64, 128)
+constexpr int BK = 128;           // K of a stage: one swizzled column of 128 bytes
 constexpr int KSTEP = 32;         // K of one tcgen05.mma kind::f8f6f4
 constexpr int kAccBufs = 2;
 constexpr uint32_t TMEM_COLS = kAccBufs * BN;
@@ -58,14 +58,10 @@ template <bool kPair>
 struct Cfg {
     static constexpr int CTAS = kPair ? 2 : 1;
     static constexpr int BM = kTileRows * CTAS;
-    static constexpr int BK = kPair ? 256 : 128;  // K of a stage
-    static constexpr int COLUMNS = BK / BKS;
-    static constexpr int STAGES = kPair ? 3 : 4;
+    static constexpr int STAGES = kPair ? 6 : 4;
     static constexpr int B_ROWS = BN / CTAS;      // weight rows in this CTA
-    static constexpr uint32_t A_COLUMN = kTileRows * BKS;
-    static constexpr uint32_t B_COLUMN = B_ROWS * BKS;
-    static constexpr uint32_t A_TILE = A_COLUMN * COLUMNS;
-    static constexpr uint32_t B_TILE = B_COLUMN * COLUMNS;
+    static constexpr uint32_t A_TILE = kTileRows * BK;
+    static constexpr uint32_t B_TILE = B_ROWS * BK;
     static constexpr uint32_t RING = STAGES * (A_TILE + B_TILE);
 };
 
@@ -164,9 +160,9 @@ struct Args {
     unsigned* status;
 };
 
-// X in boxes of a CTA's rows and of kBoxRows, W in boxes of kHalf and kHalf / 2 rows.
+// X in boxes of 32, 64 and 128 rows, W in boxes of kHalf and kHalf / 2 rows.
 struct Maps {
-    CUtensorMap x, x_few, w, w_small;
+    CUtensorMap x[3], w, w_small;
 };
 
 struct Bounds {
@@ -230,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = rank == 0;
     const int worker = blockIdx.x / C::CTAS, workers = gridDim.x / C::CTAS;
     const int F = kGated ? a.N / 2 : a.N;
-    const int nk = (a.K + C::BK - 1) / C::BK;
+    const int nk = (a.K + BK - 1) / BK;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -248,8 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&maps.x);
-        tma_prefetch_desc(&maps.x_few);
+        for (int i = 0; i < 3; ++i) tma_prefetch_desc(&maps.x[i]);
         tma_prefetch_desc(&maps.w);
         if constexpr (kPair) tma_prefetch_desc(&maps.w_small);
     }
@@ -305,67 +300,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Place p = find.at<C::BM>(a, bars->first, walk.tile);
             const bool small = kPair && p.rows <= kTileRows;
             const int cta_rows = small ? kTileRows / 2 : kTileRows;
-            // rows of X in boxes of 32, or all 128 in one
-            auto boxes_of = [&](int cta) {
-                return (min(max(p.rows - cta * cta_rows, 0), cta_rows) + kBoxRows - 1) / kBoxRows;
+            // rows of X in one box, the smallest that has them (further rows of it are another
+            // expert's: a copy costs the loading warp more than they cost)
+            auto box_of = [&](int cta) {  // 0: no rows
+                const int rows = min(p.rows - cta * cta_rows, cta_rows);
+                return rows <= 0 ? 0 : rows <= kMinBox ? kMinBox : rows <= 2 * kMinBox ? 2 * kMinBox : 4 * kMinBox;
             };
-            const int boxes = boxes_of(rank);
-            const bool one_box = boxes == kTileRows / kBoxRows;
+            const int box = box_of(rank);
+            const CUtensorMap* x_map = maps.x + (box >> 6);  // 32, 64, 128 -> 0, 1, 2
             const int row = p.row0 + rank * cta_rows;
-            // weight rows, halves of the tile's columns: with a gate the gate's and the values', or
-            // 128 and 128; in a small tile both CTAs have 64 of each half.  A half or a quarter that
-            // is beyond the expert's rows is left out.
-            const int n0 = p.n_blk * kOut, left = F - n0;
+            // weight rows, halves of the tile's columns: with a gate the gate's and the values' (in a
+            // small tile both CTAs have 64 of each), or 128 and 128.  A half that is beyond the
+            // expert's rows is left out.
+            const int n0 = p.n_blk * kOut;
             const int w_first = p.e * a.N + n0, w_second = w_first + (kGated ? F : kHalf);
-            const bool second = kGated || left > kHalf;
-            constexpr int kQuarter = kHalf / 2;
-            // (a small tile's CTA: with a gate 64 of the gate and the 64 values that go with them, else
-            // the two quarters of a half)
-            const bool far = kGated ? left > kQuarter : second;  // the odd CTA has weight rows
-            const int s0 = kGated ? w_first + rank * kQuarter : rank ? w_second : w_first;
-            const int s1 = kGated ? w_second + rank * kQuarter : s0 + kQuarter;
-            const bool s1_there = kGated || left > rank * kHalf + kQuarter;
-            uint32_t bytes;  // of K, that the stage's barrier waits for
-            if (small) {
-                const int near_boxes = kGated || left > kQuarter ? 2 : 1;
-                const int far_boxes = !far ? 0 : kGated || left > kHalf + kQuarter ? 2 : 1;
-                bytes = (boxes_of(0) + boxes_of(1)) * kBoxRows + (near_boxes + far_boxes) * kQuarter;
-            } else {
-                bytes = (kPair ? boxes_of(0) + boxes_of(1) : boxes) * kBoxRows + (second ? 2 : 1) * kHalf;
-            }
+            const bool second = kGated || n0 + kHalf < F;
+            const bool quarters = kGated && small;
+            const int w_row = quarters ? w_first + rank * (kHalf / 2) : rank ? w_second : w_first;
+            const bool w_there = rank == 0 || second;
+            // of K, that the stage's barrier waits for
+            const uint32_t bytes = (kPair ? box_of(0) + box_of(1) : box) + (second ? 2 : 1) * kHalf;
+            // (operands of the copies from uniform registers, see elect_one in ptx.cuh)
+            const uint32_t tx = uniform(bytes) * BK;
+            const int x_row = static_cast<int>(uniform(row));
+            const int w_row0 = static_cast<int>(uniform(kPair ? w_row : w_first)), w_row1 = static_cast<int>(uniform(kPair ? w_row + F : w_second));
+            const bool has_x = uniform(box) != 0, has_w = uniform(w_there), both = uniform(kPair ? quarters : second);
             for (int kb = walk.kb0; kb < walk.kb1; ++kb) {
-                if (!(ok = warp_wait(&bars->empty[stage], phase ^ 1u, abort_flag, a.status))) break;
-                if (lane == 0) {
-                    uint8_t* xa = sA + stage * C::A_TILE;
-                    uint8_t* wb = sB + stage * C::B_TILE;
-                    const int columns = min(C::COLUMNS, (a.K - kb * C::BK + BKS - 1) / BKS);
-                    if (leader) mbar_arrive_expect_tx(&bars->full[stage], bytes * BKS * columns);
-                    const uint32_t full0 = kPair ? map_to_rank(smem_u32(&bars->full[stage]), 0) : 0u;
-                    auto load = [&](uint8_t* to, const CUtensorMap* map, int k, int r) {
+                if (!(ok = warp_ready(&bars->empty[stage], phase ^ 1u, abort_flag, a.status))) break;
+                if (elect_one()) {
+                    uint8_t* w = sB + stage * C::B_TILE;
+                    const int k = kb * BK;
+                    uint64_t* full = &bars->full[stage];
+                    const uint32_t full0 = kPair ? map_to_rank(smem_u32(full), 0) : 0u;
+                    auto load = [&](uint8_t* to, const CUtensorMap* map, int r) {
                         if constexpr (kPair) tma_load_2d_pair(to, map, full0, k, r);
-                        else tma_load_2d(to, map, &bars->full[stage], k, r);
+                        else tma_load_2d(to, map, full, k, r);
                     };
-#pragma unroll
-                    for (int c = 0; c < C::COLUMNS; ++c) {
-                        if (c >= columns) break;
-                        const int k = kb * C::BK + c * BKS;
-                        uint8_t* w = wb + c * C::B_COLUMN;
-                        uint8_t* x = xa + c * C::A_COLUMN;
-                        if (small) {
-                            if (rank == 0 || far) {
-                                load(w, &maps.w_small, k, s0);
-                                if (s1_there) load(w + kQuarter * BKS, &maps.w_small, k, s1);
-                            }
-                        } else if (kPair) {
-                            if (rank == 0 || second) load(w, &maps.w, k, rank ? w_second : w_first);
-                        } else {
-                            load(w, &maps.w, k, w_first);
-                            if (second) load(w + kHalf * BKS, &maps.w, k, w_second);
+                    if (leader) mbar_arrive_expect_tx(full, tx);
+                    if constexpr (kPair) {
+                        if (kGated && both) {
+                            load(w, &maps.w_small, w_row0);
+                            load(w + (kHalf / 2) * BK, &maps.w_small, w_row1);
+                        } else if (has_w) {
+                            load(w, &maps.w, w_row0);
                         }
-                        if (one_box) load(x, &maps.x, k, row);
-                        else
-                            for (int i = 0; i < boxes; ++i) load(x + i * kBoxRows * BKS, &maps.x_few, k, row + i * kBoxRows);
+                    } else {
+                        load(w, &maps.w, w_row0);
+                        if (both) load(w + kHalf * BK, &maps.w, w_row1);
                     }
+                    if (has_x) load(sA + stage * C::A_TILE, x_map, x_row);
                 }
                 __syncwarp();
                 ++issued;
@@ -397,24 +380,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t d = uniform(tmem_base + buf * BN);
                 for (int kb = walk.kb0; kb < walk.kb1; ++kb) {
-                    if (!(ok = warp_wait(&bars->full[stage], phase, abort_flag, a.status))) break;
+                    if (!(ok = warp_ready(&bars->full[stage], phase, abort_flag, a.status))) break;
                     tc_fence_after();
                     const uint32_t xa = uniform(smem_u32(sA + stage * C::A_TILE));
                     const uint32_t wb = uniform(smem_u32(sB + stage * C::B_TILE));
                     const uint32_t more = uniform(kb != walk.kb0);
-                    const int steps = (a.K - kb * C::BK + KSTEP - 1) / KSTEP;  // (the last stage may have fewer)
+                    const int steps = (a.K - kb * BK + KSTEP - 1) / KSTEP;  // (the last stage may have fewer)
                     if (elect_one()) {
                         const uint64_t a0 = sdesc_kmajor_sw128(xa), b0 = sdesc_kmajor_sw128(wb);
                         auto mma = [&](int kk) {
-                            const int j = kk / (BKS / KSTEP), w = kk % (BKS / KSTEP);
-                            const uint64_t ad = a0 + ((j * C::A_COLUMN) >> 4) + 2 * w;
-                            const uint64_t bd = b0 + ((j * C::B_COLUMN) >> 4) + 2 * w;
+                            const uint64_t ad = a0 + 2 * kk, bd = b0 + 2 * kk;
                             if constexpr (kPair) mma_f8_pair(d, ad, bd, idesc, kk ? 1u : more);
                             else mma_f8(d, ad, bd, idesc, kk ? 1u : more);
                         };
-                        if (steps >= C::BK / KSTEP) {
+                        if (steps >= BK / KSTEP) {
 #pragma unroll
-                            for (int kk = 0; kk < C::BK / KSTEP; ++kk) mma(kk);
+                            for (int kk = 0; kk < BK / KSTEP; ++kk) mma(kk);
                         } else {
                             for (int kk = 0; kk < steps; ++kk) mma(kk);
                         }
@@ -716,10 +697,11 @@ cudaError_t launch(const GroupedArgs& g, const Args& a, cudaStream_t st) {
     using C = Cfg<kPair>;
     Maps maps;
     const uint64_t w_rows = static_cast<uint64_t>(g.E) * g.N;
-    if (!encode_tmap_u8(&maps.x, g.xq, g.R, g.K, g.K, BKS, kTileRows) ||
-        !encode_tmap_u8(&maps.x_few, g.xq, g.R, g.K, g.K, BKS, kBoxRows) ||
-        !encode_tmap_u8(&maps.w, g.wq, w_rows, g.K, g.K, BKS, kHalf) ||
-        !encode_tmap_u8(&maps.w_small, g.wq, w_rows, g.K, g.K, BKS, kHalf / 2))
+    if (!encode_tmap_u8(&maps.x[0], g.xq, g.R, g.K, g.K, BK, kMinBox) ||
+        !encode_tmap_u8(&maps.x[1], g.xq, g.R, g.K, g.K, BK, 2 * kMinBox) ||
+        !encode_tmap_u8(&maps.x[2], g.xq, g.R, g.K, g.K, BK, 4 * kMinBox) ||
+        !encode_tmap_u8(&maps.w, g.wq, w_rows, g.K, g.K, BK, kHalf) ||
+        !encode_tmap_u8(&maps.w_small, g.wq, w_rows, g.K, g.K, BK, kHalf / 2))
         return cudaErrorInvalidValue;
     int ctas = g.num_sms < kMaxCtas ? g.num_sms : kMaxCtas;
     if (kPair && g.pair_clusters > 0 && 2 * g.pair_clusters < ctas) ctas = 2 * g.pair_clusters;
@@ -783,17 +765,17 @@ cudaError_t launch_gemm_grouped(const GroupedArgs& g, cudaStream_t st) {
         const cudaError_t e = cudaLaunchKernelEx(&cfg, clear_counts, a.count, static_cast<int>(kCounts));
         if (e != cudaSuccess) return e;
     }
-    // Measured: an SM alone streams 75 GB/s of weights (a stage of 128 of K is 32 KB), all
-    // together 6.1 TB/s; a pair's stage of 256 of K takes the tensor cores 0.57 us; a part of
-    // 32 rows is added in 0.9 us, after 3 us for writing it and the counter.
+    // Measured: an SM alone streams 75 GB/s of weights (a stage is 32 KB), all together 6.1 TB/s;
+    // a pair's stage takes the tensor cores 0.3 us; a part of 32 rows is added in 0.9 us, a pair's
+    // in twice that, after 3 us for writing it and the counter.
     const int64_t mean = (static_cast<int64_t>(g.R) + g.E - 1) / g.E;
+    const float batches = static_cast<float>((mean < kTileRows ? mean + 31 : kTileRows) / 32);
     a.costs.fixed = 3.0f;
-    a.costs.part = 0.9f * static_cast<float>((mean < kTileRows ? mean + 31 : kTileRows) / 32);
     if (pairs_of(g.E, g.R)) {
-        a.costs.stage = 0.57f, a.costs.shared = 0.0f;
+        a.costs.stage = 0.3f, a.costs.shared = 0.0f, a.costs.part = 1.8f * batches;
         return g.swiglu ? launch<true, true>(g, a, st) : launch<true, false>(g, a, st);
     }
-    a.costs.stage = 0.44f, a.costs.shared = 0.0054f;
+    a.costs.stage = 0.44f, a.costs.shared = 0.0054f, a.costs.part = 0.9f * batches;
     return g.swiglu ? launch<false, true>(g, a, st) : launch<false, false>(g, a, st);
 }
 
