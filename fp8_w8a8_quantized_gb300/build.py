@@ -30,7 +30,8 @@ LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 SOURCES = ["api.cu", "quant.cu", "quant_variants.cu", "norm_quant.cu", "gemm_pair.cu", "gemm_decode.cu", "gemm_blockwise.cu", "noalloc.cu",
            "selftest.cu", "attention_api.cu", "kv_slots.cu", "norm_rope.cu", "attention_prompt.cu", "attention_decode.cu",
            "attention_prefix.cu", "experts_api.cu", "moe_route.cu", "gemm_grouped.cu", "residual_norm.cu"]
-HEADERS = ["ptx.cuh", "launch.h", "quant_math.cuh", "decode_common.cuh", "attention_plan.h", "attention_tile.cuh"]
+HEADERS = ["ptx.cuh", "launch.h", "quant_math.cuh", "decode_common.cuh", "attention_plan.h", "attention_tile.cuh",
+           "grouped_plan.h"]
 
 # The binding's extension modules (host code only; they link the library and torch).
 MODULES = ["attention_binding", "experts_binding"]

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxLd = int64_t(1) << 38;  // elements between two rows
+constexpr int64_t kMost = int64_t(1) << 30;   // rows and widths that the kernels count in 32 bits
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxTop = 32;
 constexpr int64_t kMaxNormWidth = 32768;
@@ -42,7 +43,8 @@ fp8_status_t check_rows(const void* p, int64_t ld, int64_t K) {
 
 fp8_status_t check_grouped_sizes(int64_t E, int64_t R, int64_t N, int64_t K, bool swiglu) {
     if (any_out({E, R, N, K}) || E < 1 || (swiglu && N % 2)) return FP8_ERR_INVALID_ARG;
-    if (K == 0 || K % 16 || E > kMaxExperts || N > kMax31 / E) return FP8_ERR_UNSUPPORTED;
+    if (K == 0 || K % 16 || E > kMaxExperts || N > kMost / E || K > kMost || R > kMost)
+        return FP8_ERR_UNSUPPORTED;
     return FP8_OK;
 }
 
@@ -81,7 +83,7 @@ extern "C" {
 
 size_t fp8_moe_route_workspace_size(int64_t T, int64_t E, int64_t top_k) {
     if (T < 0 || E < 1 || E > kMaxExperts || top_k < 1 || top_k > E || top_k > kMaxTop ||
-        T > kMax31 / top_k)
+        T > kMost / top_k)
         return 0;
     return fp8k::moe_route_workspace(T, E, top_k);
 }
@@ -92,7 +94,7 @@ fp8_status_t fp8_moe_route(const void* logits, int logits_fp32, int64_t ld, int6
                            int32_t* token_row, void* workspace, size_t ws_bytes, void* stream) {
     if (any_out({T, E, top_k}) || top_k < 1 || top_k > E || !std::isfinite(scale))
         return FP8_ERR_INVALID_ARG;
-    if (E > kMaxExperts || top_k > kMaxTop || T > kMax31 / top_k) return FP8_ERR_UNSUPPORTED;
+    if (E > kMaxExperts || top_k > kMaxTop || T > kMost / top_k) return FP8_ERR_UNSUPPORTED;
     if (!offsets || (T > 0 && (!logits || !expert_ids || !weights || !row_token || !token_row)))
         return FP8_ERR_INVALID_ARG;
     if (T > 0 && (ld < E || ld > kMaxLd)) return FP8_ERR_INVALID_ARG;

@@ -126,7 +126,7 @@ struct Lane<32> : Wide<32> {
 struct Route {
     const void* logits;
     int64_t ld;
-    int T, E, k;  // (T * k < 2^31)
+    int T, E, k;  // (T * k <= 2^30)
     bool renorm;
     float scale;
     int32_t* ids;

@@ -391,6 +391,25 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
                  : "memory");
 }
 
+// The same for kernels that come in both forms: columns for this CTA or for the
+// pair (the last allocation of the CTA), and their return.
+template <bool kPair>
+__device__ __forceinline__ void tmem_take(uint32_t* dst, uint32_t ncols) {
+    if constexpr (kPair) {
+        tmem_alloc_pair(dst, ncols);
+        tmem_relinquish_pair();
+    } else {
+        tmem_alloc(dst, ncols);
+        tmem_relinquish();
+    }
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_give_back(uint32_t taddr, uint32_t ncols) {
+    if constexpr (kPair) tmem_dealloc_pair(taddr, ncols);
+    else tmem_dealloc(taddr, ncols);
+}
+
 // D[tmem of both CTAs] (+)= A * B^T with M = 256: rows 0-127 of A (and of D)
 // in the even CTA, 128-255 in the odd one; the N columns of B are split in
 // halves between the two CTAs' shared memory at the same offsets.  Issued by

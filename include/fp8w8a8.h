@@ -539,7 +539,8 @@ FP8_API size_t fp8_attention_decode_workspace_size(int64_t B, int64_t Hq, int64_
  *   the pairs (t, j) sorted by expert, by token within one, are the rows:
  *   row_token[r] = t of row r,  token_row[t, j] = r,
  *   offsets[e] = rows of the experts below e.
- * A logit of -infinity or NaN switches its expert off for the token.  Where
+ * A logit of -infinity or NaN switches its expert off for the token (one of
+ * +infinity gives NaN weights, as the formula does).  Where
  * fewer than top_k are left, the rest has expert -1, weight 0 and row -1 (a
  * token of padding whose logits are all -infinity makes no rows); row_token is
  * -1 from offsets[E] on.
@@ -553,7 +554,7 @@ FP8_API size_t fp8_attention_decode_workspace_size(int64_t B, int64_t Hq, int64_
  *   workspace  [device]       fp8_moe_route_workspace_size() bytes, 16-byte
  *                             aligned; need not start at zero; not in use by
  *                             another call in flight
- * Requirements: 1 <= top_k <= E <= 1024, top_k <= 32; T * top_k < 2^31; scale
+ * Requirements: 1 <= top_k <= E <= 1024, top_k <= 32; T * top_k <= 2^30; scale
  * finite; pointers aligned to their elements.  With T == 0 only offsets is
  * written.
  */
@@ -584,7 +585,7 @@ FP8_API size_t fp8_moe_route_workspace_size(int64_t T, int64_t E, int64_t top_k)
  *                        aligned; need not start at zero; not in use by
  *                        another call in flight.  NULL if that is 0.
  * Requirements: K % 16 == 0, K > 0; with swiglu N % 2 == 0; 1 <= E <= 1024;
- * xq, wq and y 16-byte aligned; R, K, E * N < 2^31.  The order of each sum is
+ * xq, wq and y 16-byte aligned; R, K, E * N <= 2^30.  The order of each sum is
  * fixed by the sizes and offsets: repeated calls give identical bits.
  */
 FP8_API fp8_status_t fp8_grouped_gemm(const uint8_t* xq, const float* s_tok, const uint8_t* wq,

@@ -180,6 +180,48 @@ def test_grouped_rows_outside_stay_as_they_are(swiglu):
     check_grouped([200, 100], 512, 4096, swiglu, start=1, extra=300)
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("N", [2, 62, 64, 66, 126, 128, 130, 200, 254, 258, 384, 642])
+def test_grouped_many_rows_of_few_outputs(N, swiglu):
+    # tiles over two SMs; experts that end in each part of a tile
+    check_grouped([400, 130, 20, 256, 0, 385], N, 400, swiglu)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("K", [16, 32, 112, 128, 144, 272, 1008, 4112])
+def test_grouped_many_rows_of_any_depth(K, swiglu):
+    check_grouped([290, 129, 128, 511], 288, K, swiglu)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_grouped_cut_tiles_of_many_rows(swiglu):
+    # one round of few tiles with long sums: cut, each part of up to 256 rows
+    check_grouped([256], 256, 32768, swiglu)
+    check_grouped([700, 140, 20], 320, 16384 + 48, swiglu)
+
+
+def test_grouped_workspace_need_not_be_clean():
+    g = gen(21)
+    wq, s_w = weights(g, 4, 256, 8192)
+    xq = torch.randint(0, 120, (70, 8192), generator=g, device=DEV, dtype=torch.uint8)
+    s = torch.ones(70, device=DEV) * 1e-4
+    x = normal(g, 70, 8192)
+    w8 = wq.view(torch.uint8)
+    need = max(fp8.fp8_grouped_gemm_workspace_size(4, 70, 256, 8192), fp8.fp8_grouped_linear_workspace_size(4, 70, 256, 8192))
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    for counts in ([70, 0, 0, 0], [1, 2, 3, 64], [30, 30, 5, 5]):
+        off = bounds(counts)
+        good = fp8.fp8_grouped_gemm(xq, s, w8, s_w, off), fp8.fp8_grouped_linear(x, w8, s_w, off)
+        for fill in (0, 255, 1):
+            ws.fill_(fill)
+            assert torch.equal(fp8.fp8_grouped_gemm(xq, s, w8, s_w, off, workspace=ws), good[0])
+            assert torch.equal(fp8.fp8_grouped_gemm(xq, s, w8, s_w, off, workspace=ws), good[0])
+            ws.fill_(fill)
+            assert torch.equal(fp8.fp8_grouped_linear(x, w8, s_w, off, workspace=ws), good[1])
+            assert torch.equal(fp8.fp8_grouped_linear(x, w8, s_w, off, workspace=ws), good[1])
+    clean()
+
+
 def test_grouped_many_experts():
     counts = [(7 * i) % 5 for i in range(1024)]
     check_grouped(counts, 48, 64, False)
