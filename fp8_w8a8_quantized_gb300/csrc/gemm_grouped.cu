@@ -26,8 +26,8 @@
 // tile's workers to arrive (a counter, zeroed by the kernel before) adds the parts in the order of K: the order of every sum is fixed by
 // the sizes and bounds.  No worker waits for another.
 //
-// Per CTA 192 threads: warp 0 loads (TMA), warp 1 issues the MMAs (in a pair the
-// even CTA's), warps 2 to 5 scale, round and store.
+// Per CTA 320 threads: warp 0 loads (TMA), warp 1 issues the MMAs (in a pair the
+// even CTA's), warps 2 to 9 scale, round and store.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -44,7 +44,8 @@ namespace {
 using grouped::Costs;
 using grouped::Walk;
 
-constexpr int kThreads = 192;
+constexpr int kOutWarps = 8;      // two for each 32 rows of a CTA's tile
+constexpr int kThreads = 64 + 32 * kOutWarps;
 constexpr int kTileRows = 128;        // rows a CTA
 constexpr int BN = 256;           // accumulator columns
 constexpr int kHalf = 128;        // weight rows of a TMA box (of a small tile's: kHalf / 2)
@@ -55,8 +56,7 @@ constexpr int kAccBufs = 2;
 constexpr uint32_t TMEM_COLS = kAccBufs * BN;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxCtas = 152;
-constexpr int kQuarters = 4;      // epilogue warps: 32 rows each
-constexpr int kBatch = 8;         // rows whose parts are added at a time
+constexpr int kBatch = 4;         // rows whose parts are added at a time
 
 template <bool kPair>
 struct Cfg {
@@ -81,8 +81,8 @@ struct Bars {
     uint32_t tmem_base;
     int abort;
     int last;                      // this CTA is the last of the tile's to arrive
-    alignas(16) float s_w[kQuarters][BN];         // a tile's weight scales, each epilogue warp's own copy
-    alignas(16) uint4 out[kQuarters][32 * 8];      // 32 rows x 64 outputs on their way out
+    alignas(16) float s_w[kOutWarps][BN / 2];     // weight scales of the warp's columns
+    alignas(16) uint4 out[kOutWarps][32 * 4];     // 32 rows x 64 bytes on their way out
     int first[kMaxExperts + 1];    // tiles of the experts below
 };
 
@@ -179,10 +179,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < kAccBufs; ++b) {
             mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], kQuarters * C::CTAS);
+            mbar_init(&bars->acc_empty[b], kOutWarps * C::CTAS);
         }
         mbar_init(&bars->drain, 1);
-        mbar_init(&bars->part_done, kQuarters);
+        mbar_init(&bars->part_done, kOutWarps);
         mbar_init(&bars->verdict, 1);
         bars->abort = 0;
         fence_mbar_init();
@@ -359,9 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else {
-        // ---- outputs: 32 of this CTA's 128 rows a warp ----
-        const int quarter = warp & 3;
-        float* sw = bars->s_w[quarter];
+        // ---- outputs: a warp has 32 of this CTA's 128 rows and half of the columns ----
+        const int me = warp - 2, quarter = warp & 3, half = me >> 2;
+        float* sw = bars->s_w[me];
+        uint4* stage = bars->out[me];
         const bool wide = F % 8 == 0;  // rows of y at 16-byte boundaries
         int local = 0;
         uint32_t part_phase = 0;
@@ -376,57 +377,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int cta_row0 = rank * (small ? kTileRows / 2 : kTileRows);
             const int first_row = cta_row0 + (small ? quarter & 1 : quarter) * 32;  // of the warp, within the tile
             const int cta_rows = min(p.rows - cta_row0, small ? kTileRows / 2 : kTileRows);
-            const int column0 = small ? (quarter >> 1) * (kOut / 2) : 0;  // of the warp's outputs
-            const int chunks = (small ? kOut / 2 : kOut) / 32;
-            const int up = small ? kOut / 2 : kOut;  // columns from a gate to its value in tensor memory
-            const bool any = first_row < p.rows, whole = walk.kb0 == 0 && walk.kb1 == nk;
-            const bool row_ok = first_row + lane < p.rows;
+            const int here = min(32, p.rows - first_row);
+            const bool any = here > 0, whole = walk.kb0 == 0 && walk.kb1 == nk;
+            const bool row_ok = lane < here;
             const int64_t row = static_cast<int64_t>(p.row0) + first_row + lane;
+            // outputs in chunks of 32: the warp's are `chunks` from chunk0 of the lanes' on, whose
+            // first is column0 of the tile
             const int n0 = p.n_blk * kOut;
+            const int column0 = small ? (quarter >> 1) * (kOut / 2) : 0;
+            const int chunks = (small ? kOut / 2 : kOut) / 64, chunk0 = half * chunks;
+            const int up = small ? kOut / 2 : kOut;  // columns from a gate to its value in tensor memory
+            const int n_first = n0 + column0 + 32 * chunk0;
             float st = 0.0f;
-            if (cta_rows > 0) {
+            if (any && whole) {
                 if (row_ok) st = a.s_tok[row];
+                const float* s_w = a.s_w + static_cast<int64_t>(p.e) * a.N;
 #pragma unroll
-                for (int i = 0; i < BN / 32; ++i) {
-                    const int c = i * 32 + lane;
-                    const int n = kGated ? (c & (kOut - 1)) + n0 : c + n0;
-                    sw[c] = n < F ? a.s_w[static_cast<int64_t>(p.e) * a.N + n + (kGated && c >= kOut ? F : 0)] : 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    const int c = i * 32 + lane;  // (with a gate: 64 of the gate, 64 of the values)
+                    const int n = n_first + (kGated ? c & 63 : c);
+                    sw[c] = n < F ? s_w[n + (kGated && c >= 64 ? F : 0)] : 0.0f;
                 }
                 __syncwarp();
             }
-            // 32 outputs of this lane's row from column n0 + 32 c on.  Rows at 16-byte
-            // boundaries go through shared memory, so that a store instruction writes 128
-            // bytes of four rows each instead of 16 bytes of 32 rows.
-            uint4* stage = bars->out[quarter];
-            const int here = min(32, p.rows - first_row);
-            // this lane's j-th piece of 16 bytes of 8 (turned by the row: no bank is met twice)
-            auto piece = [&](int j) -> uint4& { return stage[lane * 8 + (j ^ (lane & 7))]; };
-            // the pieces of the warp's rows to rows at `out`, `row_bytes` apart, of which `bytes` are left
+            // Rows at 16-byte boundaries go through shared memory, so that a store instruction writes
+            // 64 bytes of eight rows each instead of 16 bytes of 32 rows: this lane's j-th piece of
+            // 16 bytes of 4 (turned by the row: no bank is met twice), ...
+            auto piece = [&](int j) -> uint4& { return stage[lane * 4 + (j ^ ((lane >> 1) & 3))]; };
+            // ... and the pieces to rows at `out`, `row_bytes` apart, of which `bytes` are left.
             auto flush = [&](void* out, int64_t row_bytes, int64_t bytes) {
                 __syncwarp();
-                uint8_t* to = static_cast<uint8_t*>(out) + (lane >> 3) * row_bytes + 16 * (lane & 7);
-                const bool there = 16 * (lane & 7) < bytes;
+                uint8_t* to = static_cast<uint8_t*>(out) + (lane >> 2) * row_bytes + 16 * (lane & 3);
+                const bool there = 16 * (lane & 3) < bytes;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + (lane >> 3);
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + (lane >> 2);
                     if (r < here && there)
-                        __stcg(reinterpret_cast<uint4*>(to + 4 * i * row_bytes), stage[r * 8 + ((lane & 7) ^ (r & 7))]);
+                        __stcg(reinterpret_cast<uint4*>(to + 8 * i * row_bytes),
+                               stage[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))]);
                 }
                 __syncwarp();
             };
-            auto emit = [&](const float (&v)[32], int c) {
+            // 32 outputs of this lane's row, the warp's i-th chunk
+            auto emit = [&](const float (&v)[32], int i) {
                 uint32_t packed[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-                const int n = n0 + column0 + 32 * c;
+                const int n = n_first + 32 * i;
                 if (wide) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        piece(4 * (c & 1) + j) =
-                            make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-                    if (c & 1)
-                        flush(a.y + (static_cast<int64_t>(p.row0) + first_row) * F + n - 32, 2 * static_cast<int64_t>(F),
-                              2 * (static_cast<int64_t>(F) - (n - 32)));
+                        piece(j) = make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+                    flush(a.y + (static_cast<int64_t>(p.row0) + first_row) * F + n, 2 * static_cast<int64_t>(F),
+                          2 * (static_cast<int64_t>(F) - n));
                     return;
                 }
                 if (!row_ok) return;
@@ -435,6 +438,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     if (n + j < F) o[j] = static_cast<uint16_t>(packed[j >> 1] >> ((j & 1) * 16));
+            };
+            // (acc s_tok) s_w of 32 columns, a pair of values an instruction
+            auto scale = [&](float (&v)[32], const uint32_t (&r)[32], const float* w) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    mul2(v[j], v[j + 1], __uint_as_float(r[j]), __uint_as_float(r[j + 1]), st, st);
+                    mul2(v[j], v[j + 1], v[j], v[j + 1], w[j], w[j + 1]);
+                }
             };
             // (a quotient that is rounded to 2^-22 and takes the same time for every value: rows that
             // are not there hold anything, and a true division of NaN takes 50 times as long)
@@ -455,23 +466,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             if (whole) {
-                const float* sg = sw + column0;
+                const uint32_t from = acc + 32 * chunk0;
                 if constexpr (kGated) {
-                    const float* su = sg + kOut;
 #pragma unroll
-                    for (int c = 0; c < kOut / 32; ++c) {
+                    for (int c = 0; c < kOut / 64; ++c) {
                         if (c >= chunks) break;
                         uint32_t g[32], u[32];
-                        tmem_ld_32x32b_x32(acc + 32 * c, g);
-                        tmem_ld_32x32b_x32(acc + up + 32 * c, u);
+                        tmem_ld_32x32b_x32(from + 32 * c, g);
+                        tmem_ld_32x32b_x32(from + up + 32 * c, u);
                         tmem_ld_wait_regs(g);
                         tmem_ld_wait_regs(u);
                         if (c == chunks - 1) release();
-                        float v[32];
+                        float v[32], x[32];
+                        scale(v, g, sw + 32 * c);
+                        scale(x, u, sw + 64 + 32 * c);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = gated((__uint_as_float(g[j]) * st) * sg[32 * c + j],
-                                         (__uint_as_float(u[j]) * st) * su[32 * c + j]);
+                        for (int j = 0; j < 32; ++j) v[j] = gated(v[j], x[j]);
                         emit(v, c);
                     }
                 } else {
@@ -479,19 +489,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t ra[32], rb[32];
                     auto one = [&](const uint32_t (&r)[32], int c) {
                         float v[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = (__uint_as_float(r[j]) * st) * sg[32 * c + j];
+                        scale(v, r, sw + 32 * c);
                         emit(v, c);
                     };
-                    tmem_ld_32x32b_x32(acc, ra);
+                    tmem_ld_32x32b_x32(from, ra);
                     tmem_ld_wait_regs(ra);
 #pragma unroll
-                    for (int c = 0; c < BN / 32; c += 2) {
+                    for (int c = 0; c < kOut / 64; c += 2) {
                         if (c >= chunks) break;
-                        tmem_ld_32x32b_x32(acc + (c + 1) * 32, rb);
+                        tmem_ld_32x32b_x32(from + (c + 1) * 32, rb);
                         one(ra, c);
                         tmem_ld_wait_regs(rb);
-                        if (c + 2 < chunks) tmem_ld_32x32b_x32(acc + (c + 2) * 32, ra);
+                        if (c + 2 < chunks) tmem_ld_32x32b_x32(from + (c + 2) * 32, ra);
                         else release();
                         one(rb, c + 1);
                         if (c + 2 < chunks) tmem_ld_wait_regs(ra);
@@ -500,15 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 continue;
             }
-            // Part of a tile: the sums go to the workspace, row by row.
+            // Part of a tile: the sums go to the workspace, row by row, this warp's half of the
+            // lanes' chunks.
             auto part = [&](int w, int slot) {
                 return a.parts + ((static_cast<int64_t>(w) * C::CTAS + rank) * 2 + slot) * a.slot;
             };
             if (any) {
                 float* mine = part(worker, walk.kb0 == 0 ? 1 : 0) + (first_row - cta_row0) * BN;
 #pragma unroll
-                for (int c = 0; c < BN / 32; ++c) {
-                    if (small && c >= BN / 64) break;
+                for (int i = 0; i < BN / 64; ++i) {
+                    const int mine_of = (small ? BN / 2 : BN) / 64;
+                    if (i >= mine_of) break;
+                    const int c = half * mine_of + i;
                     // (columns as in a tile of all rows: the gate's, then the values')
                     const int column = !small ? 32 * c
                                        : kGated ? column0 + 32 * (c & 1) + (c >> 1) * kOut
@@ -517,8 +529,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_32x32b_x32(acc + 32 * c, r);
                     tmem_ld_wait_regs(r);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) piece(j) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                    flush(mine + column, BN * 4, 128);
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            piece(j) = make_uint4(r[16 * h + 4 * j], r[16 * h + 4 * j + 1], r[16 * h + 4 * j + 2],
+                                                  r[16 * h + 4 * j + 3]);
+                        flush(mine + column + 16 * h, BN * 4, 64);
+                    }
                 }
             }
             release();
@@ -527,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __threadfence();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->part_done);
-            if (quarter == 0) {  // (one of the four warps)
+            if (me == 0) {
                 if (!warp_wait(&bars->part_done, part_phase, abort_flag, a.status)) break;
                 if (lane == 0) {
                     __threadfence();
@@ -542,10 +559,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             part_phase ^= 1u;
             if (!*const_cast<volatile int*>(&bars->last)) continue;
             __threadfence();
-            // The last to arrive adds the parts in the order of K: the four warps take kBatch rows in
-            // turn, a lane columns 4 l .. 4 l + 3 of each half (with a gate: the gate and its values).
-            const float4 sl = reinterpret_cast<const float4*>(sw)[lane], sh = reinterpret_cast<const float4*>(sw)[32 + lane];
+            // The last to arrive adds the parts in the order of K: the warps take kBatch rows in turn,
+            // a lane columns 4 l .. 4 l + 3 of each half (with a gate: the gate and its values).
             const int64_t step = a.slot * 2 * C::CTAS;
+            float sl[4], sh[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = n0 + 4 * lane + j, m = kGated ? n : n + BN / 2;
+                const float* s_w = a.s_w + static_cast<int64_t>(p.e) * a.N;
+                sl[j] = n < F ? s_w[n] : 0.0f;
+                sh[j] = m < F ? s_w[m + (kGated ? F : 0)] : 0.0f;
+            }
             auto put = [&](const float (&q)[4], int r, int n) {
                 __nv_bfloat16* out = a.y + (static_cast<int64_t>(p.row0) + cta_row0 + r) * F + n;
                 if (wide) {
@@ -557,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 4; ++j)
                     if (n + j < F) out[j] = __float2bfloat16_rn(q[j]);
             };
-            for (int r0 = quarter * kBatch; r0 < cta_rows; r0 += kQuarters * kBatch) {
+            for (int r0 = me * kBatch; r0 < cta_rows; r0 += kOutWarps * kBatch) {
                 float4 lo[kBatch], hi[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -582,8 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kBatch; ++i) {
                     if (r0 + i >= cta_rows) break;
                     const float t = a.s_tok[p.row0 + cta_row0 + r0 + i];
-                    float v[4] = {(lo[i].x * t) * sl.x, (lo[i].y * t) * sl.y, (lo[i].z * t) * sl.z, (lo[i].w * t) * sl.w};
-                    float u[4] = {(hi[i].x * t) * sh.x, (hi[i].y * t) * sh.y, (hi[i].z * t) * sh.z, (hi[i].w * t) * sh.w};
+                    float v[4] = {(lo[i].x * t) * sl[0], (lo[i].y * t) * sl[1], (lo[i].z * t) * sl[2], (lo[i].w * t) * sl[3]};
+                    float u[4] = {(hi[i].x * t) * sh[0], (hi[i].y * t) * sh[1], (hi[i].z * t) * sh[2], (hi[i].w * t) * sh[3]};
                     if constexpr (kGated) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) v[j] = gated(v[j], u[j]);
@@ -618,10 +642,10 @@ __global__ void clear_counts(unsigned* count, int n) {
 constexpr int64_t kCounts = kMaxCtas;
 constexpr int64_t kCountBytes = (kCounts * 4 + 255) / 256 * 256;
 
-// Floats of a part: the quarters of 32 rows that a CTA can have.
+// Floats of a part: the rows that a CTA can have, in 32s.
 int64_t slot_floats(int64_t R) {
-    const int64_t quarters = (R + 31) / 32;
-    return (quarters < kQuarters ? quarters : kQuarters) * 32 * BN;
+    const int64_t rows = (R + 31) / 32 * 32;
+    return (rows < kTileRows ? rows : kTileRows) * BN;
 }
 
 // Pairs where an expert has more rows than a CTA's tile on average.
