@@ -84,6 +84,7 @@ struct Bars {
     alignas(16) float s_w[kOutWarps][BN / 2];     // weight scales of the warp's columns
     alignas(16) uint4 out[kOutWarps][32 * 4];     // 32 rows x 64 bytes on their way out
     int first[kMaxExperts + 1];    // tiles of the experts below
+    int begin[kMaxExperts], end[kMaxExperts];  // an expert's rows
 };
 
 template <bool kPair>
@@ -123,25 +124,25 @@ __device__ __forceinline__ Bounds bounds_of(const Args& a, int e) {
 struct Place {
     int e, row0, rows, n_blk;  // its first row, how many rows the expert has from there on
 };
+template <typename B, int BM>
 struct Finder {
-    int e = -1, begin = 0, end = 0, m_tiles = 1;
-    template <int BM>
-    __device__ __forceinline__ Place at(const Args& a, const int* first, int tile) {
+    const B* bars;
+    int experts, e = -1, m_tiles = 1;
+    __device__ __forceinline__ Place at(int tile) {
+        const int* first = bars->first;
         if (e < 0 || tile < first[e] || tile >= first[e + 1]) {
-            int lo = 0, hi = a.E;  // first[lo] <= tile < first[hi]
+            int lo = 0, hi = experts;  // first[lo] <= tile < first[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (first[mid] <= tile) lo = mid;
                 else hi = mid;
             }
             e = lo;
-            const Bounds b = bounds_of(a, e);
-            begin = b.begin, end = b.end;
-            m_tiles = (end - begin + BM - 1) / BM;
+            m_tiles = (bars->end[e] - bars->begin[e] + BM - 1) / BM;
         }
         const int local = tile - first[e];
         const int n = local / m_tiles, m = local - n * m_tiles;
-        return {e, begin + m * BM, end - begin - m * BM, n};
+        return {e, bars->begin[e] + m * BM, bars->end[e] - bars->begin[e] - m * BM, n};
     }
 };
 
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_tiles = (F + kOut - 1) / kOut;
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
         const Bounds b = bounds_of(a, e);
+        bars->begin[e] = b.begin, bars->end[e] = b.end;
         bars->first[e + 1] = (b.end - b.begin + C::BM - 1) / C::BM * n_tiles;
     }
     __syncthreads();
@@ -226,14 +228,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     Walk walk(bars->first[a.E], workers, worker, nk, a.costs);
-    Finder find;
+    Finder<B, C::BM> find{bars, a.E};
 
     if (warp == 0) {
         // ---- loads: this CTA's rows of X, its part of the weight rows ----
         uint32_t stage = 0, phase = 0, issued = 0;
         bool ok = true;
         while (ok && walk.advance()) {
-            const Place p = find.at<C::BM>(a, bars->first, walk.tile);
+            const Place p = find.at(walk.tile);
             const bool small = kPair && p.rows <= kTileRows;
             const int cta_rows = small ? kTileRows / 2 : kTileRows;
             // rows of X in one box, the smallest that has them (further rows of it are another
@@ -302,32 +304,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (leader) {
             // ---- MMAs ----
+            // (the next piece is looked up while the present one's MMAs run)
             uint32_t stage = 0, phase = 0;
-            bool ok = true;
             int local = 0;
-            while (ok && walk.advance()) {
-                const bool small = kPair && find.at<C::BM>(a, bars->first, walk.tile).rows <= kTileRows;
-                const uint32_t idesc =
-                    uniform(small ? idesc_e4m3_f32(kTileRows, BN) : idesc_e4m3_f32(C::BM, BN));
+            auto shape = [&] {
+                return uniform(kPair && find.at(walk.tile).rows <= kTileRows ? idesc_e4m3_f32(kTileRows, BN)
+                                                                             : idesc_e4m3_f32(C::BM, BN));
+            };
+            bool ok = true, more = walk.advance();
+            uint32_t next_idesc = more ? shape() : 0u;
+            while (ok && more) {
+                const int kb0 = walk.kb0, kb1 = walk.kb1;
+                const uint32_t idesc = next_idesc;
                 const int buf = local % kAccBufs;
                 const uint32_t acc_phase = (local / kAccBufs) & 1;
                 ++local;
                 if (!(ok = warp_wait_cluster(&bars->acc_empty[buf], acc_phase ^ 1u, abort_flag, a.status))) break;
                 tc_fence_after();
                 const uint32_t d = uniform(tmem_base + buf * BN);
-                for (int kb = walk.kb0; kb < walk.kb1; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!(ok = warp_ready(&bars->full[stage], phase, abort_flag, a.status))) break;
                     tc_fence_after();
                     const uint32_t xa = uniform(smem_u32(sA + stage * C::A_TILE));
                     const uint32_t wb = uniform(smem_u32(sB + stage * C::B_TILE));
-                    const uint32_t more = uniform(kb != walk.kb0);
+                    const uint32_t add = uniform(kb != kb0);
                     const int steps = (a.K - kb * BK + KSTEP - 1) / KSTEP;  // (the last stage may have fewer)
                     if (elect_one()) {
                         const uint64_t a0 = sdesc_kmajor_sw128(xa), b0 = sdesc_kmajor_sw128(wb);
                         auto mma = [&](int kk) {
                             const uint64_t ad = a0 + 2 * kk, bd = b0 + 2 * kk;
-                            if constexpr (kPair) mma_f8_pair(d, ad, bd, idesc, kk ? 1u : more);
-                            else mma_f8(d, ad, bd, idesc, kk ? 1u : more);
+                            if constexpr (kPair) mma_f8_pair(d, ad, bd, idesc, kk ? 1u : add);
+                            else mma_f8(d, ad, bd, idesc, kk ? 1u : add);
                         };
                         if (steps >= BK / KSTEP) {
 #pragma unroll
@@ -339,6 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else mma_commit(&bars->empty[stage]);
                     }
                     __syncwarp();
+                    if (kb == kb0) {
+                        more = walk.advance();
+                        if (more) next_idesc = shape();
+                    }
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -366,40 +377,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool wide = F % 8 == 0;  // rows of y at 16-byte boundaries
         int local = 0;
         uint32_t part_phase = 0;
-        while (walk.advance()) {
-            const Place p = find.at<C::BM>(a, bars->first, walk.tile);
+        // a piece of the list as this warp sees it
+        struct Piece {
+            Place p;
+            int tile, kb0, kb1;
+            int cta_row0, first_row;  // the CTA's and the warp's first row within the tile
+            int column0, chunks;      // outputs in chunks of 32: the warp's first and how many
+            bool small;
+            float st, sw[4];          // scales of the lane's row, of the warp's columns (128: 4 a lane)
+        };
+        // Its scales are asked for while the piece before is on its way out.
+        auto look = [&](Piece& q) {
+            q.p = find.at(walk.tile);
+            q.tile = walk.tile, q.kb0 = walk.kb0, q.kb1 = walk.kb1;
+            // A small tile (M = 128 over the pair): 64 rows a CTA, lanes 0 .. 63 with the first half
+            // of the columns, lanes 64 .. 127 with the second.
+            q.small = kPair && q.p.rows <= kTileRows;
+            q.cta_row0 = rank * (q.small ? kTileRows / 2 : kTileRows);
+            q.first_row = q.cta_row0 + (q.small ? quarter & 1 : quarter) * 32;
+            q.chunks = (q.small ? kOut / 2 : kOut) / 64;
+            q.column0 = (q.small ? (quarter >> 1) * (kOut / 2) : 0) + 32 * half * q.chunks;
+            if (q.first_row >= q.p.rows) return;
+            if (q.first_row + lane < q.p.rows) q.st = a.s_tok[q.p.row0 + q.first_row + lane];
+            const float* s_w = a.s_w + static_cast<int64_t>(q.p.e) * a.N;
+            const int n_first = q.p.n_blk * kOut + q.column0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = i * 32 + lane;  // (with a gate: 64 of the gate, 64 of the values)
+                const int n = n_first + (kGated ? c & 63 : c);
+                q.sw[i] = n < F ? s_w[n + (kGated && c >= 64 ? F : 0)] : 0.0f;
+            }
+        };
+        Piece next = {};
+        bool more = walk.advance();
+        if (more) look(next);
+        while (more) {
+            const Piece now = next;
+            const Place& p = now.p;
+            const bool small = now.small;
             const int buf = local % kAccBufs;
             const uint32_t acc_phase = (local / kAccBufs) & 1;
             ++local;
-            // A small tile (M = 128 over the pair): 64 rows a CTA, lanes 0 .. 63 with the first half
-            // of the columns, lanes 64 .. 127 with the second.
-            const bool small = kPair && p.rows <= kTileRows;
-            const int cta_row0 = rank * (small ? kTileRows / 2 : kTileRows);
-            const int first_row = cta_row0 + (small ? quarter & 1 : quarter) * 32;  // of the warp, within the tile
+            const int cta_row0 = now.cta_row0, first_row = now.first_row;
             const int cta_rows = min(p.rows - cta_row0, small ? kTileRows / 2 : kTileRows);
             const int here = min(32, p.rows - first_row);
-            const bool any = here > 0, whole = walk.kb0 == 0 && walk.kb1 == nk;
+            const bool any = here > 0, whole = now.kb0 == 0 && now.kb1 == nk;
             const bool row_ok = lane < here;
             const int64_t row = static_cast<int64_t>(p.row0) + first_row + lane;
-            // outputs in chunks of 32: the warp's are `chunks` from chunk0 of the lanes' on, whose
-            // first is column0 of the tile
-            const int n0 = p.n_blk * kOut;
-            const int column0 = small ? (quarter >> 1) * (kOut / 2) : 0;
-            const int chunks = (small ? kOut / 2 : kOut) / 64, chunk0 = half * chunks;
+            const int n0 = p.n_blk * kOut, n_first = n0 + now.column0;
+            const int column0 = now.column0 - 32 * half * now.chunks;  // of the lanes
+            const int chunks = now.chunks, chunk0 = half * chunks;
             const int up = small ? kOut / 2 : kOut;  // columns from a gate to its value in tensor memory
-            const int n_first = n0 + column0 + 32 * chunk0;
-            float st = 0.0f;
+            const float st = row_ok ? now.st : 0.0f;
             if (any && whole) {
-                if (row_ok) st = a.s_tok[row];
-                const float* s_w = a.s_w + static_cast<int64_t>(p.e) * a.N;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = i * 32 + lane;  // (with a gate: 64 of the gate, 64 of the values)
-                    const int n = n_first + (kGated ? c & 63 : c);
-                    sw[c] = n < F ? s_w[n + (kGated && c >= 64 ? F : 0)] : 0.0f;
-                }
+                for (int i = 0; i < 4; ++i) sw[i * 32 + lane] = now.sw[i];
                 __syncwarp();
             }
+            more = walk.advance();
+            if (more) look(next);
             // Rows at 16-byte boundaries go through shared memory, so that a store instruction writes
             // 64 bytes of eight rows each instead of 16 bytes of 32 rows: this lane's j-th piece of
             // 16 bytes of 4 (turned by the row: no bank is met twice), ...
@@ -515,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return a.parts + ((static_cast<int64_t>(w) * C::CTAS + rank) * 2 + slot) * a.slot;
             };
             if (any) {
-                float* mine = part(worker, walk.kb0 == 0 ? 1 : 0) + (first_row - cta_row0) * BN;
+                float* mine = part(worker, now.kb0 == 0 ? 1 : 0) + (first_row - cta_row0) * BN;
 #pragma unroll
                 for (int i = 0; i < BN / 64; ++i) {
                     const int mine_of = (small ? BN / 2 : BN) / 64;
@@ -539,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             release();
-            const int64_t unit = static_cast<int64_t>(walk.tile - walk.whole) * nk;
+            const int64_t unit = static_cast<int64_t>(now.tile - walk.whole) * nk;
             const int w_first = walk.worker_of(unit), w_last = walk.worker_of(unit + nk - 1);
             __threadfence();
             __syncwarp();
