@@ -13,7 +13,9 @@
 // the row follow one another (sum of squares of b, of h', maximum of z), and
 // several CTAs an SM hide them.  Bound by DRAM, with the instructions close
 // behind: arithmetic is on pairs (f32x2), and z is kept negated, which is what the
-// quantizer's division wants (quant_math.cuh).
+// quantizer's division wants (quant_math.cuh).  8192 tokens of 4096: 49 us, 6.2 TB/s
+// (91% of a copy) with y as it is, 55 us with a norm and a gate, 63 us with two rows
+// of y by weight, whose places each token has to read first.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,7 +28,14 @@
 namespace fp8k {
 namespace {
 
-constexpr int kBlock = 256;
+// Threads of a CTA: a token's, so that no token waits at another's barriers; warps that have a
+// token to themselves come in eights.
+template <int G>
+constexpr int kBlockOf = G > 32 ? G : 256;
+
+// Threads an SM: with four chunks a thread half as many, with twice the registers.
+template <int VPT>
+constexpr int kResident = VPT > 2 ? 512 : 1024;
 
 template <int G, bool kMax>
 __device__ __forceinline__ float over_row(float v, float* red) {
@@ -105,8 +114,8 @@ __device__ __forceinline__ uint2 codes_of_negated(const float (&v)[8], const Div
 
 // kTop: the branch is rows of y by weight, not row t of it.
 template <int G, int VPT, bool kTop>
-__global__ void __launch_bounds__(G > kBlock ? G : kBlock, 1024 / (G > kBlock ? G : kBlock)) residual_norm(const ResidualNormArgs a) {
-    constexpr int B = G > kBlock ? G : kBlock;
+__global__ void __launch_bounds__(kBlockOf<G>, G > kResident<VPT> ? 1 : kResident<VPT> / kBlockOf<G>) residual_norm(const ResidualNormArgs a) {
+    constexpr int B = kBlockOf<G>;
     constexpr int ROWS = B / G;
     constexpr uint32_t kNegate = 0x80008000u;
     // (64 registers a thread do not hold two chunks of everything)
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock, 1024 / (G > kBlock ? 
 
 template <int G, int VPT, bool kTop>
 cudaError_t launch_as(const ResidualNormArgs& a, cudaStream_t st) {
-    constexpr int B = G > kBlock ? G : kBlock;
+    constexpr int B = kBlockOf<G>;
     constexpr int ROWS = B / G;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -239,7 +248,12 @@ cudaError_t launch(const ResidualNormArgs& a, cudaStream_t st) {
 }
 
 // Chunks of all tokens up to which a thread has one (its serial work is the
-// call's latency); beyond, two.
+// call's latency).  Beyond, two, or four where that was measured to be faster (us,
+// two / four chunks a thread):
+//   8192 tokens of 4096, y as it is 49.0 / 52.0, two rows by weight 64.1 / 62.7
+//   8192 of 1024, two rows 16.1 / 19.3;  of 2048, two rows 42.0 / 41.4
+//   4096 of 8192, two rows 94.5 / 84.2;  2048 of 16384, y as it is 87.5 / 73.4
+// (one chunk: 8192 of 4096 72.7).
 constexpr int64_t kFewChunks = 152 * 1024;
 
 }  // namespace
@@ -254,12 +268,16 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, cudaStream_t st) {
         if (C <= 512) return launch<512, 1>(a, st);
         if (C <= 1024) return launch<1024, 1>(a, st);
     }
-    if (C <= 64) return launch<32, 2>(a, st);
-    if (C <= 128) return launch<64, 2>(a, st);
-    if (C <= 256) return launch<128, 2>(a, st);
-    if (C <= 512) return launch<256, 2>(a, st);
-    if (C <= 1024) return launch<512, 2>(a, st);
-    if (C <= 2048) return launch<1024, 2>(a, st);
+    if (C <= (a.k > 0 ? 128 : 512)) {
+        if (C <= 64) return launch<32, 2>(a, st);
+        if (C <= 128) return launch<64, 2>(a, st);
+        if (C <= 256) return launch_as<128, 2, false>(a, st);
+        return launch_as<256, 2, false>(a, st);
+    }
+    if (C <= 256) return launch_as<64, 4, true>(a, st);
+    if (C <= 512) return launch_as<128, 4, true>(a, st);
+    if (C <= 1024) return launch<256, 4>(a, st);
+    if (C <= 2048) return launch<512, 4>(a, st);
     return launch<1024, 4>(a, st);
 }
 
