@@ -17,6 +17,7 @@ constexpr int64_t kMaxLd = int64_t(1) << 38;  // elements between two rows
 constexpr int64_t kMost = int64_t(1) << 30;   // rows and widths that the kernels count in 32 bits
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxTop = 32;
+constexpr int64_t kMaxTokens = int64_t(1) << 23;  // of a routing (counts of its parts in 16 bits)
 constexpr int64_t kMaxNormWidth = 32768;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -83,7 +84,7 @@ extern "C" {
 
 size_t fp8_moe_route_workspace_size(int64_t T, int64_t E, int64_t top_k) {
     if (T < 0 || E < 1 || E > kMaxExperts || top_k < 1 || top_k > E || top_k > kMaxTop ||
-        T > kMost / top_k)
+        T > kMaxTokens)
         return 0;
     return fp8k::moe_route_workspace(T, E, top_k);
 }
@@ -94,7 +95,7 @@ fp8_status_t fp8_moe_route(const void* logits, int logits_fp32, int64_t ld, int6
                            int32_t* token_row, void* workspace, size_t ws_bytes, void* stream) {
     if (any_out({T, E, top_k}) || top_k < 1 || top_k > E || !std::isfinite(scale))
         return FP8_ERR_INVALID_ARG;
-    if (E > kMaxExperts || top_k > kMaxTop || T > kMost / top_k) return FP8_ERR_UNSUPPORTED;
+    if (E > kMaxExperts || top_k > kMaxTop || T > kMaxTokens) return FP8_ERR_UNSUPPORTED;
     if (!offsets || (T > 0 && (!logits || !expert_ids || !weights || !row_token || !token_row)))
         return FP8_ERR_INVALID_ARG;
     if (T > 0 && (ld < E || ld > kMaxLd)) return FP8_ERR_INVALID_ARG;
@@ -118,7 +119,7 @@ fp8_status_t fp8_moe_route(const void* logits, int logits_fp32, int64_t ld, int6
     a.ids = expert_ids;
     a.weights = weights;
     a.offsets = offsets, a.row_token = row_token, a.token_row = token_row;
-    a.workspace = static_cast<int32_t*>(workspace);
+    a.workspace = static_cast<uint16_t*>(workspace);
     return said(fp8k::launch_moe_route(a, as_stream(stream)));
 }
 

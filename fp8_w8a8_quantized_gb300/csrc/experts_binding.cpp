@@ -64,7 +64,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const int64_t T = logits.size(0), E = logits.size(1);
     TORCH_CHECK_VALUE(k >= 1 && k <= E && k <= 32 && E <= 1024, "top_k must be 1 .. min(experts, 32) and experts "
                       "at most 1024; got ", k, " of ", E);
-    TORCH_CHECK_VALUE(T <= (int64_t(1) << 30) / k, "tokens * top_k must be at most 2^30");
+    TORCH_CHECK_VALUE(T <= int64_t(1) << 23, "at most 2^23 tokens; got ", T);
     const Place place(logits, a[10]);
     if (!ids.defined() && !weights.defined() && !offsets.defined() && !row_token.defined() && !token_row.defined() &&
         !ws.defined()) {

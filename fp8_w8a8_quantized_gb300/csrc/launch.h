@@ -196,7 +196,7 @@ struct RouteArgs {
     int32_t* ids;
     float* weights;
     int32_t *offsets, *row_token, *token_row;
-    int32_t* workspace;
+    uint16_t* workspace;
 };
 cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t st);
 size_t moe_route_workspace(int64_t T, int64_t E, int64_t k);

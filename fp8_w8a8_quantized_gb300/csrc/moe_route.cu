@@ -126,13 +126,13 @@ struct Lane<32> : Wide<32> {
 struct Route {
     const void* logits;
     int64_t ld;
-    int T, E, k;  // (T * k <= 2^30)
+    int T, E, k;  // (T <= 2^23)
     bool renorm;
     float scale;
     int32_t* ids;
     float* weights;
     int32_t *offsets, *row_token, *token_row;
-    int32_t* counts;  // with two launches: [parts][E rounded up to 4]
+    uint16_t* counts;  // with two launches: [parts][E rounded up to 8]
 };
 
 // The experts of tokens first .. last - 1, counted in `count`.
@@ -140,13 +140,21 @@ template <typename Logit, int kPerLane>
 __device__ __forceinline__ void choose(const Route& a, int first, int last, int32_t* count) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Logit* logits = static_cast<const Logit*>(a.logits);
-    for (int t = first + warp; t < last; t += kThreadsOf<kPerLane> / 32) {
-        float v[kPerLane];
+    constexpr int kWarps = kThreadsOf<kPerLane> / 32;
+    float ahead[kPerLane];  // the warp's next token
+    auto look = [&](int t) {
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) {
             const int e = i * 32 + lane;
-            v[i] = e < a.E ? logit(logits + static_cast<int64_t>(t) * a.ld + e) : -INFINITY;
+            ahead[i] = t < last && e < a.E ? logit(logits + static_cast<int64_t>(t) * a.ld + e) : -INFINITY;
         }
+    };
+    look(first + warp);
+    for (int t = first + warp; t < last; t += kWarps) {
+        float v[kPerLane];
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) v[i] = ahead[i];
+        look(t + kWarps);
         uint32_t o[kPerLane];
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) o[i] = order_of(v[i]);
@@ -278,9 +286,9 @@ __device__ __forceinline__ void clear_rest(const Route& a, int32_t rows, int par
 }
 
 // (what 48 KB hold beside three numbers an expert)
-int placers_of(int E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }
+int placers_of(int E) { return E <= 512 ? 16 : 8; }
 
-size_t shared_bytes(int E) { return sizeof(int32_t) * (placers_of(E) * E + 3 * ((E + 3) & ~3)); }
+size_t shared_bytes(int E) { return sizeof(int32_t) * (placers_of(E) * E + 3 * ((E + 7) & ~7)); }
 
 // One cluster does all of it.
 template <typename Logit, int kPerLane>
@@ -319,8 +327,9 @@ __global__ void __launch_bounds__(kThreadsOf<kPerLane>) route_cluster(const Rout
     if (parts > 1) cluster_wait();
 }
 
-// Counts of a part lie in rows of E rounded up to 4.
-__host__ __device__ __forceinline__ int padded(int E) { return (E + 3) & ~3; }
+// Counts of a part lie in rows of E rounded up to 8, in 16 bits: every CTA of the second
+// launch reads all of them, and a part has fewer than 2^16 tokens.
+__host__ __device__ __forceinline__ int padded(int E) { return (E + 7) & ~7; }
 
 template <typename Logit, int kPerLane>
 __global__ void __launch_bounds__(kThreadsOf<kPerLane>) route_choose(const Route a, int) {
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(kThreadsOf<kPerLane>) route_choose(const Route
     share(a.T, gridDim.x, blockIdx.x, &first, &last);
     choose<Logit, kPerLane>(a, first, last, count);
     __syncthreads();
-    for (int e = threadIdx.x; e < padded(a.E); e += blockDim.x) a.counts[blockIdx.x * padded(a.E) + e] = count[e];
+    for (int e = threadIdx.x; e < padded(a.E); e += blockDim.x) a.counts[blockIdx.x * padded(a.E) + e] = static_cast<uint16_t>(count[e]);
 }
 
 __global__ void __launch_bounds__(1024) route_place(const Route a, int placers) {
@@ -347,23 +356,29 @@ __global__ void __launch_bounds__(1024) route_place(const Route a, int placers) 
     pdl_launch_dependents();
     pdl_wait_primary();
     const int part = blockIdx.x, parts = gridDim.x;
-    // the parts' counts: a thread four experts of every groups-th part, all its loads on their way
+    // the parts' counts: a thread eight experts of every groups-th part, all its loads on their way
     // together (whole numbers: the order of the additions does not matter)
-    const int columns = padded(a.E) / 4, groups = blockDim.x / columns;  // (at least 4 groups)
+    const int columns = padded(a.E) / 8, groups = min(16, static_cast<int>(blockDim.x) / columns);
     const int g = threadIdx.x / columns, x = threadIdx.x - g * columns;
     if (g < groups) {
-        int4 all = make_int4(0, 0, 0, 0), mine = all;
-        const int4* counts = reinterpret_cast<const int4*>(a.counts) + x;
+        int32_t all[8] = {}, mine[8] = {};
+        const uint4* counts = reinterpret_cast<const uint4*>(a.counts) + x;
 #pragma unroll 10
         for (int c = g; c < parts; c += groups) {
-            const int4 n = counts[c * columns];
-            all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
-            if (c < part) mine.x += n.x, mine.y += n.y, mine.z += n.z, mine.w += n.w;
+            const uint4 n = counts[c * columns];
+            const uint32_t w[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int32_t v = static_cast<int32_t>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
+                all[i] += v;
+                if (c < part) mine[i] += v;
+            }
         }
-        atomicAdd(base + 4 * x, all.x), atomicAdd(base + 4 * x + 1, all.y);
-        atomicAdd(base + 4 * x + 2, all.z), atomicAdd(base + 4 * x + 3, all.w);
-        atomicAdd(prior + 4 * x, mine.x), atomicAdd(prior + 4 * x + 1, mine.y);
-        atomicAdd(prior + 4 * x + 2, mine.z), atomicAdd(prior + 4 * x + 3, mine.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (all[i]) atomicAdd(base + 8 * x + i, all[i]);
+            if (mine[i]) atomicAdd(prior + 8 * x + i, mine[i]);
+        }
     }
     __syncthreads();
     const int32_t rows = first_rows(a.E, base, prior, part == 0 ? a.offsets : nullptr, warp_sums);
@@ -421,7 +436,7 @@ cudaError_t launch_typed(const Route& r, cudaStream_t st) {
 
 size_t moe_route_workspace(int64_t T, int64_t E, int64_t k) {
     (void)k;
-    return T <= cluster_tokens(E) ? 0 : sizeof(int32_t) * padded(static_cast<int>(E)) * kMaxParts;
+    return T <= cluster_tokens(E) ? 0 : sizeof(uint16_t) * padded(static_cast<int>(E)) * kMaxParts;
 }
 
 cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t st) {

@@ -554,8 +554,8 @@ FP8_API size_t fp8_attention_decode_workspace_size(int64_t B, int64_t Hq, int64_
  *   workspace  [device]       fp8_moe_route_workspace_size() bytes, 16-byte
  *                             aligned; need not start at zero; not in use by
  *                             another call in flight
- * Requirements: 1 <= top_k <= E <= 1024, top_k <= 32; T * top_k <= 2^30; scale
- * finite; pointers aligned to their elements.  With T == 0 only offsets is
+ * Requirements: 1 <= top_k <= E <= 1024, top_k <= 32; T <= 2^23; scale finite;
+ * pointers aligned to their elements.  With T == 0 only offsets is
  * written.
  */
 FP8_API fp8_status_t fp8_moe_route(const void* logits, int logits_fp32, int64_t ld, int64_t T,
