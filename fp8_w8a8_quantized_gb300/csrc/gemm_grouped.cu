@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ---- loads: this CTA's rows of X, its part of the weight rows ----
         uint32_t stage = 0, phase = 0, issued = 0;
+        const uint64_t once = policy_evict_first(), again = policy_evict_normal();
         bool ok = true;
         while (ok && walk.advance()) {
             const Place p = find.at(walk.tile);
@@ -291,6 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool w_there = rank == 0 || second;
             // of K, that the stage's barrier waits for
             const uint32_t bytes = (kPair ? box_of(0) + box_of(1) : box) + (second ? 2 : 1) * kHalf;
+            // weights that one row tile reads leave L2 first, to what is read again (8 x 8 rows 141 ->
+            // 136 us; where several do, 570 -> 604)
+            const uint64_t policy = find.m_tiles == 1 ? once : again;
             // (operands of the copies from uniform registers, see elect_one in ptx.cuh)
             const uint32_t tx = uniform(bytes) * BK;
             const int x_row = static_cast<int>(uniform(row));
@@ -303,23 +307,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int k = kb * BK;
                     uint64_t* full = &bars->full[stage];
                     const uint32_t full0 = kPair ? map_to_rank(smem_u32(full), 0) : 0u;
-                    auto load = [&](uint8_t* to, const CUtensorMap* map, int r) {
-                        if constexpr (kPair) tma_load_2d_pair(to, map, full0, k, r);
-                        else tma_load_2d(to, map, full, k, r);
+                    auto load_w = [&](uint8_t* to, const CUtensorMap* map, int r) {
+                        if constexpr (kPair) tma_load_2d_pair_hint(to, map, full0, k, r, policy);
+                        else tma_load_2d_hint(to, map, full, k, r, policy);
                     };
                     if (leader) mbar_arrive_expect_tx(full, tx);
                     if constexpr (kPair) {
                         if (kGated && both) {
-                            load(w, &maps.w_small, w_row0);
-                            load(w + (kHalf / 2) * BK, &maps.w_small, w_row1);
+                            load_w(w, &maps.w_small, w_row0);
+                            load_w(w + (kHalf / 2) * BK, &maps.w_small, w_row1);
                         } else if (has_w) {
-                            load(w, &maps.w, w_row0);
+                            load_w(w, &maps.w, w_row0);
                         }
                     } else {
-                        load(w, &maps.w, w_row0);
-                        if (both) load(w + kHalf * BK, &maps.w, w_row1);
+                        load_w(w, &maps.w, w_row0);
+                        if (both) load_w(w + kHalf * BK, &maps.w, w_row1);
                     }
-                    if (has_x) load(sA + stage * C::A_TILE, x_map, x_row);
+                    if (has_x) {
+                        uint8_t* x = sA + stage * C::A_TILE;
+                        if constexpr (kPair) tma_load_2d_pair(x, x_map, full0, k, x_row);
+                        else tma_load_2d(x, x_map, full, k, x_row);
+                    }
                 }
                 __syncwarp();
                 ++issued;
