@@ -45,7 +45,8 @@ def fp8_grouped_gemm(xq: torch.Tensor, s_tok: torch.Tensor, wq: torch.Tensor, s_
                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rows offsets[e] .. offsets[e + 1] - 1 of the codes xq [R, K] times the codes
     wq[e] [N, K], with both scales, as bf16 [R, N]; with swiglu silu(first half)
-    * second half, [R, N / 2].  Rows outside the offsets stay as they are."""
+    * second half, [R, N / 2].  Rows outside the offsets stay as they are (in a new
+    y: anything)."""
     return _result((_module or _native()).grouped_gemm(xq, s_tok, wq, s_w, offsets, swiglu, y, workspace,
                                                        _handle(stream)), "fp8_grouped_gemm")
 

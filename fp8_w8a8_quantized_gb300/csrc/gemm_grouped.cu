@@ -535,9 +535,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mul2(v[j], v[j + 1], v[j], v[j + 1], w[j], w[j + 1]);
                 }
             };
-            // (a quotient that is rounded to 2^-22 and takes the same time for every value: rows that
-            // are not there hold anything, and a true division of NaN takes 50 times as long)
-            auto gated = [&](float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; };
+            // g / (1 + exp(-g)) u, by exp(-|g|), so that the divisor lies in 1 .. 2.  (A quotient that
+            // is rounded to 2^-22 and takes the same time for every value: rows that are not there
+            // hold anything, and a true division of NaN takes 50 times as long.)
+            auto gated = [&](float g, float u) {
+                const float t = __expf(-fabsf(g));
+                return __fdividef(g >= 0.0f ? g : g * t, 1.0f + t) * u;
+            };
             auto release = [&] {  // the accumulator has been read
                 tc_fence_before();
                 __syncwarp();

@@ -200,6 +200,38 @@ def test_grouped_cut_tiles_of_many_rows(swiglu):
     check_grouped([700, 140, 20], 320, 16384 + 48, swiglu)
 
 
+@pytest.mark.parametrize("rows", [3, 300])
+def test_grouped_gates_of_any_size(rows):
+    # gates from -inf over +-120 to inf, and values beside them: one product a row and column
+    K, F = 16, 64
+    xq = torch.zeros(rows, K, device=DEV)
+    xq[:, 0] = 1.0
+    gates = torch.cat([torch.linspace(-120, 120, F - 8, device=DEV),
+                       torch.tensor([0.0, -0.0, 1e-30, -1e-30, -87.5, -88.5, -103.0, 3e38], device=DEV)])
+    wq = torch.zeros(1, 2 * F, K, device=DEV)
+    wq[0, :, 0] = 1.0
+    s_w = torch.cat([gates, torch.full((F,), 1.5, device=DEV)])[None]  # (scales stand for the values)
+    s_tok = torch.ones(rows, device=DEV)
+    f8 = torch.float8_e4m3fn
+    y = fp8.fp8_grouped_gemm(xq.to(f8).view(torch.uint8), s_tok, wq.to(f8).view(torch.uint8), s_w, bounds([rows]),
+                             swiglu=True)
+    g = gates.double()
+    want = torch.where(g >= 0, g / (1 + torch.exp(-g.abs())), g * torch.exp(-g.abs()) / (1 + torch.exp(-g.abs()))) * 1.5
+    # exp of an argument of up to 120: rounded to 2^-24 of it, 2^-17; the rest is within 2^-20; below
+    # the normal numbers (of fp32 and bf16) half a step
+    tol = want.abs() * (ref.HALF["bf16"] + 2.0 ** -16) + 2.0 ** -133
+    # (4.5e38 lies beyond the largest bf16, 3.39e38 and half a step: infinity)
+    far = want.abs() > 3.4e38
+    assert far.sum() == 1 and torch.isinf(y[:, far].float()).all()
+    within(y[:, ~far], want[~far].expand(rows, -1), tol[~far].expand(rows, -1), "y")
+    clean()
+
+
+def test_grouped_rows_without_any_group():
+    check_grouped([0, 0, 0], 64, 128, False, start=3, extra=5)
+    check_grouped([0], 64, 128, True, start=0, extra=700)
+
+
 def test_grouped_workspace_need_not_be_clean():
     g = gen(21)
     wq, s_w = weights(g, 4, 256, 8192)
