@@ -111,7 +111,7 @@ struct Args {
     __nv_bfloat16* y;
     unsigned* count;   // [workers][CTAS]
     float* parts;      // [workers][CTAS][2][slot]
-    int64_t slot;      // floats of a part: its quarters of 32 rows x BN
+    int64_t slot;      // floats of a part: its rows x BN
     int E, R, N, K;
     Costs costs;
     bool ahead;        // the bounds can be read before griddepcontrol.wait

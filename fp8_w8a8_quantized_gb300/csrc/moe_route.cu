@@ -13,7 +13,7 @@
 // in its own part, which some of the CTA's warps number 32 pairs at a time
 // (match.sync).  Counts are whole numbers: nothing depends on an order of arrival.
 //
-// Up to 256 tokens it is one launch of one cluster, whose CTAs read one
+// Up to some hundred tokens it is one launch of one cluster, whose CTAs read one
 // another's counts through distributed shared memory; beyond, two launches with
 // the counts in the workspace (choose, place).  Small calls are bound by latency
 // (launch, logits, k rounds, numbering): 32 tokens of 64 experts, top 8, 5.0 us, 256
@@ -359,10 +359,12 @@ __global__ void __launch_bounds__(1024) route_place(const Route a, int placers) 
     pdl_wait_primary();
     const int part = blockIdx.x, parts = gridDim.x;
     // the parts' counts: a thread eight experts of every groups-th part, all its loads on their way
-    // together (whole numbers: the order of the additions does not matter)
-    const int columns = padded(a.E) / 8, groups = min(16, static_cast<int>(blockDim.x) / columns);
-    const int g = threadIdx.x / columns, x = threadIdx.x - g * columns;
-    if (g < groups) {
+    // together; a group is whole warps, so that lanes add to different numbers (whole ones: the
+    // order does not matter)
+    const int columns = padded(a.E) / 8, warps = (columns + 31) / 32;
+    const int groups = min(16, static_cast<int>(blockDim.x) / 32 / warps);
+    const int g = (threadIdx.x >> 5) / warps, x = threadIdx.x - g * warps * 32;
+    if (g < groups && x < columns) {
         int32_t all[8] = {}, mine[8] = {};
         const uint4* counts = reinterpret_cast<const uint4*>(a.counts) + x;
 #pragma unroll 10
@@ -390,9 +392,9 @@ __global__ void __launch_bounds__(1024) route_place(const Route a, int placers) 
     clear_rest(a, rows, part, parts);
 }
 
-// A token a warp of one cluster: with more, two launches are sooner done (256 experts,
-// top 8: 512 tokens 13.2 us in a cluster, 1025 in two launches 10.5).
-int64_t cluster_tokens(int64_t E) { return kClusterParts * (E <= 256 ? kThreadsOf<8> : kThreadsOf<32>) / 32; }
+// One cluster up to here (top 2 to 8, cluster / two launches, us: 512 tokens of 8 experts 5.8 /
+// 9.9, of 64 8.5 / 8.5, of 256 11.4 / 8.3).
+int64_t cluster_tokens(int64_t E) { return E <= 64 ? 512 : E <= 256 ? 256 : 128; }
 
 cudaError_t launch(void (*kernel)(const Route, int), int grid, int threads, int cluster, size_t smem, cudaStream_t st,
                    const Route& r) {
