@@ -37,6 +37,7 @@ constexpr int kBlockOf = G > 32 ? G : 256;
 template <int VPT>
 constexpr int kResident = VPT > 2 ? 512 : 1024;
 
+// Sum or maximum over a token's threads; `red` holds a float a warp and is used once.
 template <int G, bool kMax>
 __device__ __forceinline__ float over_row(float v, float* red) {
 #pragma unroll
@@ -46,14 +47,11 @@ __device__ __forceinline__ float over_row(float v, float* red) {
     }
     if constexpr (G > 32) {
         constexpr int WPG = G / 32;
-        const int warp = threadIdx.x >> 5;
-        if (lane_id() == 0) red[warp] = v;
+        if (lane_id() == 0) red[threadIdx.x >> 5] = v;
         __syncthreads();
-        const int first = (warp / WPG) * WPG;
-        v = red[first];
+        v = red[0];
 #pragma unroll
-        for (int w = 1; w < WPG; ++w) v = kMax ? fmaxf(v, red[first + w]) : v + red[first + w];
-        __syncthreads();
+        for (int w = 1; w < WPG; ++w) v = kMax ? fmaxf(v, red[w]) : v + red[w];
     }
     return v;
 }
@@ -121,7 +119,7 @@ __global__ void __launch_bounds__(kBlockOf<G>, G > kResident<VPT> ? 1 : kResiden
     // (64 registers a thread do not hold two chunks of everything)
     constexpr bool kEarly = G < 1024 || VPT == 1;
     constexpr int kAhead = kEarly ? 2 : 1;  // rows of a token on their way at a time
-    __shared__ float red[B / 32];
+    __shared__ alignas(16) float red[3][B / 32];
     pdl_launch_dependents();
     pdl_wait_primary();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / G;
@@ -180,7 +178,7 @@ __global__ void __launch_bounds__(kBlockOf<G>, G > kResident<VPT> ? 1 : kResiden
             p[i] = i < mine ? load(a.gamma_post + 8 * (i0 + i * G)) : zero;
             squares(b[i], s0, s1);
         }
-        const float ss = over_row<G, false>(s0 + s1, red);
+        const float ss = over_row<G, false>(s0 + s1, red[0]);
         const float inv = 1.0f / sqrtf(ss / K + a.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -205,7 +203,7 @@ __global__ void __launch_bounds__(kBlockOf<G>, G > kResident<VPT> ? 1 : kResiden
     uint4 p[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) p[i] = i < mine ? load(a.gamma + 8 * (i0 + i * G)) : zero;
-    const float ss = over_row<G, false>(s0 + s1, red);
+    const float ss = over_row<G, false>(s0 + s1, red[1]);
     const float inv = -1.0f / sqrtf(ss / K + a.eps);  // (z is negated from here on)
     float m = 0.0f;
 #pragma unroll
@@ -217,7 +215,7 @@ __global__ void __launch_bounds__(kBlockOf<G>, G > kResident<VPT> ? 1 : kResiden
         if (a.z && i < mine) *reinterpret_cast<uint4*>(a.z + t * a.K + 8 * (i0 + i * G)) = narrow(b[i], kNegate);
     }
     if (!a.q) return;
-    m = over_row<G, true>(m, red);
+    m = over_row<G, true>(m, red[2]);
     const float sc = scale_of(m);
     const Divisor d = divisor_of(sc);
 #pragma unroll
