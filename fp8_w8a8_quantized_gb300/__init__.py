@@ -44,5 +44,6 @@ from ._experts import (  # noqa: F401,E402
     fp8_grouped_linear,
     fp8_grouped_linear_workspace_size,
     fp8_moe_route,
+    fp8_moe_route_workspace_size,
     fp8_residual_norm_quant,
 )

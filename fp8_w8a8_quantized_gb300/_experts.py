@@ -21,6 +21,10 @@ def _native():
     return _module
 
 
+def fp8_moe_route_workspace_size(T: int, E: int, top_k: int) -> int:
+    return int(lib().fp8_moe_route_workspace_size(T, E, top_k))
+
+
 def fp8_moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, scale: float = 1.0,
                   expert_ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
                   offsets: torch.Tensor | None = None, row_token: torch.Tensor | None = None,

@@ -580,7 +580,8 @@ FP8_API size_t fp8_moe_route_workspace_size(int64_t T, int64_t E, int64_t top_k)
  *   wq     [device, in]  E4M3 [E, N, K], contiguous;  s_w [device, in] fp32 [E, N]
  *                        (fp8_quant_per_channel_weights of the [E * N, K] rows)
  *   offsets [device, in] int32 [E + 1], non-decreasing, within 0 .. R
- *   y      [device, out] bf16 [R, N], or [R, N / 2] with swiglu; contiguous
+ *   y      [device, out] bf16 [R, N], or [R, N / 2] with swiglu; contiguous;
+ *                        overlaps no input
  *   workspace [device]   fp8_grouped_gemm_workspace_size() bytes, 256-byte
  *                        aligned; need not start at zero; not in use by
  *                        another call in flight.  NULL if that is 0.
@@ -644,6 +645,7 @@ FP8_API size_t fp8_grouped_linear_workspace_size(int64_t E, int64_t R, int64_t N
  *   h_out  [device, out]  bf16 [T, K], ldho; may be h itself (ldho = ldh)
  *   z_out  [device, out]  bf16 [T, K], contiguous, or NULL
  *   xq     [device, out]  E4M3 [T, K], ldq, with s_tok fp32 [T]; or both NULL
+ *   Outputs overlap no input (but h_out h) and one another.
  * Requirements: K % 16 == 0, 0 < K <= 32768; top_k <= 32; leading dimensions >= K
  * and % 8 == 0 (ldq % 16); bf16 tensors and xq 16-byte aligned, others 4; eps
  * >= 0 finite; scales finite; T, R < 2^31.
