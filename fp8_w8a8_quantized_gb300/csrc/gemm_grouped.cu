@@ -52,6 +52,7 @@
 namespace fp8k {
 namespace {
 
+using grouped::Bounds;
 using grouped::Costs;
 using grouped::Walk;
 
@@ -123,15 +124,9 @@ struct Maps {
     CUtensorMap x[3], w, w_small;
 };
 
-struct Bounds {
-    int begin, end;
-};
+// (from L2: read before the wait and again behind it)
 __device__ __forceinline__ Bounds bounds_of(const Args& a, int e) {
-    Bounds b;
-    // (from L2: read before the wait and again behind it)
-    b.begin = min(max(__ldcg(a.offsets + e), 0), a.R);
-    b.end = min(max(__ldcg(a.offsets + e + 1), b.begin), a.R);
-    return b;
+    return grouped::bounds_within(__ldcg(a.offsets + e), __ldcg(a.offsets + e + 1), a.R);
 }
 
 // Where a tile lies.
@@ -219,12 +214,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tiles of each expert, then of all below it
     const int n_tiles = (F + kOut - 1) / kOut;
     auto make_list = [&] {
+        auto tiles_of = [&](int rows) { return (rows + C::BM - 1) / C::BM * n_tiles; };
+        bool back = false;
         for (int e = threadIdx.x; e < a.E; e += kThreads) {
             const Bounds b = bounds_of(a, e);
             bars->begin[e] = b.begin, bars->end[e] = b.end;
-            bars->first[e + 1] = (b.end - b.begin + C::BM - 1) / C::BM * n_tiles;
+            bars->first[e + 1] = tiles_of(b.end - b.begin);
+            back |= b.back;
         }
-        __syncthreads();
+        if (__syncthreads_or(back)) {  // (bounds that no routing makes)
+            if (threadIdx.x == 0) {
+                grouped::put_in_order(bars->begin, bars->end, a.E);
+                for (int e = 0; e < a.E; ++e) bars->first[e + 1] = tiles_of(bars->end[e] - bars->begin[e]);
+            }
+            __syncthreads();
+        }
         if (warp == 0) {
             int sum = 0;
             for (int e0 = 0; e0 < a.E; e0 += 32) {

@@ -1,5 +1,5 @@
-// How the workers of a grouped product share its tiles (gemm_grouped.cu); host
-// code too, so that it can be checked without a GPU.
+// Which rows the experts of a grouped product have and how the workers share its
+// tiles (gemm_grouped.cu); host code too, so that it can be checked without a GPU.
 #pragma once
 
 #include <cmath>
@@ -8,6 +8,27 @@
 
 namespace fp8k {
 namespace grouped {
+
+// An expert's rows: its two bounds cut to 0 .. R, the end no lower than the begin.
+struct Bounds {
+    int begin, end;
+    bool back;  // the second bound is below the first
+};
+__host__ __device__ __forceinline__ Bounds bounds_within(int lo, int hi, int R) {
+    const int begin = lo < 0 ? 0 : lo < R ? lo : R;
+    const int end = hi < 0 ? 0 : hi < R ? hi : R;
+    return {begin, end < begin ? begin : end, end < begin};
+}
+
+// Where bounds go back, each counts as the largest up to it, so that no row has two
+// experts and the experts' tiles stay as many as R rows can have.
+__host__ __device__ inline void put_in_order(int* begin, int* end, int E) {
+    int most = 0;
+    for (int e = 0; e < E; ++e) {
+        begin[e] = most = begin[e] < most ? most : begin[e];
+        end[e] = most = end[e] < most ? most : end[e];
+    }
+}
 
 // A worker's pieces of the list in order: whole tiles, then its share of the
 // tiles that are cut.

@@ -579,7 +579,9 @@ FP8_API size_t fp8_moe_route_workspace_size(int64_t T, int64_t E, int64_t top_k)
  *   xq     [device, in]  E4M3 [R, K], contiguous;  s_tok [device, in] fp32 [R]
  *   wq     [device, in]  E4M3 [E, N, K], contiguous;  s_w [device, in] fp32 [E, N]
  *                        (fp8_quant_per_channel_weights of the [E * N, K] rows)
- *   offsets [device, in] int32 [E + 1], non-decreasing, within 0 .. R
+ *   offsets [device, in] int32 [E + 1], non-decreasing, within 0 .. R (what lies
+ *                        outside is cut to 0 .. R, and a bound below an earlier
+ *                        one counts as the largest up to it: no row has two experts)
  *   y      [device, out] bf16 [R, N], or [R, N / 2] with swiglu; contiguous;
  *                        overlaps no input
  *   workspace [device]   fp8_grouped_gemm_workspace_size() bytes, 256-byte
