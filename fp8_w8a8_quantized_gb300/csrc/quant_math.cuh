@@ -130,8 +130,11 @@ __device__ __forceinline__ uint2 quant8(const uint4& v, const Divisor& d) {
                       quant2<kBounded>(v.z, d) | (quant2<kBounded>(v.w, d) << 16));
 }
 
+// (1 also where the quotient rounds to 0, from 2^-150 down: no code is a quotient by
+// 0.  Only maxima of unrounded values are that small; one of bf16 values is 2^-133 at least.)
 __device__ __forceinline__ float scale_of(float amax) {
-    return amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    return s > 0.0f ? s : 1.0f;
 }
 
 }  // namespace fp8k

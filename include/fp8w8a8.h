@@ -632,7 +632,7 @@ FP8_API size_t fp8_grouped_linear_workspace_size(int64_t E, int64_t R, int64_t N
  *   b = b * gate                                 (with a gate)
  *   h' = residual_scale h + branch_scale b;      h_out = bf16_rn(h')
  *   z = h' / sqrt(mean h'^2 + eps) * gamma;      z_out = bf16_rn(z)
- *   s = amax |z| / 448 (1 if z is zero),  xq = E4M3(z / s)
+ *   s = amax |z| / 448 (1 if that rounds to 0),  xq = E4M3(z / s)
  * All of it is in fp32, each result rounded once: the norm takes h' and the
  * quantizer z before their rounding to bf16.
  *
