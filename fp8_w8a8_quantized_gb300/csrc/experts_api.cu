@@ -176,7 +176,7 @@ fp8_status_t fp8_grouped_linear(const void* x_bf16, int64_t T, int64_t ldx,
     if ((st = fp8k::device_info(&a.num_sms, &a.status, &a.pair_clusters)) != FP8_OK) return st;
     const cudaError_t e = fp8k::launch_quant_gather(
         x_bf16, T, R, K, ldx, row_token, xq, s_tok, reinterpret_cast<uint32_t*>(rest),
-        fp8k::gemm_grouped_zero_words(), fp8k::gemm_grouped_ahead(R), as_stream(stream));
+        fp8k::gemm_grouped_zero_words(), as_stream(stream));
     return e != cudaSuccess ? FP8_ERR_CUDA
                             : said(fp8k::launch_gemm_grouped(a, as_stream(stream)));
 }

@@ -115,7 +115,6 @@ struct Args {
     int64_t slot;      // floats of a part: its rows x BN
     int E, R, N, K;
     Costs costs;
-    bool ahead;        // the bounds can be read before griddepcontrol.wait
     unsigned* status;
 };
 
@@ -245,36 +244,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncthreads();
     };
-    // With `ahead` the kernel before (the quantizer, or the one that clears the counters) lets this
-    // one start when all work before it is done, so that the bounds are there already: the list is
-    // made and the weights of the first stages are brought into L2 while it runs.  Behind the wait
-    // the bounds are read again, and the list made again if they are others.
-    bool made = false;
-    if (a.ahead) {
-        make_list();
-        if (warp == 0) {
-            Walk first(bars->first[a.E], workers, worker, nk, a.costs);
-            if (first.advance()) {
-                const Place p = Finder<B, C::BM>{bars, a.E}.at(first.tile);
-                const int n0 = p.n_blk * kOut;
-                const int w_first = p.e * a.N + n0, w_second = w_first + (kGated ? F : kHalf);
-                const int stages = min(first.kb1 - first.kb0, kPrefetched);
-                if (lane < 2 * stages && (kGated || n0 + (lane & 1) * kHalf < F) && (!kPair || (lane & 1) == rank))
-                    tma_prefetch_l2_2d(&maps.w, (first.kb0 + (lane >> 1)) * BK, lane & 1 ? w_second : w_first);
-            }
-            __syncwarp();
+    // The kernel before (the quantizer, or the one that clears the counters) lets this one start when
+    // all work before it is done, so that the bounds are there already: the list is made and the
+    // weights of the first stages are brought into L2 while it runs.  Behind the wait the bounds are
+    // read again, and the list made again if they are others.  (Against a start beside the work before
+    // that kernel, in a graph: 1 token on two of eight experts 44.0 -> 42.1 us, 16 tokens 121.7 -> 117.5,
+    // 32 tokens 139.3 -> 134.3, 253 tokens on 8 of 64 60.9 -> 60.3.)
+    make_list();
+    if (warp == 0) {
+        Walk first(bars->first[a.E], workers, worker, nk, a.costs);
+        if (first.advance()) {
+            const Place p = Finder<B, C::BM>{bars, a.E}.at(first.tile);
+            const int n0 = p.n_blk * kOut;
+            const int w_first = p.e * a.N + n0, w_second = w_first + (kGated ? F : kHalf);
+            const int stages = min(first.kb1 - first.kb0, kPrefetched);
+            if (lane < 2 * stages && (kGated || n0 + (lane & 1) * kHalf < F) && (!kPair || (lane & 1) == rank))
+                tma_prefetch_l2_2d(&maps.w, (first.kb0 + (lane >> 1)) * BK, lane & 1 ? w_second : w_first);
         }
-        pdl_wait_primary();
-        bool same = true;
-        for (int e = threadIdx.x; e < a.E; e += kThreads) {
-            const Bounds b = bounds_of(a, e);
-            same = same && b.begin == bars->begin[e] && b.end == bars->end[e];
-        }
-        made = __syncthreads_and(same);
-    } else {
-        pdl_wait_primary();
+        __syncwarp();
     }
-    if (!made) make_list();
+    pdl_wait_primary();
+    bool same = true;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        const Bounds b = bounds_of(a, e);
+        same = same && b.begin == bars->begin[e] && b.end == bars->end[e];
+    }
+    if (!__syncthreads_and(same)) make_list();
     Walk walk(bars->first[a.E], workers, worker, nk, a.costs);
     Finder<B, C::BM> find{bars, a.E};
 
@@ -729,10 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-__global__ void clear_counts(unsigned* count, int n, bool ahead) {
-    if (!ahead) pdl_launch_dependents();
+__global__ void clear_counts(unsigned* count, int n) {
     pdl_wait_primary();
-    if (ahead) pdl_launch_dependents();
+    pdl_launch_dependents();  // (behind the wait: the products read the bounds ahead of theirs)
     for (int i = threadIdx.x; i < n; i += blockDim.x) count[i] = 0;
 }
 
@@ -789,11 +783,6 @@ size_t gemm_grouped_workspace(int64_t E, int64_t R, int64_t N, int64_t K) {
 
 int64_t gemm_grouped_zero_words() { return kCounts; }
 
-// Few rows are quantized in less time than this kernel takes to start, which is then better
-// started beside the work before them (1 token of 8 experts 44.8 us, started ahead of its wait 45.9;
-// 32 tokens 146.1 and 144.7, 253 of 64 experts 66.5 and 64.9).
-bool gemm_grouped_ahead(int64_t R) { return R > 32; }
-
 cudaError_t prepare_gemm_grouped() {
     auto set = [](auto kernel, size_t bytes) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
@@ -815,7 +804,6 @@ cudaError_t launch_gemm_grouped(const GroupedArgs& g, cudaStream_t st) {
     a.slot = slot_floats(g.R);
     a.E = g.E, a.R = g.R, a.N = g.N, a.K = g.K;
     a.status = g.status;
-    a.ahead = gemm_grouped_ahead(g.R);
     if (!g.zeroed) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
@@ -826,7 +814,7 @@ cudaError_t launch_gemm_grouped(const GroupedArgs& g, cudaStream_t st) {
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, clear_counts, a.count, static_cast<int>(kCounts), a.ahead);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, clear_counts, a.count, static_cast<int>(kCounts));
         if (e != cudaSuccess) return e;
     }
     // Measured: an SM alone streams 75 GB/s of weights (a stage is 32 KB), all together 6.1 TB/s;

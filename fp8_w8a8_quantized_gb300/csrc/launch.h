@@ -203,11 +203,11 @@ size_t moe_route_workspace(int64_t T, int64_t E, int64_t k);
 
 // Rows of x gathered by row_token (null: row r is row r) and quantized
 // (quant.cu); a row without a token gets zeros with scale 1.  `zero` (optional)
-// is set to zeros, zero_words 32-bit words.  late: the next kernel may start only
-// when all work before this one is done.
+// is set to zeros, zero_words 32-bit words.  The next kernel may start only when
+// all work before this one is done.
 cudaError_t launch_quant_gather(const void* x, int64_t T, int64_t R, int64_t K, int64_t ldx,
                                 const int32_t* row_token, uint8_t* q, float* s, uint32_t* zero,
-                                int64_t zero_words, bool late, cudaStream_t st);
+                                int64_t zero_words, cudaStream_t st);
 
 // Products of each expert's rows with its weights (gemm_grouped.cu).
 struct GroupedArgs {
@@ -220,7 +220,9 @@ struct GroupedArgs {
     bool swiglu;
     void* y;
     void* workspace;
-    bool zeroed;        // the first gemm_grouped_zero_words() words of it are zero
+    bool zeroed;        // the kernel before this launch sets its first gemm_grouped_zero_words()
+                        // words to zero, and lets the next start only when all work before it is
+                        // done (the products read the bounds ahead of their wait)
     unsigned* status;
     int num_sms;
     int pair_clusters;  // co-resident clusters of the paired kernel (0: unknown)
@@ -228,9 +230,6 @@ struct GroupedArgs {
 cudaError_t launch_gemm_grouped(const GroupedArgs& a, cudaStream_t st);
 size_t gemm_grouped_workspace(int64_t E, int64_t R, int64_t N, int64_t K);
 int64_t gemm_grouped_zero_words();
-// Whether the kernel before a product of R rows lets it start only when all work
-// before that kernel is done, so that it may read the bounds ahead of its wait.
-bool gemm_grouped_ahead(int64_t R);
 
 // The end of a block and the start of the next (residual_norm.cu).
 struct ResidualNormArgs {

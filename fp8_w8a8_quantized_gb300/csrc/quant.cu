@@ -96,7 +96,6 @@ struct Gather {
     int64_t T;
     uint32_t* zero;
     int64_t zero_words;
-    bool late;
 };
 
 template <int G, int VPT, bool kGiven = false, bool kGather = false>
@@ -111,12 +110,11 @@ __global__ void __launch_bounds__(G > kBlock ? G : kBlock)
     // once (it reads nothing but L2 prefetches before its own wait, which
     // returns after this grid has completed); this one waits for its
     // predecessor before touching memory.
-    // (g.late: behind the wait, so that the next kernel finds at its start what the kernels before
+    // (kGather: behind the wait, so that the next kernel finds at its start what the kernels before
     // this one left)
-    const bool late = kGather && g.late;
-    if (!late) pdl_launch_dependents();
+    if constexpr (!kGather) pdl_launch_dependents();
     pdl_wait_primary();
-    if (late) pdl_launch_dependents();
+    if constexpr (kGather) pdl_launch_dependents();
 
     const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / G;
     const int t = threadIdx.x % G;
@@ -177,10 +175,9 @@ __global__ void __launch_bounds__(1024)
     quant_rows_stream(const uint16_t* __restrict__ x, int64_t R, int64_t K, int64_t ldx,
                       uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s, Gather g) {
     __shared__ float red[32];
-    const bool late = kGather && g.late;
-    if (!late) pdl_launch_dependents();
+    if constexpr (!kGather) pdl_launch_dependents();
     pdl_wait_primary();
-    if (late) pdl_launch_dependents();
+    if constexpr (kGather) pdl_launch_dependents();
     const int64_t row = blockIdx.x;
     const int64_t C = K >> 4;
     int64_t from = row;
@@ -322,9 +319,9 @@ cudaError_t launch_quant_rows(const void* x, int64_t R, int64_t K, int64_t ldx, 
 // Preconditions as above, and K > 0.
 cudaError_t launch_quant_gather(const void* x, int64_t T, int64_t R, int64_t K, int64_t ldx,
                                 const int32_t* row_token, uint8_t* q, float* s, uint32_t* zero,
-                                int64_t zero_words, bool late, cudaStream_t st) {
+                                int64_t zero_words, cudaStream_t st) {
     const uint16_t* xb = static_cast<const uint16_t*>(x);
-    const Gather g{row_token, T, zero, zero_words, late};
+    const Gather g{row_token, T, zero, zero_words};
     const cudaError_t e = dispatch_regs<false, true>(xb, R, K, ldx, q, K, s, nullptr, st, g);
     if (e != cudaErrorNotSupported) return e;
     return launch_pdl(quant_rows_stream<true>, R, 1024, st, xb, R, K, ldx, q, K, s, g);
