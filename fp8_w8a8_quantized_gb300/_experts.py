@@ -30,8 +30,8 @@ def fp8_moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, sc
                   offsets: torch.Tensor | None = None, row_token: torch.Tensor | None = None,
                   token_row: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                   stream=None):
-    """Each token's top_k experts of logits [T, E] (fp32 or bf16; -inf or NaN
-    switches an expert off) and the rows that they make, sorted by expert.
+    """Each token's top_k experts by the softmax of logits [T, E] (fp32 or bf16; -inf or
+    NaN switches an expert off) and the rows that they make, sorted by expert.
     Returns (expert_ids int32 [T, top_k], weights fp32 [T, top_k], offsets int32
     [E + 1], row_token int32 [T * top_k], token_row int32 [T, top_k]); where none
     of them is given, all share one allocation."""

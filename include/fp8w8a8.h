@@ -539,6 +539,8 @@ FP8_API size_t fp8_attention_decode_workspace_size(int64_t B, int64_t Hq, int64_
  *   the pairs (t, j) sorted by expert, by token within one, are the rows:
  *   row_token[r] = t of row r,  token_row[t, j] = r,
  *   offsets[e] = rows of the experts below e.
+ * The scores are this softmax alone: a choice by sigmoids, by a bias that selects
+ * without weighing, or within groups of experts is not offered.
  * A logit of -infinity or NaN switches its expert off for the token (one of
  * +infinity gives NaN weights, as the formula does).  Where
  * fewer than top_k are left, the rest has expert -1, weight 0 and row -1 (a
@@ -590,6 +592,9 @@ FP8_API size_t fp8_moe_route_workspace_size(int64_t T, int64_t E, int64_t top_k)
  * Requirements: K % 16 == 0, K > 0; with swiglu N % 2 == 0; 1 <= E <= 1024;
  * xq, wq and y 16-byte aligned; R, K, E * N <= 2^30.  The order of each sum is
  * fixed by the sizes and offsets: repeated calls give identical bits.
+ * Speed: the form of the product is chosen by R / E, as offsets is known on the GPU
+ * alone.  Rows that no expert has cost the product nothing themselves, but with R far
+ * above the rows in use the form is the one for many rows.
  */
 FP8_API fp8_status_t fp8_grouped_gemm(const uint8_t* xq, const float* s_tok, const uint8_t* wq,
                                       const float* s_w, const int32_t* offsets, int64_t E,
@@ -612,7 +617,7 @@ FP8_API size_t fp8_grouped_gemm_workspace_size(int64_t E, int64_t R, int64_t N, 
  *                           aligned; need not start at zero; not in use by
  *                           another call in flight
  * Requirements: as for fp8_grouped_gemm; x_bf16 16-byte aligned, ldx >= K and
- * ldx % 8 == 0.
+ * ldx % 8 == 0.  All R rows are quantized, those outside the offsets too.
  */
 FP8_API fp8_status_t fp8_grouped_linear(const void* x_bf16, int64_t T, int64_t ldx,
                                         const int32_t* row_token, const uint8_t* wq,
