@@ -35,10 +35,11 @@
 //
 // Measured: 8 x 8 rows of 4096 x 28672 136 us, 6.9 TB/s of weights (102% of a
 // copy); 64 x 32 rows of 2048 x 2816 59 us, 6.4 TB/s; 4096 tokens on two of eight
-// experts 571 us, 3.4 PFLOP/s with the tensor cores 89% busy at the 1.6 GHz that the
+// experts 585 us, 3.3 PFLOP/s with the tensor cores 89% busy at the 1.6 GHz that the
 // card's power leaves.  40 experts of 0 to 2866 rows, 1408 x 2048: 57 us where bytes
-// take 31: 29% of the tiles' rows are empty, and between tiles of only 11 stages 1.3
-// of 4.9 us go to the outputs' way to memory and the accumulators' hand-over.
+// take 31: between tiles of only 11 stages 1.3 of 4.9 us go to the outputs' way to
+// memory and the accumulators' hand-over, and 13% of the tiles' rows are empty (25%
+// where a tile of 128 rows counts as one of 256).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -16,9 +16,10 @@
 // Up to some hundred tokens it is one launch of one cluster, whose CTAs read one
 // another's counts through distributed shared memory; beyond, two launches with
 // the counts in the workspace (choose, place).  Small calls are bound by latency
-// (launch, logits, k rounds, numbering): 32 tokens of 64 experts, top 8, 5.0 us, 256
-// tokens 6.2.  8192 tokens of 256 experts take 14.4 us where their bytes take 1.4: two
-// launches and their dependent reads 7, two tokens a warp 5.5, the numbering 2.
+// (launch, logits, k rounds, numbering): 32 tokens of 64 experts, top 8, 5.1 us, of 128
+// 5.5, 256 tokens of 128 6.7.  8192 tokens of 256 experts take 13.9 us (of 128 16.8) where
+// their bytes take 1.4: two launches and their dependent reads 7, two tokens a warp 5, the
+// numbering 2.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
