@@ -639,7 +639,9 @@ FP8_API size_t fp8_grouped_linear_workspace_size(int64_t E, int64_t R, int64_t N
  *   z = h' / sqrt(mean h'^2 + eps) * gamma;      z_out = bf16_rn(z)
  *   s = amax |z| / 448 (1 if that rounds to 0),  xq = E4M3(z / s)
  * All of it is in fp32, each result rounded once: the norm takes h' and the
- * quantizer z before their rounding to bf16.
+ * quantizer z before their rounding to bf16.  A row whose sum of squares leaves
+ * fp32 (values from 2^64 / sqrt(K) on) is normed to zeros; with eps == 0 a row
+ * whose squares all round to 0 is divided by 0 (zeros give NaN).
  *
  *   h      [device, in]   bf16 [T, K], ldh: the residual stream
  *   y      [device, in]   bf16 [R, K], ldy (top_k == 0: R == T)

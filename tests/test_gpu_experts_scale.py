@@ -31,3 +31,34 @@ def test_rows_whose_scale_rounds_to_zero(K):
     assert not torch.isnan(value).any()
     assert (off <= 0).all(), off.max()
     assert (value[:, :5] == 0).all() and (value[:, 6:] == 0).all()
+
+
+def test_rows_whose_squares_leave_fp32():
+    # as the header says: normed to zeros, the stream itself kept; the rows beside them as ever
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    h = torch.randn(5, 256, generator=g, device=DEV).to(torch.bfloat16)
+    y, one = torch.zeros_like(h), torch.ones(256, dtype=torch.bfloat16, device=DEV)
+    plain = fp8.fp8_residual_norm_quant(h, y, one)
+    big = h.clone()
+    big[[1, 3], 7] = 2.0 ** 70
+    out, z, xq, s = fp8.fp8_residual_norm_quant(big, y, one)
+    torch.cuda.synchronize()
+    assert torch.equal(out, big)
+    for got, want in zip((z, xq, s), plain[1:]):
+        assert torch.equal(got[[0, 2, 4]], want[[0, 2, 4]])
+    assert (z[[1, 3]] == 0).all() and (s[[1, 3]] == 1).all()
+    assert (xq[[1, 3]].view(torch.float8_e4m3fn).float() == 0).all()
+    # (the branch's own norm: nothing is left of it, and the stream stays)
+    out = fp8.fp8_residual_norm_quant(h, big, one, gamma_post=one)[0]
+    assert torch.equal(out[[1, 3]], h[[1, 3]])
+
+
+def test_rows_of_zeros_without_eps_are_divided_by_zero():
+    h = torch.zeros(3, 64, dtype=torch.bfloat16, device=DEV)
+    h[1] = 2.0
+    one = torch.ones(64, dtype=torch.bfloat16, device=DEV)
+    out, z, xq, s = fp8.fp8_residual_norm_quant(h, torch.zeros_like(h), one, eps=0.0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, h) and torch.isnan(z[[0, 2]].float()).all() and (z[1] == 1).all()
+    assert torch.isnan(xq[[0, 2]].view(torch.float8_e4m3fn).float()).all()
